@@ -22,6 +22,7 @@ MOE_SINGLE_CTA_TILES = 0x8
 MOE_SHARED_SERIAL = 0x10
 MOE_FP8_DISPATCH = 0x20
 MOE_FP8_MX = 0x40
+MOE_ACCUMULATE = 0x80
 STATUS = {0: "MOE_OK", 1: "MOE_ERR_INVALID_ARG", 2: "MOE_ERR_UNSUPPORTED", 3: "MOE_ERR_WORKSPACE",
           4: "MOE_ERR_BAD_ROUTING", 5: "MOE_ERR_TIMEOUT", 6: "MOE_ERR_CUDA"}
 
@@ -31,7 +32,12 @@ SYMBOLS = ("moe_status_string", "moe_version", "moe_last_cuda_error", "moe_trace
            "moe_route", "moe_dispatch", "moe_dispatch_noalloc", "moe_dispatch_fp8",
            "moe_dequant_fp8", "moe_quantize_mx", "moe_dispatch_mx", "moe_grouped_ffn_mx",
            "moe_prepack_weights", "moe_grouped_ffn", "moe_grouped_ffn_fp8",
-           "moe_combine", "moe_layer_fwd", "moe_layer_bwd")
+           "moe_combine", "moe_layer_fwd", "moe_layer_bwd",
+           "moe_sort_rows_bound", "moe_sort", "moe_permute", "moe_permute_bwd", "moe_unpermute",
+           "moe_unpermute_bwd", "moe_embed", "moe_embed_bwd", "moe_grad_norm", "moe_adamw_step")
+
+# moe_dtype_t
+DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
 
 # moe_stage_t
 STAGES = ("gate", "topk", "dispatch", "gateup", "down", "combine", "bwd_route", "bwd_dh", "bwd_dx",
@@ -71,6 +77,18 @@ class moe_layer_t(ctypes.Structure):
 class moe_saved_t(ctypes.Structure):
     _fields_ = [(n, _vp) for n in ("logits", "topk_idx", "topk_w", "counts", "offsets", "row_slot",
                                    "slot_row", "x_perm", "a", "b", "h", "o", "sa", "sb", "sh")]
+
+
+class moe_adamw_tensor_t(ctypes.Structure):
+    _fields_ = [("p", _vp), ("master", _vp), ("g", _vp), ("m", _vp), ("v", _vp),
+                ("m_scale", _vp), ("v_scale", _vp), ("n", ctypes.c_longlong),
+                ("weight_decay", ctypes.c_double), ("p_dtype", _i), ("g_dtype", _i),
+                ("state_bits", _i)]
+
+
+class moe_adamw_t(ctypes.Structure):
+    _fields_ = [("lr", ctypes.c_double), ("beta1", ctypes.c_double), ("beta2", ctypes.c_double),
+                ("eps", ctypes.c_double), ("step", ctypes.c_longlong), ("seed", ctypes.c_uint32)]
 
 
 def _declare(lib):
@@ -122,6 +140,31 @@ def _declare(lib):
     lib.moe_layer_bwd.restype = _i
     lib.moe_layer_bwd.argtypes = [ctypes.POINTER(moe_layer_t), _vp, ctypes.POINTER(moe_saved_t),
                                   _vp, _vp, _vp, _vp, _vp, _vp, _vp, _szp, _u, _vp]
+    lib.moe_sort_rows_bound.restype = _ll
+    lib.moe_sort_rows_bound.argtypes = [_i, _i, _i, _i, _i]
+    lib.moe_sort.restype = _i
+    lib.moe_sort.argtypes = [_vp, _i, _i, _i, _i, _i, _i, _vp, _vp, _vp, _vp, _vp, _szp, _u, _vp]
+    lib.moe_permute.restype = _i
+    lib.moe_permute.argtypes = [_vp, _ll, _vp, _vp, _vp, _i, _i, _i, _i, _i, _vp, _ll, _vp]
+    lib.moe_permute_bwd.restype = _i
+    lib.moe_permute_bwd.argtypes = [_vp, _ll, _vp, _vp, _vp, _ll, _i, _i, _i, _i, _i, _vp, _ll,
+                                    _vp, _vp]
+    lib.moe_unpermute.restype = _i
+    lib.moe_unpermute.argtypes = [_vp, _ll, _vp, _vp, _i, _i, _i, _i, _i, _vp, _ll, _vp]
+    lib.moe_unpermute_bwd.restype = _i
+    lib.moe_unpermute_bwd.argtypes = [_vp, _ll, _vp, _vp, _vp, _vp, _ll, _i, _i, _i, _i, _i, _vp,
+                                      _ll, _vp, _vp]
+    _f = ctypes.c_float
+    lib.moe_embed.restype = _i
+    lib.moe_embed.argtypes = [_vp, _i, _ll, _vp, _ll, _i, _i, _i, _f, _vp, _ll, _i, _vp]
+    lib.moe_embed_bwd.restype = _i
+    lib.moe_embed_bwd.argtypes = [_vp, _ll, _vp, _i, _ll, _i, _i, _i, _f, _vp, _ll, _i, _vp, _szp,
+                                  _u, _vp]
+    _list = ctypes.POINTER(moe_adamw_tensor_t)
+    lib.moe_grad_norm.restype = _i
+    lib.moe_grad_norm.argtypes = [_list, _i, ctypes.c_double, _vp, _vp, _szp, _vp]
+    lib.moe_adamw_step.restype = _i
+    lib.moe_adamw_step.argtypes = [_list, _i, ctypes.POINTER(moe_adamw_t), _vp, _vp]
 
 
 _LIB = None
@@ -376,6 +419,223 @@ def moe_combine(expert_out, slot_row, topk_w, y, R, stream=None):
     st = lib().moe_combine(_p(expert_out), _p(slot_row), _p(topk_w), T, d, R, _p(y),
                            _stream(stream))
     _check(st, "moe_combine")
+
+
+# ---------------------------------------------------------------- around the layer
+def _rows(t, name, dtype=None):
+    """(pointer, row stride) of a matrix whose rows are contiguous."""
+    if t is None:
+        return None, 0
+    if not t.is_cuda:
+        raise ValueError(f"{name} must live on a CUDA device")
+    if t.dim() != 2 or (t.stride(1) != 1 and t.shape[1] > 1):
+        raise ValueError(f"{name} must be a matrix with contiguous rows")
+    if t.dtype not in DTYPES or (dtype is not None and t.dtype != dtype):
+        raise TypeError(f"{name} must be {dtype or 'bf16, fp16 or fp32'}, got {t.dtype}")
+    return t.data_ptr(), t.stride(0) if t.shape[0] > 1 else t.shape[1]
+
+
+def _shape(t, shape, name):
+    if t is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+
+
+def sort_rows_bound(T, R, E, align=1, capacity=0) -> int:
+    """Rows that hold every plan of moe_sort for these arguments."""
+    n = int(lib().moe_sort_rows_bound(T, R, E, align, capacity))
+    if n < 0:
+        raise MoeError(2, "moe_sort_rows_bound")
+    return n
+
+
+def sort_ws_bytes(T, E, R) -> int:
+    n = ctypes.c_size_t(0)
+    _check(lib().moe_sort(None, T, E, R, 1, 0, 0, None, None, None, None, None, ctypes.byref(n), 0,
+                          None), "moe_sort(ws query)")
+    return n.value
+
+
+def moe_sort(topk_idx, E, counts, offsets, row_slot, slot_row, ws, align=1, capacity=0, flags=0,
+             stream=None):
+    """Plan of an expert sort (see include/moe.h); row_slot has at least
+    sort_rows_bound(T, R, E, align, capacity) entries."""
+    T, R = topk_idx.shape
+    for name, t in (("topk_idx", topk_idx), ("counts", counts), ("offsets", offsets),
+                    ("row_slot", row_slot), ("slot_row", slot_row)):
+        _dt(t, torch.int32, name)
+    _shape(counts, (E,), "counts"); _shape(offsets, (E + 1,), "offsets")
+    if slot_row.numel() != T * R:
+        raise ValueError(f"slot_row must have {T * R} entries")
+    n = ctypes.c_size_t(ws.numel())
+    st = lib().moe_sort(_p(topk_idx), T, E, R, align, capacity, row_slot.numel(), _p(counts),
+                        _p(offsets), _p(row_slot), _p(slot_row), _p(ws), ctypes.byref(n), flags,
+                        _stream(stream))
+    _check(st, "moe_sort")
+
+
+def _plan_args(T, N, w, slot_row, row_slot=None):
+    _dt(slot_row, torch.int32, "slot_row"); _dt(row_slot, torch.int32, "row_slot")
+    _dt(w, torch.float32, "w")
+    if slot_row.dim() != 2 or slot_row.shape[0] != T:
+        raise ValueError(f"slot_row must have shape ({T}, R)")
+    _shape(w, slot_row.shape, "w")
+    _shape(row_slot, (N,), "row_slot")
+    return slot_row.shape[1]
+
+
+def moe_permute(x, w, row_slot, slot_row, rows, stream=None):
+    """rows[slot_row[t, r]] = w[t, r] * x[t] (w None: a copy); rows without a slot are zero."""
+    (px, ldx), (pr, ldr) = _rows(x, "x"), _rows(rows, "rows", x.dtype)
+    T, d = x.shape
+    N = rows.shape[0]
+    _shape(rows, (N, d), "rows")
+    R = _plan_args(T, N, w, slot_row, row_slot)
+    st = lib().moe_permute(px, ldx, _p(w), _p(row_slot), _p(slot_row), T, d, R, N,
+                           DTYPES[x.dtype], pr, ldr, _stream(stream))
+    _check(st, "moe_permute")
+
+
+def moe_permute_bwd(drows, slot_row, w, x, dx, dw, stream=None):
+    """dx[t] = sum_r w[t, r] drows[slot_row[t, r]], dw[t, r] = <x[t], drows[slot_row[t, r]]>
+    (x and dw None: no weight gradient)."""
+    (pr, ldr), (pd, ldd) = _rows(drows, "drows"), _rows(dx, "dx", drows.dtype)
+    px, ldx = _rows(x, "x", drows.dtype)
+    N, d = drows.shape
+    T = dx.shape[0]
+    _shape(dx, (T, d), "dx"); _shape(x, (T, d), "x")
+    R = _plan_args(T, N, w, slot_row)
+    _dt(dw, torch.float32, "dw"); _shape(dw, (T, R), "dw")
+    st = lib().moe_permute_bwd(pr, ldr, _p(slot_row), _p(w), px, ldx, T, d, R, N,
+                               DTYPES[drows.dtype], pd, ldd, _p(dw), _stream(stream))
+    _check(st, "moe_permute_bwd")
+
+
+def moe_unpermute(rows, slot_row, w, y, stream=None):
+    """y[t] = sum_r w[t, r] rows[slot_row[t, r]] (w None: weight 1)."""
+    (pr, ldr), (py, ldy) = _rows(rows, "rows"), _rows(y, "y", rows.dtype)
+    N, d = rows.shape
+    T = y.shape[0]
+    _shape(y, (T, d), "y")
+    R = _plan_args(T, N, w, slot_row)
+    st = lib().moe_unpermute(pr, ldr, _p(slot_row), _p(w), T, d, R, N, DTYPES[rows.dtype], py, ldy,
+                             _stream(stream))
+    _check(st, "moe_unpermute")
+
+
+def moe_unpermute_bwd(dy, row_slot, slot_row, w, rows, drows, dw, stream=None):
+    """drows[slot_row[t, r]] = w[t, r] dy[t] (zero without a slot), dw[t, r] =
+    <dy[t], rows[slot_row[t, r]]> (rows and dw None: no weight gradient)."""
+    (py, ldy), (pd, ldd) = _rows(dy, "dy"), _rows(drows, "drows", dy.dtype)
+    pr, ldr = _rows(rows, "rows", dy.dtype)
+    T, d = dy.shape
+    N = drows.shape[0]
+    _shape(drows, (N, d), "drows"); _shape(rows, (N, d), "rows")
+    R = _plan_args(T, N, w, slot_row, row_slot)
+    _dt(dw, torch.float32, "dw"); _shape(dw, (T, R), "dw")
+    st = lib().moe_unpermute_bwd(py, ldy, _p(row_slot), _p(slot_row), _p(w), pr, ldr, T, d, R, N,
+                                 DTYPES[dy.dtype], pd, ldd, _p(dw), _stream(stream))
+    _check(st, "moe_unpermute_bwd")
+
+
+def _ids(ids):
+    if ids.dtype not in (torch.int32, torch.int64):
+        raise TypeError(f"ids must be int32 or int64, got {ids.dtype}")
+    return _p(ids), ids.element_size(), ids.numel()
+
+
+def moe_embed(ids, table, out, scale=1.0, stream=None):
+    """out[i] = scale * table[ids[i]]; zeros where ids[i] is outside the table."""
+    (pi, ib, n), (pt, ldt), (po, ldo) = _ids(ids), _rows(table, "table"), _rows(out, "out")
+    V, d = table.shape
+    _shape(out, (n, d), "out")
+    st = lib().moe_embed(pi, ib, n, pt, ldt, V, d, DTYPES[table.dtype], scale, po, ldo,
+                         DTYPES[out.dtype], _stream(stream))
+    _check(st, "moe_embed")
+
+
+def embed_bwd_ws_bytes(n, V, d) -> int:
+    b = ctypes.c_size_t(0)
+    _check(lib().moe_embed_bwd(None, d, None, 4, n, V, d, 0, 1.0, None, d, 0, None,
+                               ctypes.byref(b), 0, None), "moe_embed_bwd(ws query)")
+    return b.value
+
+
+def moe_embed_bwd(dout, ids, dtable, ws, scale=1.0, accumulate=False, flags=0, stream=None):
+    """dtable[v] (+)= scale * sum of the rows of dout whose id is v; negative ids contribute
+    nothing."""
+    (pi, ib, n), (pd, ldd), (pt, ldt) = _ids(ids), _rows(dout, "dout"), _rows(dtable, "dtable")
+    V, d = dtable.shape
+    _shape(dout, (n, d), "dout")
+    b = ctypes.c_size_t(ws.numel())
+    st = lib().moe_embed_bwd(pd, ldd, pi, ib, n, V, d, DTYPES[dout.dtype], scale, pt, ldt,
+                             DTYPES[dtable.dtype], _p(ws), ctypes.byref(b),
+                             flags | (MOE_ACCUMULATE if accumulate else 0), _stream(stream))
+    _check(st, "moe_embed_bwd")
+
+
+class AdamWTensor:
+    """One tensor of an optimiser step (moe_adamw_tensor_t).  fp32 m and v: 32-bit states;
+    uint8 or float8_e4m3fn m and v with fp32 scales, one per 256 elements: 8-bit states.
+    Zeros are the state before the first step."""
+
+    def __init__(self, p, g, m, v, master=None, m_scale=None, v_scale=None, weight_decay=0.0):
+        n = p.numel()
+        for name, t in (("g", g), ("m", m), ("v", v), ("master", master)):
+            if t is not None and t.numel() != n:
+                raise ValueError(f"{name} must have {n} elements, got {t.numel()}")
+        for name, t in (("p", p), ("g", g)):
+            if t.dtype not in (torch.bfloat16, torch.float32):
+                raise TypeError(f"{name} must be bf16 or fp32, got {t.dtype}")
+        _dt(master, torch.float32, "master")
+        codes = (torch.uint8, torch.float8_e4m3fn)
+        if m.dtype != v.dtype or (m.dtype != torch.float32 and m.dtype not in codes):
+            raise TypeError(f"m and v must both be fp32 or both 8-bit codes, got {m.dtype}, {v.dtype}")
+        bits = 8 if m.dtype in codes else 32
+        for name, t in (("m_scale", m_scale), ("v_scale", v_scale)):
+            if (t is None) != (bits == 32):
+                raise ValueError(f"{name} goes with 8-bit states only")
+            if t is not None and (t.dtype != torch.float32 or t.numel() != -(-n // 256)):
+                raise ValueError(f"{name} must be fp32 with {-(-n // 256)} elements")
+        self.tensors = (p, master, g, m, v, m_scale, v_scale)
+        self.c = moe_adamw_tensor_t(_p(p), _p(master), _p(g), _p(m), _p(v), _p(m_scale),
+                                    _p(v_scale), n, weight_decay, DTYPES[p.dtype],
+                                    DTYPES[g.dtype], bits)
+
+
+class AdamWList:
+    """The tensors of an optimiser step: a host array, kept between steps."""
+
+    def __init__(self, tensors):
+        self.tensors = list(tensors)
+        self.c = (moe_adamw_tensor_t * max(1, len(self.tensors)))(*[t.c for t in self.tensors])
+
+    def __len__(self):
+        return len(self.tensors)
+
+
+def grad_norm_ws_bytes(tensors: AdamWList) -> int:
+    n = ctypes.c_size_t(0)
+    _check(lib().moe_grad_norm(tensors.c, len(tensors), 0.0, None, None, ctypes.byref(n), None),
+           "moe_grad_norm(ws query)")
+    return n.value
+
+
+def moe_grad_norm(tensors: AdamWList, max_norm, norm, ws, stream=None):
+    """norm (fp32 [4]) = L2 norm over all gradients, clip factor, 1 if finite, 0."""
+    _dt(norm, torch.float32, "norm"); _shape(norm, (4,), "norm")
+    n = ctypes.c_size_t(ws.numel())
+    st = lib().moe_grad_norm(tensors.c, len(tensors), max_norm, _p(norm), _p(ws), ctypes.byref(n),
+                             _stream(stream))
+    _check(st, "moe_grad_norm")
+
+
+def moe_adamw_step(tensors: AdamWList, lr, beta1=0.9, beta2=0.999, eps=1e-8, step=1, seed=0,
+                   norm=None, stream=None):
+    """One AdamW step in place; norm: the record of moe_grad_norm (clip, skip if not finite)."""
+    _dt(norm, torch.float32, "norm"); _shape(norm, (4,), "norm")
+    h = moe_adamw_t(lr, beta1, beta2, eps, step, seed)
+    st = lib().moe_adamw_step(tensors.c, len(tensors), ctypes.byref(h), _p(norm), _stream(stream))
+    _check(st, "moe_adamw_step")
 
 
 # ---------------------------------------------------------------- layer

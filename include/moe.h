@@ -465,6 +465,183 @@ moe_status_t moe_layer_bwd(const moe_layer_t* layer, const uint16_t* x, const mo
                            float* dW3, float* dW2, void* ws, size_t* ws_bytes, unsigned flags,
                            moe_stream_t stream);
 
+/* ------------------------------------------------------------------------
+ * Around the layer in a training step: rows sorted for experts of the
+ * caller's own and brought back, with their gradients; the embedding that
+ * makes x out of token ids, with its gradient; the optimiser step on the
+ * gradients that moe_layer_bwd writes.  (The page has no counterpart of the
+ * last two.)  These calls take bf16, fp16 and fp32 data, any row length, rows
+ * apart by any stride (in elements, at least the row length) and pointers
+ * aligned to their element; 16-byte aligned rows of a multiple of 16 bytes
+ * move fastest.  Outputs must not overlap inputs.
+ */
+typedef enum {
+  MOE_BF16 = 0,
+  MOE_F16 = 1,
+  MOE_F32 = 2
+} moe_dtype_t;
+
+#define MOE_ACCUMULATE 0x80u        /* moe_embed_bwd: add to dtable instead of overwriting it */
+
+/*
+ * moe_sort_rows_bound -- the number of rows that holds every plan of moe_sort
+ * for these arguments, whatever the routing:
+ *   min( floor_to_align(T*R + min(E, T*R) * (align - 1)), E * ceil_to_align(capacity) )
+ * (the second term only with capacity > 0).  -1 for arguments moe_sort refuses.
+ */
+long long moe_sort_rows_bound(int T, int R, int E, int align, int capacity);
+
+/*
+ * moe_sort -- the plan that groups slots by expert, for experts that moe_dispatch
+ * does not serve: slots may be empty, an expert may take a limited number of
+ * rows, and each expert's rows may start at a multiple of a tile.
+ *   topk_idx[t,r] = -1: the slot is empty (e.g. its expert lives elsewhere)
+ *   counts[e]  = min(#{slots s : topk_idx[s] == e}, capacity)   (capacity <= 0: no limit)
+ *   offsets[e] = sum_{e' < e} counts[e'] rounded up to a multiple of align; offsets[E] = the end
+ *   rows offsets[e] .. offsets[e] + counts[e] - 1 are expert e's first counts[e]
+ *   slots, in ascending slot order
+ *   row_slot[row] = s, or -1 for a row without a slot;  slot_row[s] = row, or -1
+ * topk_idx, slot_row: int32 [T,R]; counts int32 [E]; offsets int32 [E+1]; row_slot
+ * int32 [N] with N at least moe_sort_rows_bound(...) (all N entries are written).
+ * An expert may appear twice in a token.  Entries outside [-1, E) count as
+ * empty and are reported (MOE_ERR_BAD_ROUTING with MOE_CHECK).  1 <= align <= 4096;
+ * T*R and N below 2^31.  Needs a workspace (error word).  Deterministic.
+ */
+moe_status_t moe_sort(const int32_t* topk_idx, int T, int E, int R, int align, int capacity, int N,
+                      int32_t* counts, int32_t* offsets, int32_t* row_slot, int32_t* slot_row,
+                      void* ws, size_t* ws_bytes, unsigned flags, moe_stream_t stream);
+
+/*
+ * moe_permute -- tokens to their rows, optionally times their weights:
+ *   rows[slot_row[t,r]] = w[t,r] * x[t]   (fp32 product, one rounding; w NULL: a copy)
+ *   rows[i] = 0 where row_slot[i] < 0
+ * x: [T,d], rows: [N,d] of type dtype, row strides ldx, ld_rows; w fp32 [T,R] or
+ * NULL; row_slot [N] and slot_row [T,R] from moe_sort.  No workspace.
+ */
+moe_status_t moe_permute(const void* x, long long ldx, const float* w, const int32_t* row_slot,
+                         const int32_t* slot_row, int T, int d, int R, int N, int dtype,
+                         void* rows, long long ld_rows, moe_stream_t stream);
+
+/*
+ * moe_permute_bwd -- gradient of moe_permute, given drows = dL/drows:
+ *   dx[t]   = sum_r w[t,r] * drows[slot_row[t,r]]      (fp32 sum in r order, one rounding)
+ *   dw[t,r] = <x[t], drows[slot_row[t,r]]>             (fp32; dw and x both NULL: not computed)
+ * Slots without a row contribute nothing and get dw = 0; rows without a slot are
+ * not read.
+ */
+moe_status_t moe_permute_bwd(const void* drows, long long ld_drows, const int32_t* slot_row,
+                             const float* w, const void* x, long long ldx, int T, int d, int R,
+                             int N, int dtype, void* dx, long long ld_dx, float* dw,
+                             moe_stream_t stream);
+
+/*
+ * moe_unpermute -- rows back to their tokens, summed with their weights:
+ *   y[t] = sum_r w[t,r] * rows[slot_row[t,r]]     (fp32 sum in r order, one rounding)
+ * w NULL: weight 1.  A token without rows gets zeros.
+ */
+moe_status_t moe_unpermute(const void* rows, long long ld_rows, const int32_t* slot_row,
+                           const float* w, int T, int d, int R, int N, int dtype, void* y,
+                           long long ldy, moe_stream_t stream);
+
+/*
+ * moe_unpermute_bwd -- gradient of moe_unpermute, given dy = dL/dy:
+ *   drows[slot_row[t,r]] = w[t,r] * dy[t],  drows[i] = 0 where row_slot[i] < 0
+ *   dw[t,r] = <dy[t], rows[slot_row[t,r]]>  (fp32; dw and rows both NULL: not computed)
+ */
+moe_status_t moe_unpermute_bwd(const void* dy, long long ld_dy, const int32_t* row_slot,
+                               const int32_t* slot_row, const float* w, const void* rows,
+                               long long ld_rows, int T, int d, int R, int N, int dtype,
+                               void* drows, long long ld_drows, float* dw, moe_stream_t stream);
+
+/*
+ * moe_embed -- out[i] = scale * table[ids[i]], zeros where ids[i] is outside
+ * [0, V) (a position without a token).  ids: int32 or int64 (ids_bytes 4 or 8)
+ * [n]; table [V,d] of table_dtype, out [n,d] of out_dtype, row strides ld_table,
+ * ld_out.  n < 2^31.  No workspace.
+ */
+moe_status_t moe_embed(const void* ids, int ids_bytes, long long n, const void* table,
+                       long long ld_table, int V, int d, int table_dtype, float scale, void* out,
+                       long long ld_out, int out_dtype, moe_stream_t stream);
+
+/*
+ * moe_embed_bwd -- gradient of moe_embed with respect to the table:
+ *   dtable[v] = scale * sum_{i : ids[i] == v} dout[i]
+ * (fp32 sums in an order fixed by the ids, one rounding).  Every row is written;
+ * with MOE_ACCUMULATE the sum is added to dtable and rows without a token are
+ * left alone.  Ids below 0 contribute nothing; ids >= V neither, and are
+ * reported (MOE_ERR_BAD_ROUTING with MOE_CHECK).  dout [n,d] of dout_dtype;
+ * dtable [V,d] of dtable_dtype.  n < 2^30, V <= 2^30.  Needs a workspace (error
+ * word, sorted ids, partial sums).
+ */
+moe_status_t moe_embed_bwd(const void* dout, long long ld_dout, const void* ids, int ids_bytes,
+                           long long n, int V, int d, int dout_dtype, float scale, void* dtable,
+                           long long ld_dtable, int dtable_dtype, void* ws, size_t* ws_bytes,
+                           unsigned flags, moe_stream_t stream);
+
+/*
+ * One tensor of an optimiser step: n elements, contiguous.  p_dtype MOE_BF16 or
+ * MOE_F32; g_dtype MOE_BF16 or MOE_F32.  master: fp32 [n] copy that the step
+ * updates in p's place (p then gets its rounding), or NULL; only with a bf16 p.
+ * state_bits 32: m, v fp32 [n], scales NULL.  state_bits 8: E4M3 codes uint8 [n]
+ * with one fp32 scale per 256 consecutive elements (m_scale, v_scale:
+ * fp32 [ceil(n/256)]), m = code * m_scale and sqrt(v) = code * v_scale.  All
+ * zeros is the state before the first step.
+ */
+typedef struct {
+  void* p;
+  float* master;
+  const void* g;
+  void* m;
+  void* v;
+  float* m_scale;
+  float* v_scale;
+  long long n;
+  double weight_decay;
+  int p_dtype;
+  int g_dtype;
+  int state_bits;
+} moe_adamw_tensor_t;
+
+/* Settings of a step; step counts from 1.  seed: dither of the 8-bit states,
+ * another one each step (e.g. the step's number). */
+typedef struct {
+  double lr, beta1, beta2, eps;
+  long long step;
+  uint32_t seed;
+} moe_adamw_t;
+
+/*
+ * moe_grad_norm -- the L2 norm over all gradients of a list and the factor that
+ * clips it, left on the device for moe_adamw_step:
+ *   norm[0] = sqrt(sum g^2),  norm[1] = min(1, max_norm / (norm[0] + 1e-6))
+ *   (1 when max_norm <= 0),   norm[2] = 1 if norm[0] is finite, else 0,  norm[3] = 0
+ * tensors: host array of n_tensors (only g, g_dtype and n are used; read before
+ * the call returns).  norm: fp32 [4] on the device.  Squares are summed in fp32
+ * over eight elements and in fp64 from there, in a fixed order (a gradient above
+ * 1.8e19 in magnitude counts as not finite).  Needs a workspace.
+ */
+moe_status_t moe_grad_norm(const moe_adamw_tensor_t* tensors, int n_tensors, double max_norm,
+                           float* norm, void* ws, size_t* ws_bytes, moe_stream_t stream);
+
+/*
+ * moe_adamw_step -- one AdamW step on every tensor of a list, in place:
+ *   g' = norm[1] * g  (norm NULL: g)
+ *   m = beta1 m + (1 - beta1) g',   v = beta2 v + (1 - beta2) g'^2
+ *   p = p (1 - lr * weight_decay) - lr / (1 - beta1^step) * m /
+ *       (sqrt(v) / sqrt(1 - beta2^step) + eps)
+ * in fp32, p rounded once to its type.  With norm and norm[2] == 0 nothing is
+ * changed.  8-bit states are rounded after the update has used them: per block,
+ * scale = max / 448 and code = |value| / scale rounded to one of its two E4M3
+ * neighbours by adding 20 dither bits below the kept mantissa bits; sqrt(v) > 0
+ * never rounds to 0.  Element i of the k-th tensor takes the dither
+ *   h = mix(floor(i/2) * 0x9E3779B1 + mix(seed + k * 0x9E3779B1))   (mod 2^32)
+ *   mix(x): x = (x ^ x>>16) * 0x6A09E667; x = (x ^ x>>15) * 0xBB67AE85; x ^ x>>16
+ *   dither = 16 * (i even ? h mod 2^16 : h >> 16) + 8
+ * No workspace; the list travels in the launch.  Tensors must not overlap.
+ */
+moe_status_t moe_adamw_step(const moe_adamw_tensor_t* tensors, int n_tensors,
+                            const moe_adamw_t* settings, const float* norm, moe_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif
