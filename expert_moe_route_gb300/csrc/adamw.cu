@@ -25,6 +25,7 @@
 
 #include "adamw.cuh"
 #include "kernels.h"
+#include "rows.cuh"
 
 namespace moe {
 
@@ -36,7 +37,7 @@ constexpr int kPerLaunch = 256;              // tensors in one launch's paramete
 constexpr int kNormBlocks = 152 * 8;
 
 // Bits of AdamEntry::kind.
-constexpr int kP16 = 1, kG16 = 2, kS8 = 4, kWide = 8;
+constexpr int kP16 = 1, kG16 = 2, kWide = 4;
 
 struct AdamEntry {
   void* p;
@@ -90,96 +91,195 @@ __host__ __device__ __forceinline__ uint32_t mix(uint32_t x) {
 }
 constexpr uint32_t kGolden = 0x9E3779B1u;   // 2^32 / golden ratio
 
-// r in [0, 448] rounded to an E4M3 value by 20 dither bits: adding them below
-// the kept mantissa bits and cutting rounds up with probability equal to the
-// fraction.  Below 2^-6 the spacing is 2^-9; adding 2^-6 moves r to a binade
-// with that spacing.
-__device__ __forceinline__ float round_e4m3(float r, uint32_t dither) {
-  const float shift = r < 0.015625f ? 0.015625f : 0.f;
-  const uint32_t b = (__float_as_uint(__fadd_rn(r, shift)) + dither) & 0xFFF00000u;
-  return fminf(__uint_as_float(b) - shift, 448.f);
+// The E4M3 code (without sign) of one of the two neighbours of r >= 0, chosen by
+// 20 dither bits: added below the three kept mantissa bits they carry with
+// probability equal to the cut fraction.  Below 2^-6 the spacing is 2^-9; adding
+// 2^-6 moves r to a binade with that spacing, and the kept bits count it.
+// At most 0x7e (448).
+__device__ __forceinline__ uint32_t code_e4m3(float r, uint32_t dither) {
+  const bool low = r < 0.015625f;
+  const uint32_t b = __float_as_uint(r + (low ? 0.015625f : 0.f)) + dither;
+  return min((b >> 20) - (low ? 121u * 8 : 120u * 8), 0x7eu);
 }
 
-__device__ __forceinline__ float e4m3_value(uint8_t c) {
-  return __half2float(__half(__nv_cvt_fp8_to_halfraw(c, __NV_E4M3)));
+// Codes to values, two at a time (exact).
+__device__ __forceinline__ float2 e4m3x2_values(uint32_t two) {
+  const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)two, __NV_E4M3);
+  return __half22float2(*reinterpret_cast<const __half2*>(&h));
 }
 
+__device__ __forceinline__ float root_of(float v) {   // within 2^-23 of itself; 0 at 0
+  float u;
+  asm("sqrt.approx.f32 %0, %1;" : "=f"(u) : "f"(v));
+  return u;
+}
+
+// Largest of the warp's values (all >= 0: their bits order as they do).
 __device__ __forceinline__ float warp_max(float v) {
-#pragma unroll
-  for (int off = 16; off > 0; off >>= 1) v = fmaxf(v, __shfl_xor_sync(kFull, v, off));
-  return v;
+  return __uint_as_float(__reduce_max_sync(kFull, __float_as_uint(v)));
 }
 
-// One block of 256 elements of one tensor, elements lane + 32 j.
+__device__ __forceinline__ void ld8(const float* p, float* f) {   // 32-byte aligned
+  asm volatile("ld.global.v8.f32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=f"(f[0]), "=f"(f[1]), "=f"(f[2]), "=f"(f[3]), "=f"(f[4]), "=f"(f[5]),
+                 "=f"(f[6]), "=f"(f[7])
+               : "l"(p));
+}
+
+// This lane's eight elements of a block, as fp32.  In a block that is whole and
+// aligned (wide) lane l holds elements 8 l .. 8 l + 7, one access per array;
+// otherwise elements l + 32 j, single accesses, `left` of them in the block.
+struct Lane {
+  int lane, left;
+  bool wide;
+  __device__ __forceinline__ int at(int j) const { return wide ? lane * 8 + j : lane + 32 * j; }
+  __device__ __forceinline__ bool has(int j) const { return wide || lane + 32 * j < left; }
+
+  __device__ __forceinline__ void get_f32(const float* p, float* f) const {
+    if (wide) {
+      ld8(p + lane * 8, f);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) f[j] = has(j) ? p[at(j)] : 0.f;
+    }
+  }
+  __device__ __forceinline__ void put_f32(float* p, const float* f) const {
+    if (wide) {
+      st_global_v8(p + lane * 8, f);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (has(j)) p[at(j)] = f[j];
+    }
+  }
+  __device__ __forceinline__ void get_bf16(const uint16_t* p, float* f) const {
+    if (wide) {
+      unpack8(*reinterpret_cast<const uint4*>(p + lane * 8), f);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) f[j] = has(j) ? __uint_as_float((uint32_t)p[at(j)] << 16) : 0.f;
+    }
+  }
+  __device__ __forceinline__ void put_bf16(uint16_t* p, const float* f) const {
+    if (wide) {
+      *reinterpret_cast<uint4*>(p + lane * 8) = pack8(f);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (has(j)) p[at(j)] = __bfloat16_as_ushort(__float2bfloat16_rn(f[j]));
+    }
+  }
+  __device__ __forceinline__ uint2 get_codes(const uint8_t* p) const {
+    if (wide) return *reinterpret_cast<const uint2*>(p + lane * 8);
+    uint32_t w[2] = {0, 0};
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (has(j)) w[j / 4] |= (uint32_t)p[at(j)] << (8 * (j % 4));
+    return make_uint2(w[0], w[1]);
+  }
+  __device__ __forceinline__ void put_codes(uint8_t* p, const uint2& c) const {
+    if (wide) {
+      *reinterpret_cast<uint2*>(p + lane * 8) = c;
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (has(j)) p[at(j)] = (uint8_t)((j < 4 ? c.x : c.y) >> (8 * (j % 4)));
+    }
+  }
+};
+
+__device__ __forceinline__ void values8(const uint2& c, float* f) {
+  const uint32_t w[4] = {c.x & 0xffffu, c.x >> 16, c.y & 0xffffu, c.y >> 16};
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const float2 v = e4m3x2_values(w[j]);
+    f[2 * j] = v.x;
+    f[2 * j + 1] = v.y;
+  }
+}
+
+// One block of up to 256 elements of one tensor, one warp.
+template <bool S8>
 __device__ __forceinline__ void step_block(const AdamEntry& e, const AdamTable& t, long long base,
                                            float coef) {
-  const int lane = threadIdx.x & 31;
-  const long long blk = base / kBlock;
+  Lane l;
+  l.lane = threadIdx.x & 31;
+  l.left = (int)min((long long)kBlock, e.n - base);
+  l.wide = (e.kind & kWide) && l.left == kBlock;
+  float p[8], g[8], m[8], v[8];
   float ms = 0.f, vs = 0.f;
-  if (e.kind & kS8) {
+  const long long blk = base / kBlock;
+  if (e.kind & kG16) l.get_bf16((const uint16_t*)e.g + base, g);
+  else l.get_f32((const float*)e.g + base, g);
+  if (S8) {
+    const uint2 mc = l.get_codes((const uint8_t*)e.m + base);
+    const uint2 vc = l.get_codes((const uint8_t*)e.v + base);
     ms = e.m_scale[blk];
     vs = e.v_scale[blk];
+    values8(mc, m);
+    values8(vc, v);
+  } else {
+    l.get_f32((const float*)e.m + base, m);
+    l.get_f32((const float*)e.v + base, v);
   }
-  float m[8], u[8];
-  float am = 0.f, au = 0.f;
+  if (e.master) l.get_f32(e.master + base, p);
+  else if (e.kind & kP16) l.get_bf16((const uint16_t*)e.p + base, p);
+  else l.get_f32((const float*)e.p + base, p);
+  float u[8], am = 0.f, au = 0.f;
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
-    const long long i = base + lane + 32 * j;
-    m[j] = u[j] = 0.f;
-    if (i >= e.n) continue;
-    const float g0 = e.kind & kG16 ? __bfloat162float(((const __nv_bfloat16*)e.g)[i])
-                                   : ((const float*)e.g)[i];
-    const float g = __fmul_rn(g0, coef);
-    float m0, v0;
-    if (e.kind & kS8) {
-      m0 = __fmul_rn(e4m3_value(((const uint8_t*)e.m)[i]), ms);
-      const float q = __fmul_rn(e4m3_value(((const uint8_t*)e.v)[i]), vs);
-      v0 = __fmul_rn(q, q);
-    } else {
-      m0 = ((const float*)e.m)[i];
-      v0 = ((const float*)e.v)[i];
+    const float gc = g[j] * coef;
+    if (S8) {
+      m[j] *= ms;
+      v[j] *= vs;
+      v[j] *= v[j];
     }
-    m[j] = __fadd_rn(__fmul_rn(m0, t.b1), __fmul_rn(g, t.c1));
-    const float v = __fadd_rn(__fmul_rn(v0, t.b2), __fmul_rn(__fmul_rn(g, g), t.c2));
-    u[j] = __fsqrt_rn(v);
-    float p;
-    if (e.master) p = e.master[i];
-    else p = e.kind & kP16 ? __bfloat162float(((const __nv_bfloat16*)e.p)[i]) : ((const float*)e.p)[i];
-    p = p * e.decay - m[j] * t.step_size / (u[j] * t.root + t.eps);
-    if (e.master) e.master[i] = p;
-    if (e.kind & kP16) ((__nv_bfloat16*)e.p)[i] = __float2bfloat16_rn(p);
-    else ((float*)e.p)[i] = p;
-    if (!(e.kind & kS8)) {
-      ((float*)e.m)[i] = m[j];
-      ((float*)e.v)[i] = v;
+    m[j] = fmaf(m[j], t.b1, gc * t.c1);
+    v[j] = fmaf(v[j], t.b2, gc * gc * t.c2);
+    u[j] = root_of(v[j]);
+    p[j] = fmaf(p[j], e.decay, -__fdividef(m[j] * t.step_size, fmaf(u[j], t.root, t.eps)));
+    if (S8) {
+      am = fmaxf(am, fabsf(m[j]));
+      au = fmaxf(au, u[j]);
     }
-    am = fmaxf(am, fabsf(m[j]));
-    au = fmaxf(au, u[j]);
   }
-  if (!(e.kind & kS8)) return;
-  ms = __fdiv_rn(warp_max(am), 448.f);
-  vs = __fdiv_rn(warp_max(au), 448.f);
-  const float im = ms >= 0x1p-126f ? __fdiv_rn(1.f, ms) : 0.f;
-  const float iu = vs >= 0x1p-126f ? __fdiv_rn(1.f, vs) : 0.f;
-  if (lane == 0) {
+  if (e.master) l.put_f32(e.master + base, p);
+  if (e.kind & kP16) l.put_bf16((uint16_t*)e.p + base, p);
+  else l.put_f32((float*)e.p + base, p);
+  if (!S8) {
+    l.put_f32((float*)e.m + base, m);
+    l.put_f32((float*)e.v + base, v);
+    return;
+  }
+  // elements past the end hold zeros: they do not touch the maxima
+  ms = warp_max(am) / 448.f;
+  vs = warp_max(au) / 448.f;
+  const float im = ms >= 0x1p-126f ? 1.f / ms : 0.f;
+  const float iu = vs >= 0x1p-126f ? 1.f / vs : 0.f;
+  if (l.lane == 0) {
     e.m_scale[blk] = im > 0.f ? ms : 0.f;
     e.v_scale[blk] = iu > 0.f ? vs : 0.f;
   }
+  uint32_t mc[2] = {0, 0}, vc[2] = {0, 0};
+  uint32_t h = 0;
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
-    const long long i = base + lane + 32 * j;
-    if (i >= e.n) continue;
-    const uint32_t h = mix((uint32_t)((unsigned long long)i >> 1) * kGolden + e.place);
-    const uint32_t dither = ((i & 1 ? h >> 16 : h & 0xffffu) << 4) | 8u;
-    const float rm = fminf(__fmul_rn(fabsf(m[j]), im), 448.f);
-    const float ru = fminf(__fmul_rn(u[j], iu), 448.f);
-    const float qm = rm > 0.f ? round_e4m3(rm, dither) : 0.f;
-    const float qu = ru > 0.f ? fmaxf(round_e4m3(ru, dither), 0x1p-9f) : 0.f;
-    ((uint8_t*)e.m)[i] = __nv_cvt_float_to_fp8(copysignf(qm, m[j]), __NV_SATFINITE, __NV_E4M3);
-    ((uint8_t*)e.v)[i] = __nv_cvt_float_to_fp8(qu, __NV_SATFINITE, __NV_E4M3);
+    const uint32_t i = (uint32_t)((unsigned long long)(base + l.at(j)) >> 1);
+    if (!l.wide || j % 2 == 0) h = mix(i * kGolden + e.place);
+    const bool odd = l.wide ? j % 2 : l.lane & 1;
+    const uint32_t dither = (odd ? (h >> 12) & 0xffff0u : (h << 4) & 0xffff0u) | 8u;
+    const uint32_t cm = code_e4m3(fabsf(m[j]) * im, dither) |
+                        ((__float_as_uint(m[j]) >> 24) & 0x80u);
+    const float ru = u[j] * iu;
+    const uint32_t cu = max(code_e4m3(ru, dither), ru > 0.f ? 1u : 0u);
+    mc[j / 4] |= cm << (8 * (j % 4));
+    vc[j / 4] |= cu << (8 * (j % 4));
   }
+  l.put_codes((uint8_t*)e.m + base, make_uint2(mc[0], mc[1]));
+  l.put_codes((uint8_t*)e.v + base, make_uint2(vc[0], vc[1]));
 }
 
+template <bool S8>
 __global__ void __launch_bounds__(AT) adamw_kernel(const __grid_constant__ AdamTable t) {
   float coef = 1.f;
   if (t.norm) {
@@ -187,10 +287,15 @@ __global__ void __launch_bounds__(AT) adamw_kernel(const __grid_constant__ AdamT
     coef = t.norm[1];
   }
   const int wid = threadIdx.x >> 5;
+  int k = 0, end = 0;                  // the tensor of the last chunk, its first chunk past it
   for (int c = blockIdx.x; c < t.chunks; c += gridDim.x) {
-    const AdamEntry& e = t.e[entry_of(t, c)];
+    if (c >= end) {
+      k = entry_of(t, c);
+      end = k + 1 < t.count ? t.e[k + 1].first : t.chunks;
+    }
+    const AdamEntry& e = t.e[k];
     const long long base = (long long)(c - e.first) * kChunk + wid * kBlock;
-    if (base < e.n) step_block(e, t, base, coef);
+    if (base < e.n) step_block<S8>(e, t, base, coef);
   }
 }
 
@@ -200,25 +305,31 @@ __global__ void __launch_bounds__(AT) adamw_kernel(const __grid_constant__ AdamT
 __global__ void __launch_bounds__(AT) square_sums_kernel(const __grid_constant__ NormTable t,
                                                          double* __restrict__ sums) {
   __shared__ double red[AT / 32];
-  const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
+  const int wid = threadIdx.x >> 5;
   double sum = 0.0;
+  int k = 0, end = 0;
+  Lane l;
+  l.lane = threadIdx.x & 31;
   for (int c = blockIdx.x; c < t.chunks; c += gridDim.x) {
-    const NormEntry& e = t.e[entry_of(t, c)];
-    const long long base = (long long)(c - e.first) * kChunk;
-    float s = 0.f;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const long long i = base + threadIdx.x + AT * j;
-      if (i >= e.n) break;
-      const float g = e.kind & kG16 ? __bfloat162float(((const __nv_bfloat16*)e.g)[i])
-                                    : ((const float*)e.g)[i];
-      s = fmaf(g, g, s);
+    if (c >= end) {
+      k = entry_of(t, c);
+      end = k + 1 < t.count ? t.e[k + 1].first : t.chunks;
     }
+    const NormEntry& e = t.e[k];
+    const long long base = (long long)(c - e.first) * kChunk + wid * kBlock;
+    if (base >= e.n) continue;
+    l.left = (int)min((long long)kBlock, e.n - base);
+    l.wide = (e.kind & kWide) && l.left == kBlock;
+    float g[8], s = 0.f;
+    if (e.kind & kG16) l.get_bf16((const uint16_t*)e.g + base, g);
+    else l.get_f32((const float*)e.g + base, g);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) s = fmaf(g[j], g[j], s);
     sum += (double)s;
   }
 #pragma unroll
   for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(kFull, sum, off);
-  if (lane == 0) red[wid] = sum;
+  if (l.lane == 0) red[wid] = sum;
   __syncthreads();
   if (threadIdx.x == 0) {
     double total = 0.0;
@@ -250,6 +361,11 @@ __global__ void __launch_bounds__(AT) norm_kernel(const double* __restrict__ sum
 int chunks_of(long long n) { return (int)((n + kChunk - 1) / kChunk); }
 int grid_for(int chunks) { return chunks < kNormBlocks ? chunks : kNormBlocks; }
 int grad_bits(const moe_adamw_tensor_t& x) { return x.g_dtype == MOE_BF16 ? kG16 : 0; }
+
+// Eight elements of each array from any multiple of eight are one access.
+bool wide_at(const void* p, int element_bytes) {
+  return reinterpret_cast<uintptr_t>(p) % (8 * element_bytes) == 0;
+}
 
 // Calls launch(first tensor, past the last, chunks) for runs of tensors that fit
 // one launch's parameter and chunk count.
@@ -287,7 +403,8 @@ cudaError_t launch_grad_norm(const moe_adamw_tensor_t* x, int n, float max_norm,
     int first = 0;
     for (int k = i; k < j; ++k) {
       if (x[k].n == 0) continue;
-      t.e[t.count++] = {x[k].g, x[k].n, grad_bits(x[k]), first};
+      const bool wide = wide_at(x[k].g, dtype_bytes(x[k].g_dtype));
+      t.e[t.count++] = {x[k].g, x[k].n, grad_bits(x[k]) | (wide ? kWide : 0), first};
       first += chunks_of(x[k].n);
     }
     const int blocks = grid_for(chunks);
@@ -304,10 +421,8 @@ cudaError_t launch_grad_norm(const moe_adamw_tensor_t* x, int n, float max_norm,
 
 cudaError_t launch_adamw(const moe_adamw_tensor_t* x, int n, const moe_adamw_t& h,
                          const float* norm, cudaStream_t s) {
-  return in_runs(x, n, [&](int i, int j, int chunks) {
+  return in_runs(x, n, [&](int i, int j, int) {
     AdamTable t;
-    t.count = 0;
-    t.chunks = chunks;
     t.b1 = (float)h.beta1;
     t.b2 = (float)h.beta2;
     t.c1 = (float)(1.0 - h.beta1);
@@ -316,28 +431,36 @@ cudaError_t launch_adamw(const moe_adamw_tensor_t* x, int n, const moe_adamw_t& 
     t.root = (float)(1.0 / sqrt(1.0 - pow(h.beta2, (double)h.step)));
     t.eps = (float)h.eps;
     t.norm = norm;
-    int first = 0;
-    for (int k = i; k < j; ++k) {
-      if (x[k].n == 0) continue;
-      AdamEntry& e = t.e[t.count++];
-      e.p = x[k].p;
-      e.master = x[k].master;
-      e.g = x[k].g;
-      e.m = x[k].m;
-      e.v = x[k].v;
-      e.m_scale = x[k].m_scale;
-      e.v_scale = x[k].v_scale;
-      e.n = x[k].n;
-      e.decay = (float)(1.0 - h.lr * x[k].weight_decay);
-      e.place = mix(h.seed + (uint32_t)k * kGolden);
-      e.kind = grad_bits(x[k]) | (x[k].p_dtype == MOE_BF16 ? kP16 : 0) |
-               (x[k].state_bits == 8 ? kS8 : 0);
-      e.first = first;
-      first += chunks_of(x[k].n);
+    for (const int bits : {8, 32}) {   // a launch for each kind of state in the run
+      t.count = t.chunks = 0;
+      for (int k = i; k < j; ++k) {
+        if (x[k].n == 0 || x[k].state_bits != bits) continue;
+        AdamEntry& e = t.e[t.count++];
+        e.p = x[k].p;
+        e.master = x[k].master;
+        e.g = x[k].g;
+        e.m = x[k].m;
+        e.v = x[k].v;
+        e.m_scale = x[k].m_scale;
+        e.v_scale = x[k].v_scale;
+        e.n = x[k].n;
+        e.decay = (float)(1.0 - h.lr * x[k].weight_decay);
+        e.place = mix(h.seed + (uint32_t)k * kGolden);
+        const bool wide = wide_at(e.p, dtype_bytes(x[k].p_dtype)) && wide_at(e.master, 4) &&
+                          wide_at(e.g, dtype_bytes(x[k].g_dtype)) && wide_at(e.m, bits / 8) &&
+                          wide_at(e.v, bits / 8);
+        e.kind = grad_bits(x[k]) | (x[k].p_dtype == MOE_BF16 ? kP16 : 0) | (wide ? kWide : 0);
+        e.first = t.chunks;
+        t.chunks += chunks_of(x[k].n);
+      }
+      if (t.count == 0) continue;
+      if (bits == 8) adamw_kernel<true><<<grid_for(t.chunks), AT, 0, s>>>(t);
+      else adamw_kernel<false><<<grid_for(t.chunks), AT, 0, s>>>(t);
+      count_launches(1);
+      const cudaError_t e = cudaGetLastError();
+      if (e != cudaSuccess) return e;
     }
-    adamw_kernel<<<grid_for(chunks), AT, 0, s>>>(t);
-    count_launches(1);
-    return cudaGetLastError();
+    return cudaSuccess;
   });
 }
 

@@ -11,7 +11,8 @@
 // Both are bound by HBM.  A group of threads (a warp for short rows, a block for
 // long ones) owns a token: x[t] is read once for its R rows (row by row it would
 // be read R times, from all over the sorted order).
-#include "common.cuh"
+#include <algorithm>
+
 #include "kernels.h"
 #include "permute.cuh"
 
@@ -21,45 +22,49 @@ namespace {
 constexpr int PT = 256;              // threads per block
 constexpr int kMaxR = 32;
 
-// Sums acc[0..R) over the threads of a group (32 or PT threads); every thread of
-// the group's first warp gets the sums.
-template <int G, int RM>
-__device__ __forceinline__ void group_sum(float (&acc)[RM], int R, float* red) {
-  const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
+// Sums each of acc[0..RM) over the warp: every exchange halves the values a lane
+// still holds, RM - 1 + log2(32 / RM) shuffles instead of 5 RM.  Lane
+// r * (32 / RM) ends with the sum of acc[r] in acc[0].
+template <int RM>
+__device__ __forceinline__ void warp_sums(float (&acc)[RM]) {
+  const int lane = threadIdx.x & 31;
+  int off = 16;
 #pragma unroll
-  for (int r = 0; r < RM; ++r) {
-    if (r >= R) break;
+  for (int n = RM; n > 1; n /= 2, off /= 2) {
+    const bool hi = lane & off;
 #pragma unroll
-    for (int off = 16; off > 0; off >>= 1) acc[r] += __shfl_xor_sync(kFull, acc[r], off);
-  }
-  if (G == 32) return;
-#pragma unroll
-  for (int r = 0; r < RM; ++r) {
-    if (r >= R) break;
-    if (lane == 0) red[wid * kMaxR + r] = acc[r];
-  }
-  __syncthreads();
-  if (wid == 0) {
-#pragma unroll
-    for (int r = 0; r < RM; ++r) {
-      if (r >= R) break;
-      float s = 0.f;
-      for (int w = 0; w < PT / 32; ++w) s += red[w * kMaxR + r];
-      acc[r] = s;
+    for (int i = 0; i < RM / 2; ++i) {
+      if (i >= n / 2) break;
+      const float send = hi ? acc[i] : acc[i + n / 2];
+      const float keep = hi ? acc[i + n / 2] : acc[i];
+      acc[i] = keep + __shfl_xor_sync(kFull, send, off);
     }
   }
+#pragma unroll
+  for (; off > 0; off /= 2) acc[0] += __shfl_xor_sync(kFull, acc[0], off);
 }
 
-// lane r of the group's first warp writes dw[t, r]; slots without a row get 0.
-template <int RM>
-__device__ __forceinline__ void store_dots(const float (&acc)[RM], const int* rows_s, int R,
+// dw[r] = acc[r] summed over the group (32 or PT threads); slots without a row
+// get 0.  Ends with the group's threads in step when G > 32.
+template <int G, int RM>
+__device__ __forceinline__ void store_dots(float (&acc)[RM], const int* rows_s, int R, float* red,
                                            float* dw) {
-  const int lane = threadIdx.x & 31;
-  float mine = 0.f;
+  constexpr int STEP = 32 / RM;
+  const int lane = threadIdx.x & 31, gt = threadIdx.x % G;
+  warp_sums<RM>(acc);
+  const int r = lane / STEP;
+  if (G == 32) {
+    if (lane % STEP == 0 && r < R) dw[r] = rows_s[r] >= 0 ? acc[0] : 0.f;
+    return;
+  }
+  if (lane % STEP == 0) red[gt / 32 * RM + r] = acc[0];
+  __syncthreads();
+  if (gt < R) {
+    float s = 0.f;
 #pragma unroll
-  for (int r = 0; r < RM; ++r)
-    if (r == lane) mine = acc[r];
-  if (lane < R) dw[lane] = rows_s[lane] >= 0 ? mine : 0.f;
+    for (int w = 0; w < G / 32; ++w) s += red[w * RM + gt];
+    dw[gt] = rows_s[gt] >= 0 ? s : 0.f;
+  }
 }
 
 template <typename T, int W, int G, int RM, bool DOTS>
@@ -71,7 +76,7 @@ __global__ void __launch_bounds__(PT) spread_kernel(
   constexpr int NG = PT / G;
   __shared__ int rows_s[NG][kMaxR];
   __shared__ float w_s[NG][kMaxR];
-  __shared__ float red[DOTS && G > 32 ? PT / 32 * kMaxR : 1];
+  __shared__ float red[DOTS && G > 32 ? PT / 32 * RM : 1];
   using V = Vec<T, W>;
   const int grp = threadIdx.x / G, gt = threadIdx.x % G;
   const int nv = d / W;
@@ -120,22 +125,20 @@ __global__ void __launch_bounds__(PT) spread_kernel(
         }
       }
     }
-    if (DOTS) {
-      group_sum<G, RM>(acc, R, red);
-      if (gt < 32) store_dots(acc, rows_s[grp], R, dw + t * R);
-    }
+    if (DOTS) store_dots<G, RM>(acc, rows_s[grp], R, red, dw + t * R);
     sync();
   }
-  // rows without a slot are zero
+  // Rows without a slot are zero.  They come in runs (the ends of segments), so
+  // neighbouring rows go to different groups; a group looks at 32 rows at a time.
   const int lane = threadIdx.x & 31;
-  const long long warps = (long long)gridDim.x * (PT / 32);
-  for (long long i = ((long long)blockIdx.x * (PT / 32) + threadIdx.x / 32) * 32; i < N;
-       i += warps * 32) {
-    unsigned empty = __ballot_sync(kFull, i + lane < N && row_slot[i + lane] < 0);
+  const long long groups = (long long)gridDim.x * NG;
+  for (long long i = (long long)blockIdx.x * NG + grp; i < N; i += groups * 32) {
+    const long long mine = i + lane * groups;
+    unsigned empty = __ballot_sync(kFull, mine < N && row_slot[mine] < 0);
     while (empty) {
-      const long long row = i + __ffs(empty) - 1;
+      const long long row = i + (__ffs(empty) - 1) * groups;
       empty &= empty - 1;
-      for (int v = lane; v < nv; v += 32) V::store(rows + row * ldr + (long long)v * W, V::zero());
+      for (int v = gt; v < nv; v += G) V::store(rows + row * ldr + (long long)v * W, V::zero());
     }
   }
 }
@@ -148,7 +151,7 @@ __global__ void __launch_bounds__(PT) collect_kernel(
   constexpr int NG = PT / G;
   __shared__ int rows_s[NG][kMaxR];
   __shared__ float w_s[NG][kMaxR];
-  __shared__ float red[DOTS && G > 32 ? PT / 32 * kMaxR : 1];
+  __shared__ float red[DOTS && G > 32 ? PT / 32 * RM : 1];
   using V = Vec<T, W>;
   const int grp = threadIdx.x / G, gt = threadIdx.x % G;
   const int nv = d / W;
@@ -193,20 +196,15 @@ __global__ void __launch_bounds__(PT) collect_kernel(
       }
       V::store(y + t * ldy + (long long)v * W, V::pack(sum));
     }
-    if (DOTS) {
-      group_sum<G, RM>(acc, R, red);
-      if (gt < 32) store_dots(acc, rows_s[grp], R, dw + t * R);
-    }
+    if (DOTS) store_dots<G, RM>(acc, rows_s[grp], R, red, dw + t * R);
     sync();
   }
 }
 
 template <typename T, int W, int G, int RM>
 cudaError_t spread_t(const PermuteArgs& a, cudaStream_t s) {
-  const long long units = ((long long)a.T + PT / G - 1) / (PT / G);
-  const long long fill = (a.N + PT - 1) / PT;          // 32 rows a warp
-  const long long want = units > fill ? units : fill;
-  const int blocks = (int)(want < 152 * 8 ? want : 152 * 8);
+  const long long units = std::max<long long>(a.T, (a.N + 31) / 32);
+  const int blocks = (int)((units + PT / G - 1) / (PT / G));
   if (a.dw)
     spread_kernel<T, W, G, RM, true><<<blocks, PT, 0, s>>>(
         (const T*)a.tok.p, a.tok.ld, a.w, a.row_slot, a.slot_row, a.T, a.d, a.R, a.N,
@@ -221,8 +219,7 @@ cudaError_t spread_t(const PermuteArgs& a, cudaStream_t s) {
 
 template <typename T, int W, int G, int RM>
 cudaError_t collect_t(const PermuteArgs& a, cudaStream_t s) {
-  const long long units = ((long long)a.T + PT / G - 1) / (PT / G);
-  const int blocks = (int)(units < 152 * 8 ? units : 152 * 8);
+  const int blocks = (int)(((long long)a.T + PT / G - 1) / (PT / G));
   if (a.dw)
     collect_kernel<T, W, G, RM, true><<<blocks, PT, 0, s>>>(
         (const T*)a.tok.p, a.tok.ld, a.slot_row, a.w, a.T, a.d, a.R, a.N, (const T*)a.other.p,
@@ -235,8 +232,12 @@ cudaError_t collect_t(const PermuteArgs& a, cudaStream_t s) {
   return cudaGetLastError();
 }
 
+// A block per token for rows of over 128 accesses, a warp for shorter ones.  At
+// T = 16384, d = 4096 bf16 a block takes 362 us for moe_unpermute_bwd and a warp
+// 373, at T = 4096, d = 2048 moe_permute_bwd 29 and 40 us: a warp's rows wait for
+// one another.
 template <typename T, int W> cudaError_t by_shape(const PermuteArgs& a, bool spread, cudaStream_t s) {
-  const bool wide = a.d / W > 128;     // a block per token
+  const bool wide = a.d / W > 128;
   if (a.R <= 8) {
     if (spread) return wide ? spread_t<T, W, PT, 8>(a, s) : spread_t<T, W, 32, 8>(a, s);
     return wide ? collect_t<T, W, PT, 8>(a, s) : collect_t<T, W, 32, 8>(a, s);

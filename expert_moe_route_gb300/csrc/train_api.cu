@@ -1,6 +1,7 @@
 // C ABI of the operators around the layer in a training step (declared in
 // include/moe.h): argument checks, workspace layout, launches on the caller's
 // stream.
+#include <float.h>
 #include <math.h>
 
 #include <algorithm>
@@ -263,7 +264,7 @@ moe_status_t moe_adamw_step(const moe_adamw_tensor_t* tensors, int n_tensors,
   if (!settings) return MOE_ERR_INVALID_ARG;
   const moe_adamw_t& h = *settings;
   if (!isfinite(h.lr) || !(h.beta1 >= 0 && h.beta1 < 1) || !(h.beta2 >= 0 && h.beta2 < 1) ||
-      !((float)h.eps > 0) || !isfinite((float)h.eps) || h.step < 1)
+      !((float)h.eps >= FLT_MIN) || !isfinite((float)h.eps) || h.step < 1)
     return MOE_ERR_INVALID_ARG;
   if (!aligned(norm, 16)) return MOE_ERR_UNSUPPORTED;
   return finish(launch_adamw(tensors, n_tensors, h, norm, S(stream)), nullptr, 0, S(stream));

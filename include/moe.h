@@ -638,6 +638,7 @@ moe_status_t moe_grad_norm(const moe_adamw_tensor_t* tensors, int n_tensors, dou
  *   mix(x): x = (x ^ x>>16) * 0x6A09E667; x = (x ^ x>>15) * 0xBB67AE85; x ^ x>>16
  *   dither = 16 * (i even ? h mod 2^16 : h >> 16) + 8
  * No workspace; the list travels in the launch.  Tensors must not overlap.
+ * step >= 1, 0 <= beta < 1, eps at least the smallest normal fp32 number.
  */
 moe_status_t moe_adamw_step(const moe_adamw_tensor_t* tensors, int n_tensors,
                             const moe_adamw_t* settings, const float* norm, moe_stream_t stream);
