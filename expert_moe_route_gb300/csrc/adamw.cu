@@ -91,21 +91,32 @@ __host__ __device__ __forceinline__ uint32_t mix(uint32_t x) {
 }
 constexpr uint32_t kGolden = 0x9E3779B1u;   // 2^32 / golden ratio
 
-// The E4M3 code (without sign) of one of the two neighbours of r >= 0, chosen by
-// 20 dither bits: added below the three kept mantissa bits they carry with
-// probability equal to the cut fraction.  Below 2^-6 the spacing is 2^-9; adding
-// 2^-6 moves r to a binade with that spacing, and the kept bits count it.
-// At most 0x7e (448).
-__device__ __forceinline__ uint32_t code_e4m3(float r, uint32_t dither) {
-  const bool low = r < 0.015625f;
-  const uint32_t b = __float_as_uint(r + (low ? 0.015625f : 0.f)) + dither;
-  return min((b >> 20) - (low ? 121u * 8 : 120u * 8), 0x7eu);
+// r / 2^120 in fp32 has E4M3's exponent field (bias 7 against 127) and, below
+// 2^-6, its fixed spacing, since fp32 becomes subnormal at 2^-126: the bits'
+// upper end is the code.  20 dither bits added below the three kept mantissa bits
+// carry into them with probability equal to the cut fraction.  Multiplying by 16
+// moves the code to the top byte and drops the sign; `dither` comes times 16.
+// r <= 448 (1 + 3 * 2^-24) cannot carry past 448: the dither's last bits are 1000.
+constexpr float kToCode = 0x1p-120f;
+__device__ __forceinline__ uint32_t code_top(float scaled, uint32_t dither) {
+  return __float_as_uint(scaled) * 16u + dither;
+}
+
+// The top bytes of four words.
+__device__ __forceinline__ uint32_t top_bytes(const uint32_t* w) {
+  return __byte_perm(__byte_perm(w[0], w[1], 0x0073), __byte_perm(w[2], w[3], 0x0073), 0x5410);
 }
 
 // Codes to values, two at a time (exact).
 __device__ __forceinline__ float2 e4m3x2_values(uint32_t two) {
   const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)two, __NV_E4M3);
   return __half22float2(*reinterpret_cast<const __half2*>(&h));
+}
+
+__device__ __forceinline__ float reciprocal(float v) {   // v normal; within 2^-23 of itself
+  float u;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(u) : "f"(v));
+  return u;
 }
 
 __device__ __forceinline__ float root_of(float v) {   // within 2^-23 of itself; 0 at 0
@@ -127,24 +138,24 @@ __device__ __forceinline__ void ld8(const float* p, float* f) {   // 32-byte ali
 }
 
 // This lane's eight elements of a block, as fp32.  In a block that is whole and
-// aligned (wide) lane l holds elements 8 l .. 8 l + 7, one access per array;
+// aligned (WIDE) lane l holds elements 8 l .. 8 l + 7, one access per array;
 // otherwise elements l + 32 j, single accesses, `left` of them in the block.
+template <bool WIDE>
 struct Lane {
   int lane, left;
-  bool wide;
-  __device__ __forceinline__ int at(int j) const { return wide ? lane * 8 + j : lane + 32 * j; }
-  __device__ __forceinline__ bool has(int j) const { return wide || lane + 32 * j < left; }
+  __device__ __forceinline__ int at(int j) const { return WIDE ? lane * 8 + j : lane + 32 * j; }
+  __device__ __forceinline__ bool has(int j) const { return WIDE || lane + 32 * j < left; }
 
-  __device__ __forceinline__ void get_f32(const float* p, float* f) const {
-    if (wide) {
+  __device__ __forceinline__ void get(const float* p, float* f) const {
+    if (WIDE) {
       ld8(p + lane * 8, f);
     } else {
 #pragma unroll
       for (int j = 0; j < 8; ++j) f[j] = has(j) ? p[at(j)] : 0.f;
     }
   }
-  __device__ __forceinline__ void put_f32(float* p, const float* f) const {
-    if (wide) {
+  __device__ __forceinline__ void put(float* p, const float* f) const {
+    if (WIDE) {
       st_global_v8(p + lane * 8, f);
     } else {
 #pragma unroll
@@ -152,16 +163,16 @@ struct Lane {
         if (has(j)) p[at(j)] = f[j];
     }
   }
-  __device__ __forceinline__ void get_bf16(const uint16_t* p, float* f) const {
-    if (wide) {
+  __device__ __forceinline__ void get(const uint16_t* p, float* f) const {   // bf16
+    if (WIDE) {
       unpack8(*reinterpret_cast<const uint4*>(p + lane * 8), f);
     } else {
 #pragma unroll
       for (int j = 0; j < 8; ++j) f[j] = has(j) ? __uint_as_float((uint32_t)p[at(j)] << 16) : 0.f;
     }
   }
-  __device__ __forceinline__ void put_bf16(uint16_t* p, const float* f) const {
-    if (wide) {
+  __device__ __forceinline__ void put(uint16_t* p, const float* f) const {
+    if (WIDE) {
       *reinterpret_cast<uint4*>(p + lane * 8) = pack8(f);
     } else {
 #pragma unroll
@@ -169,21 +180,40 @@ struct Lane {
         if (has(j)) p[at(j)] = __bfloat16_as_ushort(__float2bfloat16_rn(f[j]));
     }
   }
-  __device__ __forceinline__ uint2 get_codes(const uint8_t* p) const {
-    if (wide) return *reinterpret_cast<const uint2*>(p + lane * 8);
+  __device__ __forceinline__ uint2 get(const uint8_t* p) const {   // codes
+    if (WIDE) return *reinterpret_cast<const uint2*>(p + lane * 8);
     uint32_t w[2] = {0, 0};
 #pragma unroll
     for (int j = 0; j < 8; ++j)
       if (has(j)) w[j / 4] |= (uint32_t)p[at(j)] << (8 * (j % 4));
     return make_uint2(w[0], w[1]);
   }
-  __device__ __forceinline__ void put_codes(uint8_t* p, const uint2& c) const {
-    if (wide) {
+  __device__ __forceinline__ void put(uint8_t* p, const uint2& c) const {
+    if (WIDE) {
       *reinterpret_cast<uint2*>(p + lane * 8) = c;
     } else {
 #pragma unroll
       for (int j = 0; j < 8; ++j)
         if (has(j)) p[at(j)] = (uint8_t)((j < 4 ? c.x : c.y) >> (8 * (j % 4)));
+    }
+  }
+  // Each element's dither times 16, for the block's first element `base`.
+  __device__ __forceinline__ void dithers(long long base, uint32_t place, uint32_t* d) const {
+    const uint32_t first = (uint32_t)((unsigned long long)base >> 1);   // base is even
+    if (WIDE) {
+      const uint32_t x = (first + lane * 4) * kGolden + place;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const uint32_t h = mix(x + j * kGolden);
+        d[2 * j] = __byte_perm(h, 0x80, 0x5104);       // (h & 0xffff) << 8 | 0x80
+        d[2 * j + 1] = __byte_perm(h, 0x80, 0x5324);   // (h >> 16) << 8 | 0x80
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const uint32_t h = mix((first + (lane >> 1) + 16 * j) * kGolden + place);
+        d[j] = (lane & 1 ? h >> 16 : h & 0xffffu) << 8 | 0x80u;
+      }
     }
   }
 };
@@ -198,57 +228,73 @@ __device__ __forceinline__ void values8(const uint2& c, float* f) {
   }
 }
 
-// One block of up to 256 elements of one tensor, one warp.
-template <bool S8>
+__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
+
+// One block of up to 256 elements of one tensor, one warp.  The arithmetic goes
+// in pairs (two fp32 products, sums or fused products an instruction): with
+// 8-bit states the instructions, not the bytes, are what a plain form runs out of.
+template <bool S8, bool WIDE>
 __device__ __forceinline__ void step_block(const AdamEntry& e, const AdamTable& t, long long base,
-                                           float coef) {
-  Lane l;
+                                           int left, float coef) {
+  Lane<WIDE> l;
   l.lane = threadIdx.x & 31;
-  l.left = (int)min((long long)kBlock, e.n - base);
-  l.wide = (e.kind & kWide) && l.left == kBlock;
-  float p[8], g[8], m[8], v[8];
-  float ms = 0.f, vs = 0.f;
+  l.left = left;
+  float p[8], g[8], m[8], v[8], u[8];
+  float ms = 1.f, vs = 1.f;
   const long long blk = base / kBlock;
-  if (e.kind & kG16) l.get_bf16((const uint16_t*)e.g + base, g);
-  else l.get_f32((const float*)e.g + base, g);
+  if (e.kind & kG16) l.get((const uint16_t*)e.g + base, g);
+  else l.get((const float*)e.g + base, g);
   if (S8) {
-    const uint2 mc = l.get_codes((const uint8_t*)e.m + base);
-    const uint2 vc = l.get_codes((const uint8_t*)e.v + base);
+    const uint2 mc = l.get((const uint8_t*)e.m + base);
+    const uint2 vc = l.get((const uint8_t*)e.v + base);
     ms = e.m_scale[blk];
     vs = e.v_scale[blk];
     values8(mc, m);
     values8(vc, v);
   } else {
-    l.get_f32((const float*)e.m + base, m);
-    l.get_f32((const float*)e.v + base, v);
+    l.get((const float*)e.m + base, m);
+    l.get((const float*)e.v + base, v);
   }
-  if (e.master) l.get_f32(e.master + base, p);
-  else if (e.kind & kP16) l.get_bf16((const uint16_t*)e.p + base, p);
-  else l.get_f32((const float*)e.p + base, p);
-  float u[8], am = 0.f, au = 0.f;
+  if (e.master) l.get(e.master + base, p);
+  else if (e.kind & kP16) l.get((const uint16_t*)e.p + base, p);
+  else l.get((const float*)e.p + base, p);
+  const float2 mb = both(ms * t.b1), gm = both(coef * t.c1), k = both(coef);
+  const float2 b2 = both(t.b2), c2 = both(t.c2), qs = both(vs);
+  const float2 root = both(t.root), eps = both(t.eps), decay = both(e.decay),
+               step = both(-t.step_size);
+  float am = 0.f, au = 0.f;
 #pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    const float gc = g[j] * coef;
+  for (int j = 0; j < 8; j += 2) {
+    const float2 gj = make_float2(g[j], g[j + 1]);
+    const float2 mj = __ffma2_rn(gj, gm, __fmul2_rn(make_float2(m[j], m[j + 1]), mb));
+    const float2 gc = __fmul2_rn(gj, k);
+    const float2 sq = __fmul2_rn(gc, __fmul2_rn(gc, c2));
+    float2 vj = make_float2(v[j], v[j + 1]);
     if (S8) {
-      m[j] *= ms;
-      v[j] *= vs;
-      v[j] *= v[j];
+      const float2 q = __fmul2_rn(vj, qs);
+      vj = __ffma2_rn(q, __fmul2_rn(q, b2), sq);
+    } else {
+      vj = __ffma2_rn(vj, b2, sq);
     }
-    m[j] = fmaf(m[j], t.b1, gc * t.c1);
-    v[j] = fmaf(v[j], t.b2, gc * gc * t.c2);
-    u[j] = root_of(v[j]);
-    p[j] = fmaf(p[j], e.decay, -__fdividef(m[j] * t.step_size, fmaf(u[j], t.root, t.eps)));
+    const float2 uj = make_float2(root_of(vj.x), root_of(vj.y));
+    const float2 den = __ffma2_rn(uj, root, eps);
+    const float2 ratio = __fmul2_rn(mj, make_float2(reciprocal(den.x), reciprocal(den.y)));
+    const float2 pj = __ffma2_rn(ratio, step, __fmul2_rn(make_float2(p[j], p[j + 1]), decay));
+    p[j] = pj.x, p[j + 1] = pj.y;
+    m[j] = mj.x, m[j + 1] = mj.y;
+    v[j] = vj.x, v[j + 1] = vj.y;
+    u[j] = uj.x, u[j + 1] = uj.y;
     if (S8) {
-      am = fmaxf(am, fabsf(m[j]));
-      au = fmaxf(au, u[j]);
+      am = fmaxf(fmaxf(am, fabsf(mj.x)), fabsf(mj.y));
+      au = fmaxf(fmaxf(au, uj.x), uj.y);
     }
   }
-  if (e.master) l.put_f32(e.master + base, p);
-  if (e.kind & kP16) l.put_bf16((uint16_t*)e.p + base, p);
-  else l.put_f32((float*)e.p + base, p);
+  if (e.master) l.put(e.master + base, p);
+  if (e.kind & kP16) l.put((uint16_t*)e.p + base, p);
+  else l.put((float*)e.p + base, p);
   if (!S8) {
-    l.put_f32((float*)e.m + base, m);
-    l.put_f32((float*)e.v + base, v);
+    l.put((float*)e.m + base, m);
+    l.put((float*)e.v + base, v);
     return;
   }
   // elements past the end hold zeros: they do not touch the maxima
@@ -260,23 +306,20 @@ __device__ __forceinline__ void step_block(const AdamEntry& e, const AdamTable& 
     e.m_scale[blk] = im > 0.f ? ms : 0.f;
     e.v_scale[blk] = iu > 0.f ? vs : 0.f;
   }
-  uint32_t mc[2] = {0, 0}, vc[2] = {0, 0};
-  uint32_t h = 0;
+  uint32_t d[8], wm[8], wu[8];
+  l.dithers(base, e.place, d);
 #pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    const uint32_t i = (uint32_t)((unsigned long long)(base + l.at(j)) >> 1);
-    if (!l.wide || j % 2 == 0) h = mix(i * kGolden + e.place);
-    const bool odd = l.wide ? j % 2 : l.lane & 1;
-    const uint32_t dither = (odd ? (h >> 12) & 0xffff0u : (h << 4) & 0xffff0u) | 8u;
-    const uint32_t cm = code_e4m3(fabsf(m[j]) * im, dither) |
-                        ((__float_as_uint(m[j]) >> 24) & 0x80u);
-    const float ru = u[j] * iu;
-    const uint32_t cu = max(code_e4m3(ru, dither), ru > 0.f ? 1u : 0u);
-    mc[j / 4] |= cm << (8 * (j % 4));
-    vc[j / 4] |= cu << (8 * (j % 4));
+  for (int j = 0; j < 8; j += 2) {
+    const float2 to = both(kToCode);
+    const float2 rm = __fmul2_rn(__fmul2_rn(make_float2(m[j], m[j + 1]), both(im)), to);
+    const float2 ru = __fmul2_rn(__fmul2_rn(make_float2(u[j], u[j + 1]), both(iu)), to);
+    wm[j] = code_top(rm.x, d[j]) | (__float_as_uint(rm.x) & 0x80000000u);
+    wm[j + 1] = code_top(rm.y, d[j + 1]) | (__float_as_uint(rm.y) & 0x80000000u);
+    wu[j] = max(code_top(ru.x, d[j]), ru.x > 0.f ? 1u << 24 : 0u);
+    wu[j + 1] = max(code_top(ru.y, d[j + 1]), ru.y > 0.f ? 1u << 24 : 0u);
   }
-  l.put_codes((uint8_t*)e.m + base, make_uint2(mc[0], mc[1]));
-  l.put_codes((uint8_t*)e.v + base, make_uint2(vc[0], vc[1]));
+  l.put((uint8_t*)e.m + base, make_uint2(top_bytes(wm), top_bytes(wm + 4)));
+  l.put((uint8_t*)e.v + base, make_uint2(top_bytes(wu), top_bytes(wu + 4)));
 }
 
 template <bool S8>
@@ -295,11 +338,21 @@ __global__ void __launch_bounds__(AT) adamw_kernel(const __grid_constant__ AdamT
     }
     const AdamEntry& e = t.e[k];
     const long long base = (long long)(c - e.first) * kChunk + wid * kBlock;
-    if (base < e.n) step_block<S8>(e, t, base, coef);
+    if (base >= e.n) continue;
+    const int left = (int)min((long long)kBlock, e.n - base);
+    if ((e.kind & kWide) && left == kBlock) step_block<S8, true>(e, t, base, left, coef);
+    else step_block<S8, false>(e, t, base, left, coef);
   }
 }
 
 // ---------------------------------------------------------------- norm
+template <bool WIDE>
+__device__ __forceinline__ void get_grad(const Lane<WIDE>& l, const NormEntry& e, long long base,
+                                         float* g) {
+  if (e.kind & kG16) l.get((const uint16_t*)e.g + base, g);
+  else l.get((const float*)e.g + base, g);
+}
+
 // Block b's sum of squares over its chunks: fp32 over a thread's eight elements
 // of a chunk, double from there.
 __global__ void __launch_bounds__(AT) square_sums_kernel(const __grid_constant__ NormTable t,
@@ -308,8 +361,7 @@ __global__ void __launch_bounds__(AT) square_sums_kernel(const __grid_constant__
   const int wid = threadIdx.x >> 5;
   double sum = 0.0;
   int k = 0, end = 0;
-  Lane l;
-  l.lane = threadIdx.x & 31;
+  const int lane = threadIdx.x & 31;
   for (int c = blockIdx.x; c < t.chunks; c += gridDim.x) {
     if (c >= end) {
       k = entry_of(t, c);
@@ -318,18 +370,17 @@ __global__ void __launch_bounds__(AT) square_sums_kernel(const __grid_constant__
     const NormEntry& e = t.e[k];
     const long long base = (long long)(c - e.first) * kChunk + wid * kBlock;
     if (base >= e.n) continue;
-    l.left = (int)min((long long)kBlock, e.n - base);
-    l.wide = (e.kind & kWide) && l.left == kBlock;
+    const int left = (int)min((long long)kBlock, e.n - base);
     float g[8], s = 0.f;
-    if (e.kind & kG16) l.get_bf16((const uint16_t*)e.g + base, g);
-    else l.get_f32((const float*)e.g + base, g);
+    if ((e.kind & kWide) && left == kBlock) get_grad(Lane<true>{lane, left}, e, base, g);
+    else get_grad(Lane<false>{lane, left}, e, base, g);
 #pragma unroll
     for (int j = 0; j < 8; ++j) s = fmaf(g[j], g[j], s);
     sum += (double)s;
   }
 #pragma unroll
   for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(kFull, sum, off);
-  if (l.lane == 0) red[wid] = sum;
+  if (lane == 0) red[wid] = sum;
   __syncthreads();
   if (threadIdx.x == 0) {
     double total = 0.0;

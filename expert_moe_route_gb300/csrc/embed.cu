@@ -20,55 +20,52 @@ namespace {
 constexpr int ET = 256;
 constexpr int kPiece = 64;
 
+// A group of G threads copies kRows rows side by side, so that a thread has that
+// many loads in flight although a row is only one or two accesses a thread.
+constexpr int kRows = 4;
+
 template <typename T, typename O, int W, int G, typename I>
 __global__ void __launch_bounds__(ET) embed_kernel(const I* __restrict__ ids, long long n,
                                                    const T* __restrict__ table, long long ldt,
                                                    int V, int d, float scale, O* __restrict__ out,
                                                    long long ldo) {
-  constexpr int NG = ET / G;
   const int grp = threadIdx.x / G, gt = threadIdx.x % G;
   const int nv = d / W;
-  for (long long i = (long long)blockIdx.x * NG + grp; i < n; i += (long long)gridDim.x * NG) {
-    const I id = ids[i];
-    const bool live = id >= 0 && id < (I)V;
-    const T* src = table + (live ? (long long)id : 0) * ldt;
-    O* dst = out + i * ldo;
-    for (int v0 = gt; v0 < nv; v0 += G * 4) {
-      typename Vec<T, W>::Raw q[4];
+  const long long i0 = ((long long)blockIdx.x * (ET / G) + grp) * kRows;
+  const T* src[kRows];
+  bool live[kRows];
 #pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        const int v = v0 + u * G;
-        q[u] = live && v < nv ? Vec<T, W>::load(src + (long long)v * W) : Vec<T, W>::zero();
-      }
+  for (int u = 0; u < kRows; ++u) {
+    const I id = i0 + u < n ? ids[i0 + u] : (I)-1;
+    live[u] = id >= 0 && id < (I)V;
+    src[u] = table + (live[u] ? (long long)id : 0) * ldt;
+  }
+  for (int v = gt; v < nv; v += G) {
+    typename Vec<T, W>::Raw q[kRows];
 #pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        const int v = v0 + u * G;
-        if (v >= nv) break;
-        float f[W];
-        Vec<T, W>::unpack(q[u], f);
+    for (int u = 0; u < kRows; ++u)
+      q[u] = live[u] ? Vec<T, W>::load(src[u] + (long long)v * W) : Vec<T, W>::zero();
 #pragma unroll
-        for (int j = 0; j < W; ++j) f[j] = live ? f[j] * scale : 0.f;
-        Vec<O, W>::store(dst + (long long)v * W, Vec<O, W>::pack(f));
-      }
+    for (int u = 0; u < kRows; ++u) {
+      if (i0 + u >= n) break;
+      float f[W];
+      Vec<T, W>::unpack(q[u], f);
+#pragma unroll
+      for (int j = 0; j < W; ++j) f[j] = live[u] ? f[j] * scale : 0.f;
+      Vec<O, W>::store(out + (i0 + u) * ldo + (long long)v * W, Vec<O, W>::pack(f));
     }
   }
 }
 
-// start[v] = first sorted position whose id is >= v, v = 0..V.
-__global__ void __launch_bounds__(ET) starts_kernel(const int2* __restrict__ sorted,
-                                                    const int32_t* __restrict__ live, int V,
-                                                    int32_t* __restrict__ start) {
-  const int n = *live;
-  for (long long v = blockIdx.x * (long long)ET + threadIdx.x; v <= V;
-       v += (long long)gridDim.x * ET) {
-    int lo = 0, hi = n;
-    while (lo < hi) {
-      const int mid = lo + (hi - lo) / 2;
-      if (sorted[mid].x < (int)v) lo = mid + 1;
-      else hi = mid;
-    }
-    start[v] = lo;
+// First of the n sorted positions whose id is >= v.
+__device__ __forceinline__ int first_at(const int2* __restrict__ sorted, int n, int v) {
+  int lo = 0, hi = n;
+  while (lo < hi) {
+    const int mid = lo + (hi - lo) / 2;
+    if (sorted[mid].x < v) lo = mid + 1;
+    else hi = mid;
   }
+  return lo;
 }
 
 // acc += dout rows of sorted[lo..hi), in order.
@@ -93,40 +90,48 @@ __device__ __forceinline__ void add_rows(const int2* __restrict__ sorted, int lo
   }
 }
 
-// partial[k] = sum of piece k, for the pieces inside one row.
-template <typename T, int W, int G>
+// partial[k] = sum of piece k, for the pieces inside one row.  There are few
+// pieces, so a warp takes 32 accesses of a row, not a group the whole row.
+template <typename T, int W>
 __global__ void __launch_bounds__(ET) pieces_kernel(const int2* __restrict__ sorted,
                                                     const int32_t* __restrict__ live,
                                                     const T* __restrict__ dout, long long ldd,
-                                                    int d, float* __restrict__ partial) {
-  constexpr int NG = ET / G;
-  const int grp = threadIdx.x / G, gt = threadIdx.x % G;
-  const int nv = d / W;
+                                                    int d, int cols, float* __restrict__ partial) {
+  const int lane = threadIdx.x & 31;
   const int pieces = *live / kPiece;
-  for (int k = blockIdx.x * NG + grp; k < pieces; k += gridDim.x * NG) {
-    const int lo = k * kPiece;
-    if (sorted[lo].x != sorted[lo + kPiece - 1].x) continue;
-    for (int v = gt; v < nv; v += G) {
-      float acc[W];
+  const long long unit = (long long)blockIdx.x * (ET / 32) + threadIdx.x / 32;
+  const int k = (int)(unit / cols), v = (int)(unit % cols) * 32 + lane;
+  if (k >= pieces) return;
+  const int lo = k * kPiece;
+  if (sorted[lo].x != sorted[lo + kPiece - 1].x || v >= d / W) return;
+  float acc[W];
 #pragma unroll
-      for (int j = 0; j < W; ++j) acc[j] = 0.f;
-      add_rows<T, W>(sorted, lo, lo + kPiece, dout, ldd, v, acc);
-#pragma unroll
-      for (int j = 0; j < W; ++j) partial[(long long)k * d + v * W + j] = acc[j];
-    }
-  }
+  for (int j = 0; j < W; ++j) acc[j] = 0.f;
+  add_rows<T, W>(sorted, lo, lo + kPiece, dout, ldd, v, acc);
+  Vec<float, W>::store(partial + (long long)k * d + (long long)v * W, Vec<float, W>::pack(acc));
 }
+
+// A group of G threads owns kOwn neighbouring rows of the table.
+constexpr int kOwn = 8;
 
 template <typename T, typename O, int W, int G, bool ADD>
 __global__ void __launch_bounds__(ET) table_rows_kernel(
-    const int2* __restrict__ sorted, const int32_t* __restrict__ start,
+    const int2* __restrict__ sorted, const int32_t* __restrict__ live,
     const T* __restrict__ dout, long long ldd, const float* __restrict__ partial, int V, int d,
     float scale, O* __restrict__ dtable, long long ldt) {
   constexpr int NG = ET / G;
+  __shared__ int start_s[NG][kOwn + 1];
   const int grp = threadIdx.x / G, gt = threadIdx.x % G;
   const int nv = d / W;
-  for (long long r = (long long)blockIdx.x * NG + grp; r < V; r += (long long)gridDim.x * NG) {
-    const int lo = start[r], hi = start[r + 1];
+  const long long r0 = ((long long)blockIdx.x * NG + grp) * kOwn;
+  if (gt <= kOwn)
+    start_s[grp][gt] = first_at(sorted, *live, (int)min((long long)V, r0 + gt));
+  if (G == 32) __syncwarp();
+  else __syncthreads();
+  for (int k = 0; k < kOwn; ++k) {
+    const long long r = r0 + k;
+    if (r >= V) return;
+    const int lo = start_s[grp][k], hi = start_s[grp][k + 1];
     if (ADD && lo == hi) continue;
     const int p0 = (lo + kPiece - 1) / kPiece, p1 = hi / kPiece;   // whole pieces in the row
     const int head = p0 < p1 ? p0 * kPiece : hi;
@@ -135,9 +140,12 @@ __global__ void __launch_bounds__(ET) table_rows_kernel(
 #pragma unroll
       for (int j = 0; j < W; ++j) acc[j] = 0.f;
       add_rows<T, W>(sorted, lo, head, dout, ldd, v, acc);
-      for (int p = p0; p < p1; ++p)
+      for (int p = p0; p < p1; ++p) {
+        float part[W];
+        Vec<float, W>::unpack(Vec<float, W>::load(partial + (long long)p * d + (long long)v * W), part);
 #pragma unroll
-        for (int j = 0; j < W; ++j) acc[j] += partial[(long long)p * d + v * W + j];
+        for (int j = 0; j < W; ++j) acc[j] += part[j];
+      }
       if (p0 < p1) add_rows<T, W>(sorted, p1 * kPiece, hi, dout, ldd, v, acc);
       O* dst = dtable + r * ldt + (long long)v * W;
 #pragma unroll
@@ -153,11 +161,11 @@ __global__ void __launch_bounds__(ET) table_rows_kernel(
   }
 }
 
-int grid_for(long long units) { return (int)(units < 152 * 8 ? units : 152 * 8); }
+int blocks_for(long long units, int per_block) { return (int)((units + per_block - 1) / per_block); }
 
 template <typename T, typename O, int W, int G>
 cudaError_t embed_t(const EmbedArgs& a, cudaStream_t s) {
-  const int blocks = grid_for((a.n + ET / G - 1) / (ET / G));
+  const int blocks = blocks_for(a.n, ET / G * kRows);
   if (a.ids_bytes == 8)
     embed_kernel<T, O, W, G, int64_t><<<blocks, ET, 0, s>>>(
         (const int64_t*)a.ids, a.n, (const T*)a.in.p, a.in.ld, a.V, a.d, a.scale, (O*)a.out.p,
@@ -178,26 +186,24 @@ cudaError_t table_t(const EmbedArgs& a, void* ws, int* err, cudaStream_t s) {
   int2* scratch = reinterpret_cast<int2*>(p);
   int2* sorted = reinterpret_cast<int2*>(p + sort_bytes(a.n));
   int32_t* live = reinterpret_cast<int32_t*>(p + 2 * sort_bytes(a.n));
-  int32_t* start = live + 64;
-  float* partial = reinterpret_cast<float*>(p + 2 * sort_bytes(a.n) +
-                                            align_up(sizeof(int32_t) * (64 + (size_t)a.V + 1), 256));
+  float* partial = reinterpret_cast<float*>(p + 2 * sort_bytes(a.n) + 256);
   cudaError_t e = launch_sort_ids(a.ids, a.ids_bytes, (int)a.n, a.V, scratch, sorted, live, err, s);
   if (e != cudaSuccess) return e;
-  starts_kernel<<<grid_for((a.V + (long long)ET) / ET), ET, 0, s>>>(sorted, live, a.V, start);
-  const int pieces = (int)(a.n / kPiece);
+  const long long pieces = a.n / kPiece;
+  const int cols = blocks_for(a.d / W, 32);
   if (pieces > 0)
-    pieces_kernel<T, W, G><<<grid_for((pieces + ET / G - 1) / (ET / G)), ET, 0, s>>>(
-        sorted, live, (const T*)a.in.p, a.in.ld, a.d, partial);
-  const int blocks = grid_for(((long long)a.V + ET / G - 1) / (ET / G));
+    pieces_kernel<T, W><<<blocks_for(pieces * cols, ET / 32), ET, 0, s>>>(
+        sorted, live, (const T*)a.in.p, a.in.ld, a.d, cols, partial);
+  const int blocks = blocks_for(a.V, ET / G * kOwn);
   if (a.accumulate)
     table_rows_kernel<T, O, W, G, true><<<blocks, ET, 0, s>>>(
-        sorted, start, (const T*)a.in.p, a.in.ld, partial, a.V, a.d, a.scale, (O*)a.out.p,
+        sorted, live, (const T*)a.in.p, a.in.ld, partial, a.V, a.d, a.scale, (O*)a.out.p,
         a.out.ld);
   else
     table_rows_kernel<T, O, W, G, false><<<blocks, ET, 0, s>>>(
-        sorted, start, (const T*)a.in.p, a.in.ld, partial, a.V, a.d, a.scale, (O*)a.out.p,
+        sorted, live, (const T*)a.in.p, a.in.ld, partial, a.V, a.d, a.scale, (O*)a.out.p,
         a.out.ld);
-  count_launches(pieces > 0 ? 3 : 2);
+  count_launches(pieces > 0 ? 2 : 1);
   return cudaGetLastError();
 }
 
@@ -249,9 +255,8 @@ cudaError_t launch_embed(const EmbedArgs& a, cudaStream_t s) {
   return by_type(a, false, nullptr, nullptr, s);
 }
 
-size_t embed_bwd_ws_bytes(long long n, int V, int d) {
-  return 2 * sort_bytes(n) + align_up(sizeof(int32_t) * (64 + (size_t)V + 1), 256) +
-         align_up((size_t)(n / kPiece) * d * sizeof(float), 256);
+size_t embed_bwd_ws_bytes(long long n, int d) {
+  return 2 * sort_bytes(n) + 256 + align_up((size_t)(n / kPiece) * d * sizeof(float), 256);
 }
 
 cudaError_t launch_embed_bwd(const EmbedArgs& a, void* ws, int* err, cudaStream_t s) {

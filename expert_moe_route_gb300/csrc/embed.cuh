@@ -17,7 +17,7 @@ struct EmbedArgs {
   bool accumulate;   // gradient: dtable += instead of =
 };
 cudaError_t launch_embed(const EmbedArgs& a, cudaStream_t s);
-size_t embed_bwd_ws_bytes(long long n, int V, int d);
+size_t embed_bwd_ws_bytes(long long n, int d);
 cudaError_t launch_embed_bwd(const EmbedArgs& a, void* ws, int* err, cudaStream_t s);
 
 }  // namespace moe

@@ -3,7 +3,7 @@
 //
 // Keys are cut into contiguous shares, one per CTA of the cluster, and each
 // share into contiguous ranges, one per warp.  Every warp counts its range's
-// keys into its own row of a shared-memory table [32 warps][bins]; a prefix
+// keys into its own row of a shared-memory table [16 warps][bins]; a prefix
 // over the warps, then over the CTAs (each CTA reads the others' totals through
 // distributed shared memory) and over the bins gives every warp its first
 // position in every bin.  The warps then walk their ranges once more:
@@ -13,8 +13,6 @@
 // One launch does the whole plan.  Separate histogram, scan and rank launches
 // cost about 2 us each in launch latency; the cluster barrier costs well under
 // one.
-#include <algorithm>
-
 #include "common.cuh"
 #include "kernels.h"
 #include "sort.cuh"
@@ -22,9 +20,10 @@
 namespace moe {
 
 namespace {
-constexpr int ST = 1024;          // threads per CTA
+constexpr int ST = 512;           // threads per CTA
 constexpr int SW = ST / 32;       // warps per CTA
-constexpr int kMaxCluster = 8;
+constexpr int kMaxCluster = 16;   // a cluster of more than 8 CTAs is an opt-in
+constexpr int kBatch = 8;         // groups of 32 keys whose loads are in flight together
 
 __device__ __forceinline__ void cluster_arrive() {
   asm volatile("barrier.cluster.arrive.release;" ::: "memory");
@@ -36,6 +35,12 @@ __device__ __forceinline__ int ld_cluster(const int* local, uint32_t rank) {
   int v;
   asm volatile("ld.shared::cluster.s32 %0, [%1];"
                : "=r"(v) : "r"(mapa_shared(smem_u32(local), rank)) : "memory");
+  return v;
+}
+__device__ __forceinline__ int2 ld_cluster2(const int* local, uint32_t rank) {
+  int2 v;
+  asm volatile("ld.shared::cluster.v2.s32 {%0, %1}, [%2];"
+               : "=r"(v.x), "=r"(v.y) : "r"(mapa_shared(smem_u32(local), rank)) : "memory");
   return v;
 }
 __device__ __forceinline__ uint32_t cluster_size() {
@@ -55,56 +60,61 @@ __device__ __forceinline__ int block_scan(int v, int* warp_sums, int* total) {
   }
   if (lane == 31) warp_sums[wid] = incl;
   __syncthreads();
-  if (wid == 0) {
-    int ws = lane < SW ? warp_sums[lane] : 0;
+  int mine = lane < SW ? warp_sums[lane] : 0;
 #pragma unroll
-    for (int off = 1; off < 32; off <<= 1) {
-      const int o = __shfl_up_sync(kFull, ws, off);
-      if (lane >= off) ws += o;
-    }
-    warp_sums[lane] = ws;
+  for (int off = 1; off < SW; off <<= 1) {
+    const int o = __shfl_up_sync(kFull, mine, off);
+    if (lane >= off) mine += o;
   }
-  __syncthreads();
-  const int before = (wid > 0 ? warp_sums[wid - 1] : 0) + incl - v;
-  *total = warp_sums[SW - 1];
-  __syncthreads();
-  return before;
+  *total = __shfl_sync(kFull, mine, SW - 1);
+  const int before = __shfl_sync(kFull, mine, wid > 0 ? wid - 1 : 0);
+  return (wid > 0 ? before : 0) + incl - v;
 }
 
-// Shared-memory table of one pass over `bins` bins (at most ST).
+// Shared-memory table of one pass over `bins` bins (even, at most 2 ST: thread t
+// owns bins 2 t and 2 t + 1).
 struct Table {
   int* wcnt;    // [SW][bins] counts, then each warp's offset inside the CTA's part of a bin
   int* mine;    // [bins] this CTA's counts (read by the other CTAs)
   int* below;   // [bins] keys of the bin in earlier CTAs
 };
 
-// Counts are in t.wcnt: fills mine and below and returns this thread's bin total
-// over the cluster (threads past `bins` get 0).  The other CTAs' shared memory
-// has been read: a cluster barrier must follow before this CTA leaves or
+// Counts are in t.wcnt: fills mine and below and returns the totals over the
+// cluster of this thread's two bins (0 past `bins`).  The other CTAs' shared
+// memory has been read: a cluster barrier must follow before this CTA leaves or
 // changes `mine`.
-__device__ int cluster_totals(const Table& t, int bins, uint32_t rank, uint32_t nr) {
-  const int b = threadIdx.x;
+__device__ __forceinline__ int2 cluster_totals(const Table& t, int bins, uint32_t rank,
+                                               uint32_t nr) {
+  const int b = threadIdx.x * 2;
   __syncthreads();
   if (b < bins) {
-    int run = 0;
-#pragma unroll 8
+    int2 c[SW];
+#pragma unroll
+    for (int w = 0; w < SW; ++w) c[w] = *reinterpret_cast<const int2*>(t.wcnt + w * bins + b);
+    int2 run = make_int2(0, 0);
+#pragma unroll
     for (int w = 0; w < SW; ++w) {
-      const int c = t.wcnt[w * bins + b];
-      t.wcnt[w * bins + b] = run;
-      run += c;
+      *reinterpret_cast<int2*>(t.wcnt + w * bins + b) = run;
+      run.x += c[w].x;
+      run.y += c[w].y;
     }
-    t.mine[b] = run;
+    *reinterpret_cast<int2*>(t.mine + b) = run;
   }
   cluster_arrive();
   cluster_wait();
-  int total = 0, before = 0;
+  int2 total = make_int2(0, 0), before = make_int2(0, 0);
   if (b < bins) {
+#pragma unroll 4
     for (uint32_t r = 0; r < nr; ++r) {
-      const int c = ld_cluster(t.mine + b, r);
-      if (r < rank) before += c;
-      total += c;
+      const int2 c = ld_cluster2(t.mine + b, r);
+      if (r < rank) {
+        before.x += c.x;
+        before.y += c.y;
+      }
+      total.x += c.x;
+      total.y += c.y;
     }
-    t.below[b] = before;
+    *reinterpret_cast<int2*>(t.below + b) = before;
   }
   return total;
 }
@@ -131,62 +141,82 @@ __global__ void __launch_bounds__(ST) sort_slots_kernel(
   __shared__ int warp_sums[32];
   __shared__ int bad_s;
   const uint32_t rank = cluster_rank(), nr = cluster_size();
-  Table t{sm, sm + SW * E, sm + SW * E + E};
-  int* kept_s = sm + SW * E + 2 * E;   // [E]
-  int* off_s = kept_s + E;             // [E]
+  const int bins = (E + 1) & ~1;
+  Table t{sm, sm + SW * bins, sm + SW * bins + bins};
+  int* kept_s = sm + SW * bins + 2 * bins;   // [bins]
+  int* off_s = kept_s + bins;                // [bins]
   const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
   if (tid == 0) bad_s = 0;
-  for (int i = tid; i < SW * E; i += ST) t.wcnt[i] = 0;
+  for (int i = tid; i < SW * bins; i += ST) t.wcnt[i] = 0;
   __syncthreads();
-  const long long c0 = (long long)rank * share;
   const int per_warp = share / SW;
-  const long long w0 = c0 + (long long)wid * per_warp;
+  const long long w0 = (long long)rank * share + (long long)wid * per_warp;
   const long long w1 = min((long long)n, w0 + per_warp);
-  int* my = t.wcnt + wid * E;
+  int* my = t.wcnt + wid * bins;
+  auto load = [&](long long g, int* e) {
+#pragma unroll
+    for (int j = 0; j < kBatch; ++j) {
+      const long long i = g + 32 * j + lane;
+      e[j] = i < w1 ? __ldg(idx + i) : -1;
+    }
+  };
   bool bad = false;
-  for (long long g = w0; g < w1; g += 32) {
-    const long long i = g + lane;
-    if (i < w1) {
-      const int e = idx[i];
-      if ((unsigned)e < (unsigned)E) atomicAdd(&my[e], 1);
-      else bad |= e != -1;
+  for (long long g = w0; g < w1; g += 32 * kBatch) {
+    int e[kBatch];
+    load(g, e);
+#pragma unroll
+    for (int j = 0; j < kBatch; ++j) {
+      if ((unsigned)e[j] < (unsigned)E) atomicAdd(&my[e[j]], 1);
+      else bad |= e[j] != -1;
     }
   }
   if (bad) atomicOr(&bad_s, 1);
-  const int total = cluster_totals(t, E, rank, nr);
+  const int2 total = cluster_totals(t, bins, rank, nr);
   if (rank == 0 && tid == 0) {
     int any = 0;
     for (uint32_t r = 0; r < nr; ++r) any |= ld_cluster(&bad_s, r);
     *err = any ? kErrBadRouting : 0;
   }
   cluster_arrive();
-  const int kept = capacity > 0 ? min(total, capacity) : total;
-  const int padded = (kept + align - 1) / align * align;
+  const int b = tid * 2;
+  int2 kept, padded;
+  kept.x = capacity > 0 ? min(total.x, capacity) : total.x;
+  kept.y = capacity > 0 ? min(total.y, capacity) : total.y;
+  padded.x = (kept.x + align - 1) / align * align;
+  padded.y = (kept.y + align - 1) / align * align;
   int end;
-  const int off = block_scan(tid < E ? padded : 0, warp_sums, &end);
-  if (tid < E) {
-    kept_s[tid] = kept;
-    off_s[tid] = off;
+  const int off = block_scan(padded.x + padded.y, warp_sums, &end);
+  if (b < bins) {
+    *reinterpret_cast<int2*>(kept_s + b) = kept;
+    *reinterpret_cast<int2*>(off_s + b) = make_int2(off, off + padded.x);
     if (rank == 0) {
-      counts[tid] = kept;
-      offsets[tid] = off;
+      counts[b] = kept.x;
+      offsets[b] = off;
+      if (b + 1 < E) {
+        counts[b + 1] = kept.y;
+        offsets[b + 1] = off + padded.x;
+      }
     }
   }
   if (rank == 0 && tid == 0) offsets[E] = end;
   __syncthreads();
-  for (long long g = w0; g < w1; g += 32) {
-    const long long i = g + lane;
-    int e = i < w1 ? idx[i] : -1;
-    if ((unsigned)e >= (unsigned)E) e = -1;
-    const int pos = warp_rank(e, my);
-    if (i >= w1) continue;
-    int row = -1;
-    if (e >= 0) {
-      const int p = t.below[e] + pos;
-      if (p < kept_s[e]) row = off_s[e] + p;
+  for (long long g = w0; g < w1; g += 32 * kBatch) {
+    int e[kBatch];
+    load(g, e);
+#pragma unroll
+    for (int j = 0; j < kBatch; ++j) {
+      const long long i = g + 32 * j + lane;
+      if (g + 32 * j >= w1) break;       // the same for the whole warp
+      if ((unsigned)e[j] >= (unsigned)E) e[j] = -1;
+      const int pos = warp_rank(e[j], my);
+      int row = -1;
+      if (e[j] >= 0) {
+        const int p = t.below[e[j]] + pos;
+        if (p < kept_s[e[j]]) row = off_s[e[j]] + p;
+      }
+      if (i < w1) slot_row[i] = row;
+      if (row >= 0) row_slot[row] = (int)i;
     }
-    slot_row[i] = row;
-    if (row >= 0) row_slot[row] = (int)i;
   }
   // rows without a slot: the ends of the segments, and what follows the last one
   for (int e = (int)rank * SW + wid; e < E; e += (int)nr * SW) {
@@ -224,22 +254,36 @@ __global__ void __launch_bounds__(ST) sort_ids_kernel(
     const long long w0 = ((long long)rank * SW + wid) * per_warp;
     const long long w1 = min((long long)count, w0 + per_warp);
     int* my = t.wcnt + wid * bins;
-    for (long long i = w0 + lane; i < w1; i += 32) {
-      int key;
-      if (p == 0) {
-        const I id = ids[i];
-        if (id >= (I)V) bad = true;
-        key = id >= 0 && id < (I)V ? (int)id : -1;
-      } else {
-        key = __ldcg(&src[i]).x;
+    auto load = [&](long long g, int2* kv) {   // (id, position); id -1: none
+#pragma unroll
+      for (int j = 0; j < kBatch; ++j) {
+        const long long i = g + 32 * j + lane;
+        kv[j] = make_int2(-1, (int)i);
+        if (i >= w1) continue;
+        if (p == 0) {
+          const I id = ids[i];
+          if (id >= (I)V) bad = true;
+          else if (id >= 0) kv[j].x = (int)id;
+        } else {
+          kv[j] = __ldcg(&src[i]);
+        }
       }
-      if (key >= 0) atomicAdd(&my[(key >> shift) & (bins - 1)], 1);
+    };
+    for (long long g = w0; g < w1; g += 32 * kBatch) {
+      int2 kv[kBatch];
+      load(g, kv);
+#pragma unroll
+      for (int j = 0; j < kBatch; ++j)
+        if (kv[j].x >= 0) atomicAdd(&my[(kv[j].x >> shift) & (bins - 1)], 1);
     }
     if (p == 0 && bad) atomicOr(&bad_s, 1);
-    const int total = cluster_totals(t, bins, rank, nr);
+    const int2 total = cluster_totals(t, bins, rank, nr);
     int live;
-    const int off = block_scan(tid < bins ? total : 0, warp_sums, &live);
-    if (tid < bins) off_s[tid] = off + t.below[tid];
+    const int off = block_scan(total.x + total.y, warp_sums, &live);
+    if (tid * 2 < bins) {
+      off_s[tid * 2] = off + t.below[tid * 2];
+      off_s[tid * 2 + 1] = off + total.x + t.below[tid * 2 + 1];
+    }
     if (p == 0 && rank == 0 && tid == 0) {
       int any = 0;
       for (uint32_t r = 0; r < nr; ++r) any |= ld_cluster(&bad_s, r);
@@ -247,20 +291,16 @@ __global__ void __launch_bounds__(ST) sort_ids_kernel(
       *live_out = live;
     }
     __syncthreads();
-    for (long long g = w0; g < w1; g += 32) {
-      const long long i = g + lane;
-      int2 kv = make_int2(-1, (int)i);
-      if (i < w1) {
-        if (p == 0) {
-          const I id = ids[i];
-          if (id >= 0 && id < (I)V) kv.x = (int)id;
-        } else {
-          kv = __ldcg(&src[i]);
-        }
+    for (long long g = w0; g < w1; g += 32 * kBatch) {
+      int2 kv[kBatch];
+      load(g, kv);
+#pragma unroll
+      for (int j = 0; j < kBatch; ++j) {
+        if (g + 32 * j >= w1) break;     // the same for the whole warp
+        const int bin = kv[j].x >= 0 ? (kv[j].x >> shift) & (bins - 1) : -1;
+        const int pos = warp_rank(bin, my);
+        if (bin >= 0) __stcg(&dst[off_s[bin] + pos], kv[j]);
       }
-      const int bin = kv.x >= 0 ? (kv.x >> shift) & (bins - 1) : -1;
-      const int pos = warp_rank(bin, my);
-      if (bin >= 0) __stcg(&dst[off_s[bin] + pos], kv);
     }
     count = live;
     cluster_arrive();   // the totals are read, this pass's pairs written
@@ -268,25 +308,40 @@ __global__ void __launch_bounds__(ST) sort_ids_kernel(
   }
 }
 
+int g_max_cluster[64];   // per device: CTAs a cluster of these kernels may have
+
+int max_cluster() {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 8;
+  return g_max_cluster[dev] > 0 ? g_max_cluster[dev] : 8;
+}
+
+// Two keys a thread before the cluster grows.
 int cluster_for(long long n) {
+  const int most = max_cluster();
   int c = 1;
-  while (c < kMaxCluster && n > (long long)c * 4 * ST) c *= 2;
+  while (c < most && n > (long long)c * 2 * ST) c *= 2;
   return c;
 }
 
-cudaError_t launch_cluster(const void* f, int ctas, size_t smem, void** args, cudaStream_t s) {
+cudaLaunchConfig_t cluster_config(int ctas, size_t smem, cudaLaunchAttribute* at, cudaStream_t s) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(ctas);
   cfg.blockDim = dim3(ST);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
-  cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeClusterDimension;
   at[0].val.clusterDim.x = ctas;
   at[0].val.clusterDim.y = 1;
   at[0].val.clusterDim.z = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
+  return cfg;
+}
+
+cudaError_t launch_cluster(const void* f, int ctas, size_t smem, void** args, cudaStream_t s) {
+  cudaLaunchAttribute at[1];
+  const cudaLaunchConfig_t cfg = cluster_config(ctas, smem, at, s);
   const cudaError_t e = cudaLaunchKernelExC(&cfg, f, args);
   count_launches(1);
   return e != cudaSuccess ? e : cudaGetLastError();
@@ -295,16 +350,27 @@ cudaError_t launch_cluster(const void* f, int ctas, size_t smem, void** args, cu
 size_t table_bytes(int bins, int extra) { return sizeof(int) * (size_t)bins * (SW + 2 + extra); }
 }  // namespace
 
-cudaError_t sort_set_smem_limits() {
+cudaError_t sort_set_limits() {
   const int most = (int)table_bytes(1024, 2);
-  cudaError_t e = cudaFuncSetAttribute((const void*)sort_slots_kernel,
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize, most);
-  if (e == cudaSuccess)
-    e = cudaFuncSetAttribute((const void*)sort_ids_kernel<int32_t>,
-                             cudaFuncAttributeMaxDynamicSharedMemorySize, most);
-  if (e == cudaSuccess)
-    e = cudaFuncSetAttribute((const void*)sort_ids_kernel<int64_t>,
-                             cudaFuncAttributeMaxDynamicSharedMemorySize, most);
+  bool wide = true;
+  for (const void* f : {(const void*)sort_slots_kernel, (const void*)sort_ids_kernel<int32_t>,
+                        (const void*)sort_ids_kernel<int64_t>}) {
+    cudaError_t e =
+        cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
+    if (e != cudaSuccess) return e;
+    e = cudaFuncSetAttribute(f, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (e != cudaSuccess) return e;
+    cudaLaunchAttribute at[1];
+    const cudaLaunchConfig_t cfg = cluster_config(kMaxCluster, most, at, nullptr);
+    int fit = 0;
+    if (cudaOccupancyMaxActiveClusters(&fit, f, &cfg) != cudaSuccess || fit < 1) {
+      (void)cudaGetLastError();
+      wide = false;
+    }
+  }
+  int dev = 0;
+  const cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess && dev >= 0 && dev < 64) g_max_cluster[dev] = wide ? kMaxCluster : 8;
   return e;
 }
 
@@ -315,7 +381,8 @@ cudaError_t launch_sort_slots(const int32_t* idx, int n, int E, int align, int c
   int share = (int)((((long long)n + ctas - 1) / ctas + ST - 1) / ST * ST);
   void* args[] = {&idx, &n, &share, &E, &align, &capacity, &N, &counts, &offsets, &row_slot,
                   &slot_row, &err};
-  return launch_cluster((const void*)sort_slots_kernel, ctas, table_bytes(E, 2), args, s);
+  return launch_cluster((const void*)sort_slots_kernel, ctas, table_bytes((E + 1) & ~1, 2), args,
+                        s);
 }
 
 cudaError_t launch_sort_ids(const void* ids, int ids_bytes, int n, int V, int2* scratch,

@@ -6,7 +6,8 @@
 
 namespace moe {
 
-cudaError_t sort_set_smem_limits();
+// Per-device set-up (shared memory, cluster size) before the first launch.
+cudaError_t sort_set_limits();
 // The plan of moe_sort; writes every entry of counts, offsets, row_slot [N],
 // slot_row [n] and the error word.
 cudaError_t launch_sort_slots(const int32_t* idx, int n, int E, int align, int capacity, int N,

@@ -30,7 +30,7 @@ cudaError_t init_sort() {
   if (e != cudaSuccess) return e;
   if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
   if (!done[dev]) {
-    e = sort_set_smem_limits();
+    e = sort_set_limits();
     if (e != cudaSuccess) return e;
     done[dev] = 1;
   }
@@ -223,7 +223,7 @@ moe_status_t moe_embed_bwd(const void* dout, long long ld_dout, const void* ids,
   if (n >= (1LL << 30) || V > (1 << 30) || n * d >= (1LL << 40) || (long long)V * d >= (1LL << 40))
     return MOE_ERR_UNSUPPORTED;
   if (!ws_bytes) return MOE_ERR_INVALID_ARG;
-  const size_t need = kErrBytes + embed_bwd_ws_bytes(n, V, d);
+  const size_t need = kErrBytes + embed_bwd_ws_bytes(n, d);
   if (!ws) {
     *ws_bytes = need;
     return MOE_OK;
