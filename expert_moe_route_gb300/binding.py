@@ -196,7 +196,13 @@ def _p(t):
     return t.data_ptr()
 
 
+# the current stream's handle without a Stream object around it (2 us a call less)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(stream):
+    if stream is None and _raw_stream is not None:
+        return _raw_stream(torch.cuda.current_device())
     s = stream if stream is not None else torch.cuda.current_stream()
     return s.cuda_stream
 

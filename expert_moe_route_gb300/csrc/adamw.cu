@@ -5,8 +5,8 @@
 //
 // The tensors' pointers travel as a kernel parameter, so a call needs no device
 // copy of its list and can be captured in a graph; a list longer than one
-// parameter holds becomes several launches.  Work is cut into chunks of 2048
-// elements, eight blocks of 256, one per warp; a persistent grid walks them.
+// parameter holds becomes several launches.  Work is cut into blocks of 256
+// elements, `run` consecutive ones a warp, eight warps a chunk, a CTA per chunk.
 //
 // 8-bit states.  Each block of 256 elements keeps one fp32 scale and E4M3 codes:
 // m as code * m_scale, v through its root, sqrt(v) as code * v_scale (the root
@@ -23,6 +23,8 @@
 // 8-bit ones.
 #include <math.h>
 
+#include <algorithm>
+
 #include "adamw.cuh"
 #include "kernels.h"
 #include "rows.cuh"
@@ -32,10 +34,11 @@ namespace moe {
 namespace {
 constexpr int AT = 256;
 constexpr int kBlock = 256;                  // elements per scale, one warp's share
-constexpr int kChunk = kBlock * (AT / 32);   // elements per CTA pass
+constexpr int kRow = kBlock * (AT / 32);     // a block for each warp
 constexpr int kPerLaunch = 256;              // tensors in one launch's parameter
-constexpr int kNormBlocks = 152 * 8;
-
+constexpr int kNormBlocks = 152 * 32;        // partial sums of a launch
+constexpr int kNormThreads = 1024;
+constexpr int kMostRun = 8, kRun32 = 2, kNormRun = 4;   // blocks a warp takes at most
 // Bits of AdamEntry::kind.
 constexpr int kP16 = 1, kG16 = 2, kWide = 4;
 
@@ -55,7 +58,7 @@ struct AdamEntry {
 };
 struct AdamTable {
   AdamEntry e[kPerLaunch];
-  int count, chunks;
+  int count, chunks, run;       // a chunk: run blocks a warp
   float b1, b2, c1, c2;         // beta1, beta2, 1 - beta1, 1 - beta2
   float step_size, root, eps;   // lr / (1 - beta1^t), 1 / sqrt(1 - beta2^t)
   const float* norm;            // {norm, coef, finite, -} or null
@@ -68,7 +71,7 @@ struct NormEntry {
 };
 struct NormTable {
   NormEntry e[kPerLaunch];
-  int count, chunks;
+  int count, chunks, run;
 };
 
 template <typename Table>
@@ -81,6 +84,25 @@ __device__ __forceinline__ int entry_of(const Table& t, int chunk) {
   }
   return lo;
 }
+
+// A warp's walk over its runs of blocks.
+struct Walk {
+  int c, k = 0, end = 0;       // chunk, its tensor, the tensor's first chunk past it
+  long long base;              // first element of the run
+  int left;                    // its elements; <= 0: none
+  template <typename Table>
+  __device__ __forceinline__ bool at(const Table& t) {   // settles c; false past the end
+    if (c >= t.chunks) return false;
+    if (c >= end) {
+      k = entry_of(t, c);
+      end = k + 1 < t.count ? t.e[k + 1].first : t.chunks;
+    }
+    const auto& e = t.e[k];
+    base = (long long)(c - e.first) * (kRow * t.run) + (threadIdx.x >> 5) * (kBlock * t.run);
+    left = (int)min((long long)(kBlock * t.run), e.n - base);
+    return true;
+  }
+};
 
 // A 32-bit hash: two rounds of xor-shift and multiplication by an odd number
 // (the fractions of the square roots of 2 and 3).
@@ -230,12 +252,87 @@ __device__ __forceinline__ void values8(const uint2& c, float* f) {
 
 __device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
 
-// One block of up to 256 elements of one tensor, one warp.  The arithmetic goes
-// in pairs (two fp32 products, sums or fused products an instruction): with
-// 8-bit states the instructions, not the bytes, are what a plain form runs out of.
+// The step's factors as pairs.  The arithmetic goes two elements an instruction:
+// with 8-bit states the instructions, not the bytes, are what a plain form runs
+// out of.
+struct Factors {
+  float2 b1, b2, c1, c2, root, eps, step, decay;   // c1, c2 with the gradients' factor
+  __device__ __forceinline__ Factors(const AdamTable& t, const AdamEntry& e, float coef)
+      : b1(both(t.b1)), b2(both(t.b2)), c1(both(coef * t.c1)), c2(both(coef * coef * t.c2)),
+        root(both(t.root)), eps(both(t.eps)), step(both(-t.step_size)), decay(both(e.decay)) {}
+};
+
+// Eight elements' step.  S8: m and v come as code values and are scaled by ms
+// and vs (v the root's), and u gets sqrt(v).
+template <bool S8>
+__device__ __forceinline__ void step8(const Factors& f, const float* g, float* p, float* m,
+                                      float* v, float* u, float ms, float vs) {
+  const float2 mb = S8 ? both(ms * f.b1.x) : f.b1, qs = both(vs);
+#pragma unroll
+  for (int j = 0; j < 8; j += 2) {
+    const float2 gj = make_float2(g[j], g[j + 1]);
+    const float2 mj = __ffma2_rn(gj, f.c1, __fmul2_rn(make_float2(m[j], m[j + 1]), mb));
+    const float2 sq = __fmul2_rn(gj, __fmul2_rn(gj, f.c2));
+    float2 vj = make_float2(v[j], v[j + 1]);
+    if (S8) {
+      const float2 q = __fmul2_rn(vj, qs);
+      vj = __ffma2_rn(q, __fmul2_rn(q, f.b2), sq);
+    } else {
+      vj = __ffma2_rn(vj, f.b2, sq);
+    }
+    const float2 uj = make_float2(root_of(vj.x), root_of(vj.y));
+    const float2 den = __ffma2_rn(uj, f.root, f.eps);
+    const float2 ratio = __fmul2_rn(mj, make_float2(reciprocal(den.x), reciprocal(den.y)));
+    const float2 pj = __ffma2_rn(ratio, f.step, __fmul2_rn(make_float2(p[j], p[j + 1]), f.decay));
+    p[j] = pj.x, p[j + 1] = pj.y;
+    m[j] = mj.x, m[j + 1] = mj.y;
+    v[j] = vj.x, v[j + 1] = vj.y;
+    u[j] = uj.x, u[j + 1] = uj.y;
+  }
+}
+
+// Codes of eight elements of each state, given the block's scales.
+__device__ __forceinline__ void encode8(const float* m, const float* u, float im, float iu,
+                                        const uint32_t* d, uint2* mc, uint2* vc) {
+  uint32_t wm[8], wu[8];
+  const float2 to = both(kToCode);
+#pragma unroll
+  for (int j = 0; j < 8; j += 2) {
+    const float2 rm = __fmul2_rn(__fmul2_rn(make_float2(m[j], m[j + 1]), both(im)), to);
+    const float2 ru = __fmul2_rn(__fmul2_rn(make_float2(u[j], u[j + 1]), both(iu)), to);
+    wm[j] = code_top(rm.x, d[j]) | (__float_as_uint(rm.x) & 0x80000000u);
+    wm[j + 1] = code_top(rm.y, d[j + 1]) | (__float_as_uint(rm.y) & 0x80000000u);
+    wu[j] = max(code_top(ru.x, d[j]), ru.x > 0.f ? 1u << 24 : 0u);
+    wu[j + 1] = max(code_top(ru.y, d[j + 1]), ru.y > 0.f ? 1u << 24 : 0u);
+  }
+  *mc = make_uint2(top_bytes(wm), top_bytes(wm + 4));
+  *vc = make_uint2(top_bytes(wu), top_bytes(wu + 4));
+}
+
+// A block's new scales from its largest values, and their reciprocals (0 for a
+// block of zeros).
+struct Scales {
+  float m, v, im, iu;
+  __device__ __forceinline__ Scales(const float* mj, const float* uj) {
+    float am = 0.f, au = 0.f;
+#pragma unroll
+    for (int j = 0; j < 8; j += 2) {
+      am = fmaxf(fmaxf(am, fabsf(mj[j])), fabsf(mj[j + 1]));
+      au = fmaxf(fmaxf(au, uj[j]), uj[j + 1]);
+    }
+    m = warp_max(am) / 448.f;
+    v = warp_max(au) / 448.f;
+    im = m >= 0x1p-126f ? 1.f / m : 0.f;
+    iu = v >= 0x1p-126f ? 1.f / v : 0.f;
+    if (im == 0.f) m = 0.f;
+    if (iu == 0.f) v = 0.f;
+  }
+};
+
+// One block of up to 256 elements of one tensor, one warp.
 template <bool S8, bool WIDE>
-__device__ __forceinline__ void step_block(const AdamEntry& e, const AdamTable& t, long long base,
-                                           int left, float coef) {
+__device__ __forceinline__ void step_block(const AdamEntry& e, const Factors& f, long long base,
+                                           int left) {
   Lane<WIDE> l;
   l.lane = threadIdx.x & 31;
   l.left = left;
@@ -245,12 +342,10 @@ __device__ __forceinline__ void step_block(const AdamEntry& e, const AdamTable& 
   if (e.kind & kG16) l.get((const uint16_t*)e.g + base, g);
   else l.get((const float*)e.g + base, g);
   if (S8) {
-    const uint2 mc = l.get((const uint8_t*)e.m + base);
-    const uint2 vc = l.get((const uint8_t*)e.v + base);
+    values8(l.get((const uint8_t*)e.m + base), m);
+    values8(l.get((const uint8_t*)e.v + base), v);
     ms = e.m_scale[blk];
     vs = e.v_scale[blk];
-    values8(mc, m);
-    values8(vc, v);
   } else {
     l.get((const float*)e.m + base, m);
     l.get((const float*)e.v + base, v);
@@ -258,37 +353,7 @@ __device__ __forceinline__ void step_block(const AdamEntry& e, const AdamTable& 
   if (e.master) l.get(e.master + base, p);
   else if (e.kind & kP16) l.get((const uint16_t*)e.p + base, p);
   else l.get((const float*)e.p + base, p);
-  const float2 mb = both(ms * t.b1), gm = both(coef * t.c1), k = both(coef);
-  const float2 b2 = both(t.b2), c2 = both(t.c2), qs = both(vs);
-  const float2 root = both(t.root), eps = both(t.eps), decay = both(e.decay),
-               step = both(-t.step_size);
-  float am = 0.f, au = 0.f;
-#pragma unroll
-  for (int j = 0; j < 8; j += 2) {
-    const float2 gj = make_float2(g[j], g[j + 1]);
-    const float2 mj = __ffma2_rn(gj, gm, __fmul2_rn(make_float2(m[j], m[j + 1]), mb));
-    const float2 gc = __fmul2_rn(gj, k);
-    const float2 sq = __fmul2_rn(gc, __fmul2_rn(gc, c2));
-    float2 vj = make_float2(v[j], v[j + 1]);
-    if (S8) {
-      const float2 q = __fmul2_rn(vj, qs);
-      vj = __ffma2_rn(q, __fmul2_rn(q, b2), sq);
-    } else {
-      vj = __ffma2_rn(vj, b2, sq);
-    }
-    const float2 uj = make_float2(root_of(vj.x), root_of(vj.y));
-    const float2 den = __ffma2_rn(uj, root, eps);
-    const float2 ratio = __fmul2_rn(mj, make_float2(reciprocal(den.x), reciprocal(den.y)));
-    const float2 pj = __ffma2_rn(ratio, step, __fmul2_rn(make_float2(p[j], p[j + 1]), decay));
-    p[j] = pj.x, p[j + 1] = pj.y;
-    m[j] = mj.x, m[j + 1] = mj.y;
-    v[j] = vj.x, v[j + 1] = vj.y;
-    u[j] = uj.x, u[j + 1] = uj.y;
-    if (S8) {
-      am = fmaxf(fmaxf(am, fabsf(mj.x)), fabsf(mj.y));
-      au = fmaxf(fmaxf(au, uj.x), uj.y);
-    }
-  }
+  step8<S8>(f, g, p, m, v, u, ms, vs);
   if (e.master) l.put(e.master + base, p);
   if (e.kind & kP16) l.put((uint16_t*)e.p + base, p);
   else l.put((float*)e.p + base, p);
@@ -297,60 +362,202 @@ __device__ __forceinline__ void step_block(const AdamEntry& e, const AdamTable& 
     l.put((float*)e.v + base, v);
     return;
   }
-  // elements past the end hold zeros: they do not touch the maxima
-  ms = warp_max(am) / 448.f;
-  vs = warp_max(au) / 448.f;
-  const float im = ms >= 0x1p-126f ? 1.f / ms : 0.f;
-  const float iu = vs >= 0x1p-126f ? 1.f / vs : 0.f;
-  if (l.lane == 0) {
-    e.m_scale[blk] = im > 0.f ? ms : 0.f;
-    e.v_scale[blk] = iu > 0.f ? vs : 0.f;
-  }
-  uint32_t d[8], wm[8], wu[8];
+  const Scales s(m, u);   // elements past the end hold zeros: they do not touch the maxima
+  uint32_t d[8];
+  uint2 mc, vc;
   l.dithers(base, e.place, d);
-#pragma unroll
-  for (int j = 0; j < 8; j += 2) {
-    const float2 to = both(kToCode);
-    const float2 rm = __fmul2_rn(__fmul2_rn(make_float2(m[j], m[j + 1]), both(im)), to);
-    const float2 ru = __fmul2_rn(__fmul2_rn(make_float2(u[j], u[j + 1]), both(iu)), to);
-    wm[j] = code_top(rm.x, d[j]) | (__float_as_uint(rm.x) & 0x80000000u);
-    wm[j + 1] = code_top(rm.y, d[j + 1]) | (__float_as_uint(rm.y) & 0x80000000u);
-    wu[j] = max(code_top(ru.x, d[j]), ru.x > 0.f ? 1u << 24 : 0u);
-    wu[j + 1] = max(code_top(ru.y, d[j + 1]), ru.y > 0.f ? 1u << 24 : 0u);
+  encode8(m, u, s.im, s.iu, d, &mc, &vc);
+  l.put((uint8_t*)e.m + base, mc);
+  l.put((uint8_t*)e.v + base, vc);
+  if (l.lane == 0) {
+    e.m_scale[blk] = s.m;
+    e.v_scale[blk] = s.v;
   }
-  l.put((uint8_t*)e.m + base, make_uint2(top_bytes(wm), top_bytes(wm + 4)));
-  l.put((uint8_t*)e.v + base, make_uint2(top_bytes(wu), top_bytes(wu + 4)));
+}
+
+// A run of whole aligned blocks with 8-bit states, no branch in its loop.  Lane
+// b of the first 32 gets the new scale of m of block b in *sm, that of v in *sv.
+template <bool G16, bool P16, bool MASTER>
+__device__ __forceinline__ void step_run8(const AdamEntry& e, const Factors& f, long long base,
+                                          int run, float* sm, float* sv) {
+  Lane<true> l;
+  l.lane = threadIdx.x & 31;
+  l.left = kBlock;
+  float ms = 0.f, vs = 0.f;        // the blocks' old scales, a lane each
+  if (l.lane < run) {
+    ms = e.m_scale[base / kBlock + l.lane];
+    vs = e.v_scale[base / kBlock + l.lane];
+  }
+#pragma unroll 1
+  for (int b = 0; b < run; ++b, base += kBlock) {
+    float p[8], g[8], m[8], v[8], u[8];
+    if (G16) l.get((const uint16_t*)e.g + base, g);
+    else l.get((const float*)e.g + base, g);
+    const uint2 mc = l.get((const uint8_t*)e.m + base);
+    const uint2 vc = l.get((const uint8_t*)e.v + base);
+    if (MASTER) l.get(e.master + base, p);
+    else if (P16) l.get((const uint16_t*)e.p + base, p);
+    else l.get((const float*)e.p + base, p);
+    values8(mc, m);
+    values8(vc, v);
+    step8<true>(f, g, p, m, v, u, __shfl_sync(kFull, ms, b), __shfl_sync(kFull, vs, b));
+    if (MASTER) l.put(e.master + base, p);
+    if (P16) l.put((uint16_t*)e.p + base, p);
+    else l.put((float*)e.p + base, p);
+    const Scales s(m, u);
+    uint32_t d[8];
+    uint2 mn, vn;
+    l.dithers(base, e.place, d);
+    encode8(m, u, s.im, s.iu, d, &mn, &vn);
+    l.put((uint8_t*)e.m + base, mn);
+    l.put((uint8_t*)e.v + base, vn);
+    if (l.lane == b) {
+      *sm = s.m;
+      *sv = s.v;
+    }
+  }
+}
+
+__device__ __forceinline__ bool clip_of(const AdamTable& t, float* coef) {
+  *coef = 1.f;
+  if (!t.norm) return true;
+  *coef = t.norm[1];
+  return t.norm[2] != 0.f;       // some gradient is not finite: the step is skipped
 }
 
 template <bool S8>
-__global__ void __launch_bounds__(AT) adamw_kernel(const __grid_constant__ AdamTable t) {
-  float coef = 1.f;
-  if (t.norm) {
-    if (t.norm[2] == 0.f) return;      // some gradient is not finite: the step is skipped
-    coef = t.norm[1];
+__device__ __noinline__ void step_ragged(const AdamEntry& e, const AdamTable& t, float coef,
+                                         long long base, int left) {
+  const Factors f(t, e, coef);
+  for (; left > 0; left -= kBlock, base += kBlock)
+    step_block<S8, false>(e, f, base, min(left, kBlock));
+}
+
+// 32-bit states.  254M elements with master copies and bf16 gradients (28 B an
+// element, 7.1 GB): 1.00 ms, 7.05 TB/s (a copy 6.78).  Two blocks a warp in a
+// CTA per chunk; persistent CTAs took 1.06 ms.
+__global__ void __launch_bounds__(AT) adamw32_kernel(const __grid_constant__ AdamTable t) {
+  float coef;
+  Walk w;
+  w.c = blockIdx.x;
+  if (!clip_of(t, &coef) || !w.at(t) || w.left <= 0) return;
+  const AdamEntry& e = t.e[w.k];
+  const Factors f(t, e, coef);
+  if (e.kind & kWide)
+    for (; w.left >= kBlock; w.left -= kBlock, w.base += kBlock)
+      step_block<false, true>(e, f, w.base, kBlock);
+  if (w.left > 0) step_ragged<false>(e, t, coef, w.base, w.left);
+}
+
+// 8-bit states.  553M elements (bf16 p, fp32 g, 6.7 GB): 0.98 ms, 6.8 TB/s.  The
+// new scales of a whole chunk go out as lines from shared memory: written block
+// by block, 4 bytes at a time into lines that other CTAs read and write at the
+// same moment, the kernel took 2.3 ms.  Eight blocks a warp, loads not issued
+// ahead: the other warps of four CTAs cover them (one block ahead in registers,
+// three CTAs: 1.02 ms).
+__global__ void __launch_bounds__(AT, 4) adamw8_kernel(const __grid_constant__ AdamTable t) {
+  __shared__ float scales[2][kMostRun * (AT / 32)];
+  float coef;
+  Walk w;
+  w.c = blockIdx.x;
+  if (!clip_of(t, &coef) || !w.at(t)) return;
+  const AdamEntry& e = t.e[w.k];
+  const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
+  const long long first = (long long)(w.c - e.first) * kRow * t.run;
+  const Factors f(t, e, coef);
+  if (!(e.kind & kWide) || first + kRow * t.run > e.n) {
+    if (e.kind & kWide)
+      for (; w.left >= kBlock; w.left -= kBlock, w.base += kBlock)
+        step_block<true, true>(e, f, w.base, kBlock);
+    if (w.left > 0) step_ragged<true>(e, t, coef, w.base, w.left);
+    return;
   }
-  const int wid = threadIdx.x >> 5;
-  int k = 0, end = 0;                  // the tensor of the last chunk, its first chunk past it
-  for (int c = blockIdx.x; c < t.chunks; c += gridDim.x) {
-    if (c >= end) {
-      k = entry_of(t, c);
-      end = k + 1 < t.count ? t.e[k + 1].first : t.chunks;
-    }
-    const AdamEntry& e = t.e[k];
-    const long long base = (long long)(c - e.first) * kChunk + wid * kBlock;
-    if (base >= e.n) continue;
-    const int left = (int)min((long long)kBlock, e.n - base);
-    if ((e.kind & kWide) && left == kBlock) step_block<S8, true>(e, t, base, left, coef);
-    else step_block<S8, false>(e, t, base, left, coef);
+  float sm = 0.f, sv = 0.f;
+  if (e.kind & kG16) {
+    if (e.master) step_run8<true, true, true>(e, f, w.base, t.run, &sm, &sv);
+    else if (e.kind & kP16) step_run8<true, true, false>(e, f, w.base, t.run, &sm, &sv);
+    else step_run8<true, false, false>(e, f, w.base, t.run, &sm, &sv);
+  } else {
+    if (e.master) step_run8<false, true, true>(e, f, w.base, t.run, &sm, &sv);
+    else if (e.kind & kP16) step_run8<false, true, false>(e, f, w.base, t.run, &sm, &sv);
+    else step_run8<false, false, false>(e, f, w.base, t.run, &sm, &sv);
+  }
+  if (lane < t.run) {
+    scales[0][wid * t.run + lane] = sm;
+    scales[1][wid * t.run + lane] = sv;
+  }
+  __syncthreads();
+  const int all = t.run * (AT / 32);
+  if ((int)threadIdx.x < 2 * all) {
+    const int k = threadIdx.x / all, j = threadIdx.x % all;
+    (k ? e.v_scale : e.m_scale)[first / kBlock + j] = scales[k][j];
   }
 }
 
 // ---------------------------------------------------------------- norm
+// 553M fp32 gradients (2.2 GB) in 0.326 ms, 6.8 TB/s.
+__device__ __forceinline__ float square_add(float s, float g) { return fmaf(g, g, s); }
+
+// Squares of four blocks' eight elements a lane (fp32: block b at p + 256 b), all
+// loads issued before the first is used: one instruction block, since the
+// compiler, free to choose, waits for each to save registers.
+__device__ __forceinline__ double squares32(const float* p) {
+  float f[4][8];
+  asm volatile(
+      "ld.global.v8.f32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%32];\n\t"
+      "ld.global.v8.f32 {%8, %9, %10, %11, %12, %13, %14, %15}, [%32+1024];\n\t"
+      "ld.global.v8.f32 {%16, %17, %18, %19, %20, %21, %22, %23}, [%32+2048];\n\t"
+      "ld.global.v8.f32 {%24, %25, %26, %27, %28, %29, %30, %31}, [%32+3072];"
+      : "=f"(f[0][0]), "=f"(f[0][1]), "=f"(f[0][2]), "=f"(f[0][3]), "=f"(f[0][4]), "=f"(f[0][5]),
+        "=f"(f[0][6]), "=f"(f[0][7]), "=f"(f[1][0]), "=f"(f[1][1]), "=f"(f[1][2]), "=f"(f[1][3]),
+        "=f"(f[1][4]), "=f"(f[1][5]), "=f"(f[1][6]), "=f"(f[1][7]), "=f"(f[2][0]), "=f"(f[2][1]),
+        "=f"(f[2][2]), "=f"(f[2][3]), "=f"(f[2][4]), "=f"(f[2][5]), "=f"(f[2][6]), "=f"(f[2][7]),
+        "=f"(f[3][0]), "=f"(f[3][1]), "=f"(f[3][2]), "=f"(f[3][3]), "=f"(f[3][4]), "=f"(f[3][5]),
+        "=f"(f[3][6]), "=f"(f[3][7])
+      : "l"(p));
+  double sum = 0.0;
+#pragma unroll
+  for (int b = 0; b < 4; ++b) {
+    float s = 0.f;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) s = square_add(s, f[b][j]);
+    sum += (double)s;
+  }
+  return sum;
+}
+
+__device__ __forceinline__ double squares32(const uint16_t* p) {   // bf16
+  uint4 q[4];
+  asm volatile(
+      "ld.global.v4.u32 {%0, %1, %2, %3}, [%16];\n\t"
+      "ld.global.v4.u32 {%4, %5, %6, %7}, [%16+512];\n\t"
+      "ld.global.v4.u32 {%8, %9, %10, %11}, [%16+1024];\n\t"
+      "ld.global.v4.u32 {%12, %13, %14, %15}, [%16+1536];"
+      : "=r"(q[0].x), "=r"(q[0].y), "=r"(q[0].z), "=r"(q[0].w), "=r"(q[1].x), "=r"(q[1].y),
+        "=r"(q[1].z), "=r"(q[1].w), "=r"(q[2].x), "=r"(q[2].y), "=r"(q[2].z), "=r"(q[2].w),
+        "=r"(q[3].x), "=r"(q[3].y), "=r"(q[3].z), "=r"(q[3].w)
+      : "l"(p));
+  double sum = 0.0;
+#pragma unroll
+  for (int b = 0; b < 4; ++b) {
+    float f[8], s = 0.f;
+    unpack8(q[b], f);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) s = square_add(s, f[j]);
+    sum += (double)s;
+  }
+  return sum;
+}
+
 template <bool WIDE>
-__device__ __forceinline__ void get_grad(const Lane<WIDE>& l, const NormEntry& e, long long base,
-                                         float* g) {
+__device__ __forceinline__ double squares8(const NormEntry& e, long long base, int left) {
+  const Lane<WIDE> l{(int)(threadIdx.x & 31), left};
+  float g[8], s = 0.f;
   if (e.kind & kG16) l.get((const uint16_t*)e.g + base, g);
   else l.get((const float*)e.g + base, g);
+#pragma unroll
+  for (int j = 0; j < 8; ++j) s = square_add(s, g[j]);
+  return (double)s;
 }
 
 // Block b's sum of squares over its chunks: fp32 over a thread's eight elements
@@ -358,25 +565,20 @@ __device__ __forceinline__ void get_grad(const Lane<WIDE>& l, const NormEntry& e
 __global__ void __launch_bounds__(AT) square_sums_kernel(const __grid_constant__ NormTable t,
                                                          double* __restrict__ sums) {
   __shared__ double red[AT / 32];
-  const int wid = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
   double sum = 0.0;
-  int k = 0, end = 0;
-  const int lane = threadIdx.x & 31;
-  for (int c = blockIdx.x; c < t.chunks; c += gridDim.x) {
-    if (c >= end) {
-      k = entry_of(t, c);
-      end = k + 1 < t.count ? t.e[k + 1].first : t.chunks;
+  Walk w;
+  for (w.c = blockIdx.x; w.at(t); w.c += gridDim.x) {
+    const NormEntry& e = t.e[w.k];
+    const bool wide = e.kind & kWide;
+    if (wide && w.left == kBlock * kNormRun) {
+      const long long i = w.base + lane * 8;
+      sum += e.kind & kG16 ? squares32((const uint16_t*)e.g + i) : squares32((const float*)e.g + i);
+      continue;
     }
-    const NormEntry& e = t.e[k];
-    const long long base = (long long)(c - e.first) * kChunk + wid * kBlock;
-    if (base >= e.n) continue;
-    const int left = (int)min((long long)kBlock, e.n - base);
-    float g[8], s = 0.f;
-    if ((e.kind & kWide) && left == kBlock) get_grad(Lane<true>{lane, left}, e, base, g);
-    else get_grad(Lane<false>{lane, left}, e, base, g);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) s = fmaf(g[j], g[j], s);
-    sum += (double)s;
+    for (; w.left > 0; w.left -= kBlock, w.base += kBlock)
+      sum += wide && w.left >= kBlock ? squares8<true>(e, w.base, kBlock)
+                                      : squares8<false>(e, w.base, w.left);
   }
 #pragma unroll
   for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(kFull, sum, off);
@@ -389,19 +591,24 @@ __global__ void __launch_bounds__(AT) square_sums_kernel(const __grid_constant__
   }
 }
 
-__global__ void __launch_bounds__(AT) norm_kernel(const double* __restrict__ sums, int n,
-                                                  float max_norm, float* __restrict__ norm) {
-  __shared__ double red[AT];
+__global__ void __launch_bounds__(kNormThreads) norm_kernel(const double* sums, int n,
+                                                            float max_norm, float* norm) {
+  __shared__ double red[kNormThreads / 32];
+  const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
+  wait_for_previous();
   double s = 0.0;
-  for (int i = threadIdx.x; i < n; i += AT) s += sums[i];
-  red[threadIdx.x] = s;
+#pragma unroll 4
+  for (int i = threadIdx.x; i < n; i += kNormThreads) s += sums[i];
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) s += __shfl_xor_sync(kFull, s, off);
+  if (lane == 0) red[wid] = s;
   __syncthreads();
-  for (int k = AT / 2; k > 0; k >>= 1) {
-    if (threadIdx.x < k) red[threadIdx.x] += red[threadIdx.x + k];
-    __syncthreads();
-  }
-  if (threadIdx.x == 0) {
-    const float v = (float)sqrt(red[0]);
+  if (wid > 0) return;
+  s = red[lane];
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) s += __shfl_xor_sync(kFull, s, off);
+  if (lane == 0) {
+    const float v = (float)sqrt(s);
     norm[0] = v;
     norm[1] = max_norm > 0.f ? fminf(max_norm / (v + 1e-6f), 1.f) : 1.f;
     norm[2] = isfinite(v) ? 1.f : 0.f;
@@ -409,8 +616,19 @@ __global__ void __launch_bounds__(AT) norm_kernel(const double* __restrict__ sum
   }
 }
 
-int chunks_of(long long n) { return (int)((n + kChunk - 1) / kChunk); }
-int grid_for(int chunks) { return chunks < kNormBlocks ? chunks : kNormBlocks; }
+int chunks_of(long long n, int run) {
+  return (int)((n + (long long)kRow * run - 1) / ((long long)kRow * run));
+}
+
+// Blocks a warp takes in a row: the most up to `most` that leaves eight chunks
+// an SM.
+int run_for(const moe_adamw_tensor_t* x, int i, int j, int most) {
+  long long total = 0;
+  for (int k = i; k < j; ++k) total += x[k].n;
+  int run = most;
+  while (run > 1 && total < (long long)run * kRow * 152 * 8) run /= 2;
+  return run;
+}
 int grad_bits(const moe_adamw_tensor_t& x) { return x.g_dtype == MOE_BF16 ? kG16 : 0; }
 
 // Eight elements of each array from any multiple of eight are one access.
@@ -418,17 +636,17 @@ bool wide_at(const void* p, int element_bytes) {
   return reinterpret_cast<uintptr_t>(p) % (8 * element_bytes) == 0;
 }
 
-// Calls launch(first tensor, past the last, chunks) for runs of tensors that fit
-// one launch's parameter and chunk count.
+// Calls launch(first tensor, past the last) for stretches of the list that fit one
+// launch's parameter and chunk count.
 template <typename F>
 cudaError_t in_runs(const moe_adamw_tensor_t* x, int n, F launch) {
   for (int i = 0; i < n;) {
     int j = i;
     long long chunks = 0;
-    while (j < n && j - i < kPerLaunch && chunks + chunks_of(x[j].n) < (1LL << 30))
-      chunks += chunks_of(x[j++].n);
+    while (j < n && j - i < kPerLaunch && chunks + chunks_of(x[j].n, 1) < (1LL << 30))
+      chunks += chunks_of(x[j++].n, 1);
     if (chunks > 0) {
-      const cudaError_t e = launch(i, j, (int)chunks);
+      const cudaError_t e = launch(i, j);
       if (e != cudaSuccess) return e;
     }
     i = j;
@@ -439,7 +657,7 @@ cudaError_t in_runs(const moe_adamw_tensor_t* x, int n, F launch) {
 
 size_t grad_norm_ws_bytes(const moe_adamw_tensor_t* x, int n) {
   int runs = 0;
-  (void)in_runs(x, n, [&](int, int, int) { ++runs; return cudaSuccess; });
+  (void)in_runs(x, n, [&](int, int) { ++runs; return cudaSuccess; });
   return align_up(sizeof(double) * kNormBlocks * (size_t)(runs > 0 ? runs : 1), 256);
 }
 
@@ -447,32 +665,30 @@ cudaError_t launch_grad_norm(const moe_adamw_tensor_t* x, int n, float max_norm,
                              void* ws, cudaStream_t s) {
   double* sums = static_cast<double*>(ws);
   int used = 0;
-  const cudaError_t e = in_runs(x, n, [&](int i, int j, int chunks) {
+  const cudaError_t e = in_runs(x, n, [&](int i, int j) {
     NormTable t;
-    t.count = 0;
-    t.chunks = chunks;
-    int first = 0;
+    t.count = t.chunks = 0;
+    t.run = run_for(x, i, j, kNormRun);
     for (int k = i; k < j; ++k) {
       if (x[k].n == 0) continue;
       const bool wide = wide_at(x[k].g, dtype_bytes(x[k].g_dtype));
-      t.e[t.count++] = {x[k].g, x[k].n, grad_bits(x[k]) | (wide ? kWide : 0), first};
-      first += chunks_of(x[k].n);
+      t.e[t.count++] = {x[k].g, x[k].n, grad_bits(x[k]) | (wide ? kWide : 0), t.chunks};
+      t.chunks += chunks_of(x[k].n, t.run);
     }
-    const int blocks = grid_for(chunks);
+    const int blocks = std::min(t.chunks, kNormBlocks);
     square_sums_kernel<<<blocks, AT, 0, s>>>(t, sums + used);
     used += blocks;
     count_launches(1);
     return cudaGetLastError();
   });
   if (e != cudaSuccess) return e;
-  norm_kernel<<<1, AT, 0, s>>>(sums, used, max_norm, norm);
   count_launches(1);
-  return cudaGetLastError();
+  return launch_after(norm_kernel, 1, kNormThreads, s, sums, used, max_norm, norm);
 }
 
 cudaError_t launch_adamw(const moe_adamw_tensor_t* x, int n, const moe_adamw_t& h,
                          const float* norm, cudaStream_t s) {
-  return in_runs(x, n, [&](int i, int j, int) {
+  return in_runs(x, n, [&](int i, int j) {
     AdamTable t;
     t.b1 = (float)h.beta1;
     t.b2 = (float)h.beta2;
@@ -484,6 +700,7 @@ cudaError_t launch_adamw(const moe_adamw_tensor_t* x, int n, const moe_adamw_t& 
     t.norm = norm;
     for (const int bits : {8, 32}) {   // a launch for each kind of state in the run
       t.count = t.chunks = 0;
+      t.run = run_for(x, i, j, bits == 8 ? kMostRun : kRun32);
       for (int k = i; k < j; ++k) {
         if (x[k].n == 0 || x[k].state_bits != bits) continue;
         AdamEntry& e = t.e[t.count++];
@@ -502,12 +719,11 @@ cudaError_t launch_adamw(const moe_adamw_tensor_t* x, int n, const moe_adamw_t& 
                           wide_at(e.v, bits / 8);
         e.kind = grad_bits(x[k]) | (x[k].p_dtype == MOE_BF16 ? kP16 : 0) | (wide ? kWide : 0);
         e.first = t.chunks;
-        t.chunks += chunks_of(x[k].n);
+        t.chunks += chunks_of(x[k].n, t.run);
       }
       if (t.count == 0) continue;
-      if (bits == 8) adamw_kernel<true><<<grid_for(t.chunks), AT, 0, s>>>(t);
-      else adamw_kernel<false><<<grid_for(t.chunks), AT, 0, s>>>(t);
-      count_launches(1);
+      if (bits == 8) adamw8_kernel<<<t.chunks, AT, 0, s>>>(t);
+      else adamw32_kernel<<<t.chunks, AT, 0, s>>>(t);
       const cudaError_t e = cudaGetLastError();
       if (e != cudaSuccess) return e;
     }

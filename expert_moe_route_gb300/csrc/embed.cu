@@ -4,10 +4,8 @@
 // The gradient sorts the positions by id (sort.cu), so every table row is
 // written once by one owner and equal ids are summed in position order: no
 // atomics, bitwise reproducible.  The ids of text follow a power law, and the
-// commonest may own a tenth of all positions: the sorted list is cut into
-// pieces of kPiece positions, a piece that lies inside one row is summed by a
-// group of its own into the workspace, and a row's owner adds the pieces and
-// the ragged ends in order.
+// commonest may own a tenth of all positions, so the work is cut by positions of
+// the sorted list, not by rows.
 //
 // Bound by HBM: n rows read, V rows (or, accumulating, the distinct ones) written.
 #include "embed.cuh"
@@ -18,7 +16,7 @@ namespace moe {
 
 namespace {
 constexpr int ET = 256;
-constexpr int kPiece = 64;
+constexpr int kPiece = 32;
 
 // A group of G threads copies kRows rows side by side, so that a thread has that
 // many loads in flight although a row is only one or two accesses a thread.
@@ -57,9 +55,10 @@ __global__ void __launch_bounds__(ET) embed_kernel(const I* __restrict__ ids, lo
   }
 }
 
-// First of the n sorted positions whose id is >= v.
-__device__ __forceinline__ int first_at(const int2* __restrict__ sorted, int n, int v) {
-  int lo = 0, hi = n;
+// First sorted position whose id is >= v.
+__device__ __forceinline__ int first_at(const int2* sorted, const SortedHead* head, int shift,
+                                        int v) {
+  int lo = head->top[v >> shift], hi = head->top[(v >> shift) + 1];
   while (lo < hi) {
     const int mid = lo + (hi - lo) / 2;
     if (sorted[mid].x < v) lo = mid + 1;
@@ -68,96 +67,223 @@ __device__ __forceinline__ int first_at(const int2* __restrict__ sorted, int n, 
   return lo;
 }
 
-// acc += dout rows of sorted[lo..hi), in order.
-template <typename T, int W>
-__device__ __forceinline__ void add_rows(const int2* __restrict__ sorted, int lo, int hi,
-                                         const T* __restrict__ dout, long long ldd, int v,
-                                         float* acc) {
-  for (int k = lo; k < hi; k += 8) {
-    typename Vec<T, W>::Raw q[8];
+// A row that spans pieces: its first piece, its id, how many pieces it touches.
+struct Span {
+  int first, id, pieces, pad;
+};
+
+// The sorted list is cut into pieces of kPiece positions.  A warp takes a piece
+// and 32 accesses of the row length, walks the positions and writes a table row
+// where one ends.  A row that goes past the piece's end leaves its part in
+// parts[2 k + 1] and k in `spans`, one that came in from the piece before in
+// parts[2 k] (as does one that fills the whole piece); joined_kernel adds those.  What the kernel
+// before wrote is read with plain loads (no __restrict__, no __ldg): a load of
+// constant data might be moved above wait_for_previous().
+constexpr int RT = 128;          // threads a block of rows_kernel
+constexpr int kFlight = 16;      // positions whose rows a warp has in flight
+constexpr int kGroup = 4;        // positions waited for together
+constexpr int kOwn = 8;        // rows a warp looks through for rows without a token
+constexpr int kLong = 16;      // a row of more pieces is joined by a block
+
+// Copies of a lane's accesses: 4, 8 or 16 bytes on their way into shared memory.
+template <int BYTES>
+__device__ __forceinline__ void copy_async(void* to, const void* from) {
+  if (BYTES == 16)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(to)), "l"(from)
+                 : "memory");
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(smem_u32(to)), "l"(from),
+                 "n"(BYTES < 4 ? 4 : BYTES) : "memory");
+}
+
+template <typename T, typename O, int W, bool ADD>
+__global__ void __launch_bounds__(RT) rows_kernel(
+    const int2* sorted, SortedHead* head, int shift, const T* __restrict__ dout, long long ldd,
+    int V, int d, int cols, int piece_blocks, float scale, O* dtable, long long ldt, float* parts,
+    Span* spans) {
+  using In = typename Vec<T, W>::Raw;
+  constexpr bool kAsync = sizeof(In) >= 4;   // a 2-byte access has no asynchronous copy
+  constexpr bool kRed = ADD && W >= 4 && sizeof(O) == 4;   // added to by the memory
+  __shared__ In slots[RT / 32][kFlight][32];
+  wait_for_previous();
+  let_next_start();
+  const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
+  const int nv = d / W;
+  if ((int)blockIdx.x >= piece_blocks) {   // rows without a token are zero
+    const long long r0 = ((long long)(blockIdx.x - piece_blocks) * (RT / 32) + wid) * kOwn;
+    const long long r = r0 + lane;
+    const int lo = lane > kOwn ? 0 : r < V ? first_at(sorted, head, shift, (int)r) : head->live;
+    const int hi = __shfl_down_sync(kFull, lo, 1);
+    for (int k = 0; k < kOwn && r0 + k < V; ++k) {
+      if (__shfl_sync(kFull, lo, k) != __shfl_sync(kFull, hi, k)) continue;
+      O* dst = dtable + (r0 + k) * ldt;
+      for (int v = lane; v < nv; v += 32)
+        Vec<O, W>::store(dst + (long long)v * W, Vec<O, W>::zero());
+    }
+    return;
+  }
+  const int n = head->live;
+  const long long unit = (long long)blockIdx.x * (RT / 32) + wid;
+  const int k = (int)(unit / cols), v = (int)(unit % cols) * 32 + lane;
+  const int p0 = k * kPiece, count = min(kPiece, n - p0);
+  if (count <= 0) return;
+  // lane l holds position p0 + l and whether its row ends there
+  const int2 kv = lane < count ? sorted[p0 + lane] : make_int2(-1, 0);
+  const int before = p0 > 0 ? sorted[p0 - 1].x : -1;
+  const int after = p0 + count < n ? sorted[p0 + count].x : -1;
+  const bool here = v < nv;
+  const T* const column = dout + (long long)v * W;
+  In(&slot)[kFlight][32] = slots[wid];
+  auto fetch = [&](int i0) {             // positions i0 .. i0 + kGroup - 1; one commit
 #pragma unroll
-    for (int u = 0; u < 8; ++u)
-      q[u] = k + u < hi ? Vec<T, W>::load(dout + (long long)sorted[k + u].y * ldd + (long long)v * W)
-                        : Vec<T, W>::zero();
+    for (int u = 0; u < kGroup; ++u) {
+      const int i = i0 + u;
+      const int at = __shfl_sync(kFull, kv.y, i & 31);
+      if (here && i < count) {
+        const T* from = column + (long long)at * ldd;
+        if (kAsync) copy_async<sizeof(In)>(&slot[i % kFlight][lane], from);
+        else slot[i % kFlight][lane] = Vec<T, W>::load(from);
+      }
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
 #pragma unroll
-    for (int u = 0; u < 8; ++u) {
-      if (k + u >= hi) break;
+  for (int i = 0; i < kFlight; i += kGroup) fetch(i);
+  int next = __shfl_down_sync(kFull, kv.x, 1);
+  if (lane == count - 1) next = after;
+  const unsigned ends = __ballot_sync(kFull, lane < count && next != kv.x);
+  bool inherited = __shfl_sync(kFull, kv.x, 0) == before;   // the row began in an earlier piece
+  // one warp of a piece's notes the row that goes on from here: short ones from
+  // the front of `spans`, long ones from its back
+  if (v == 0 && !(ends >> (count - 1) & 1) && !(inherited && ends == 0)) {
+    const int end = after + 1 < V ? first_at(sorted, head, shift, after + 1) : n;
+    const int pieces = (end - 1) / kPiece - k + 1;
+    const int at = pieces > kLong ? (n - 1) / kPiece - atomicAdd(&head->long_spans, 1)
+                                  : atomicAdd(&head->spans, 1);
+    spans[at] = {k, after, pieces, 0};
+  }
+  float acc[W];
+#pragma unroll
+  for (int j = 0; j < W; ++j) acc[j] = 0.f;
+#pragma unroll 1
+  for (int i0 = 0; i0 < count; i0 += kGroup) {
+    asm volatile("cp.async.wait_group %0;" ::"n"(kFlight / kGroup - 1) : "memory");
+#pragma unroll
+    for (int u = 0; u < kGroup; ++u) {
+      const int i = i0 + u;
+      if (i >= count) break;
       float f[W];
-      Vec<T, W>::unpack(q[u], f);
+      if (here) Vec<T, W>::unpack(slot[i % kFlight][lane], f);
+#pragma unroll
+      for (int j = 0; j < W; ++j) acc[j] += here ? f[j] : 0.f;
+      const bool ended = ends >> i & 1;
+      if (!ended && i != count - 1) continue;
+      const int id = __shfl_sync(kFull, kv.x, i);
+      if (here && (inherited || !ended)) {
+        Vec<float, W>::store(parts + (2LL * k + (inherited ? 0 : 1)) * d + (long long)v * W,
+                             Vec<float, W>::pack(acc));
+      } else if (here) {
+        O* dst = dtable + id * ldt + (long long)v * W;
+#pragma unroll
+        for (int j = 0; j < W; ++j) acc[j] *= scale;
+        if constexpr (kRed) {
+#pragma unroll
+          for (int j = 0; j < W; j += 4) add4_in_memory(dst + j, acc + j);
+        } else {
+          if (ADD) {
+            Vec<O, W>::unpack(Vec<O, W>::load_rw(dst), f);
+#pragma unroll
+            for (int j = 0; j < W; ++j) acc[j] += f[j];
+          }
+          Vec<O, W>::store(dst, Vec<O, W>::pack(acc));
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < W; ++j) acc[j] = 0.f;
+      inherited = false;
+    }
+    fetch(i0 + kFlight);
+  }
+}
+
+// acc += parts [a, b) of a row that spans pieces, 32 accesses of it.
+template <int W>
+__device__ __forceinline__ void add_parts(const Span& sp, int a, int b, int d, int v,
+                                          const float* parts, float* acc) {
+  for (int i0 = a; i0 < b; i0 += 4) {
+    typename Vec<float, W>::Raw q[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int i = i0 + u;
+      const long long slot = i == 0 ? 2LL * sp.first + 1 : 2LL * (sp.first + i);
+      q[u] = i < b ? Vec<float, W>::load_rw(parts + slot * d + (long long)v * W)
+                   : Vec<float, W>::zero();
+    }
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      if (i0 + u >= b) break;
+      float f[W];
+      Vec<float, W>::unpack(q[u], f);
 #pragma unroll
       for (int j = 0; j < W; ++j) acc[j] += f[j];
     }
   }
 }
 
-// partial[k] = sum of piece k, for the pieces inside one row.  There are few
-// pieces, so a warp takes 32 accesses of a row, not a group the whole row.
-template <typename T, int W>
-__global__ void __launch_bounds__(ET) pieces_kernel(const int2* __restrict__ sorted,
-                                                    const int32_t* __restrict__ live,
-                                                    const T* __restrict__ dout, long long ldd,
-                                                    int d, int cols, float* __restrict__ partial) {
-  const int lane = threadIdx.x & 31;
-  const int pieces = *live / kPiece;
-  const long long unit = (long long)blockIdx.x * (ET / 32) + threadIdx.x / 32;
-  const int k = (int)(unit / cols), v = (int)(unit % cols) * 32 + lane;
-  if (k >= pieces) return;
-  const int lo = k * kPiece;
-  if (sorted[lo].x != sorted[lo + kPiece - 1].x || v >= d / W) return;
-  float acc[W];
+// Rows that span pieces: a warp adds the parts of 32 accesses of a row, in order;
+// of a long row a block, its warps contiguous ranges of the parts, then the warps'
+// sums in order.
+template <typename O, int W, bool ADD>
+__global__ void __launch_bounds__(ET) joined_kernel(const SortedHead* head, int d, int cols,
+                                                    float scale, O* dtable, long long ldt,
+                                                    const float* parts, const Span* spans) {
+  __shared__ float red[ET / 32][32][W + (W > 1)];
+  wait_for_previous();
+  const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
+  auto put = [&](int id, int v, const typename Vec<O, W>::Raw& before, float* acc) {
+    float old[W];
+    if (ADD) Vec<O, W>::unpack(before, old);
 #pragma unroll
-  for (int j = 0; j < W; ++j) acc[j] = 0.f;
-  add_rows<T, W>(sorted, lo, lo + kPiece, dout, ldd, v, acc);
-  Vec<float, W>::store(partial + (long long)k * d + (long long)v * W, Vec<float, W>::pack(acc));
-}
-
-// A group of G threads owns kOwn neighbouring rows of the table.
-constexpr int kOwn = 8;
-
-template <typename T, typename O, int W, int G, bool ADD>
-__global__ void __launch_bounds__(ET) table_rows_kernel(
-    const int2* __restrict__ sorted, const int32_t* __restrict__ live,
-    const T* __restrict__ dout, long long ldd, const float* __restrict__ partial, int V, int d,
-    float scale, O* __restrict__ dtable, long long ldt) {
-  constexpr int NG = ET / G;
-  __shared__ int start_s[NG][kOwn + 1];
-  const int grp = threadIdx.x / G, gt = threadIdx.x % G;
-  const int nv = d / W;
-  const long long r0 = ((long long)blockIdx.x * NG + grp) * kOwn;
-  if (gt <= kOwn)
-    start_s[grp][gt] = first_at(sorted, *live, (int)min((long long)V, r0 + gt));
-  if (G == 32) __syncwarp();
-  else __syncthreads();
-  for (int k = 0; k < kOwn; ++k) {
-    const long long r = r0 + k;
-    if (r >= V) return;
-    const int lo = start_s[grp][k], hi = start_s[grp][k + 1];
-    if (ADD && lo == hi) continue;
-    const int p0 = (lo + kPiece - 1) / kPiece, p1 = hi / kPiece;   // whole pieces in the row
-    const int head = p0 < p1 ? p0 * kPiece : hi;
-    for (int v = gt; v < nv; v += G) {
-      float acc[W];
+    for (int j = 0; j < W; ++j) acc[j] = ADD ? acc[j] * scale + old[j] : acc[j] * scale;
+    Vec<O, W>::store(dtable + id * ldt + (long long)v * W, Vec<O, W>::pack(acc));
+  };
+  auto get = [&](int id, int v) {
+    return ADD ? Vec<O, W>::load_rw(dtable + id * ldt + (long long)v * W) : Vec<O, W>::zero();
+  };
+  const int last = (head->live - 1) / kPiece;
+  for (long long task = blockIdx.x; task < (long long)head->long_spans * cols; task += gridDim.x) {
+    const Span sp = spans[last - task / cols];
+    const int v = (int)(task % cols) * 32 + lane;
+    const bool here = v < d / W;
+    const int share = (sp.pieces + ET / 32 - 1) / (ET / 32);
+    const int a = min(sp.pieces, wid * share), b = min(sp.pieces, a + share);
+    float acc[W];
 #pragma unroll
-      for (int j = 0; j < W; ++j) acc[j] = 0.f;
-      add_rows<T, W>(sorted, lo, head, dout, ldd, v, acc);
-      for (int p = p0; p < p1; ++p) {
-        float part[W];
-        Vec<float, W>::unpack(Vec<float, W>::load(partial + (long long)p * d + (long long)v * W), part);
+    for (int j = 0; j < W; ++j) acc[j] = 0.f;
+    if (here) add_parts<W>(sp, a, b, d, v, parts, acc);
+    __syncthreads();
 #pragma unroll
-        for (int j = 0; j < W; ++j) acc[j] += part[j];
-      }
-      if (p0 < p1) add_rows<T, W>(sorted, p1 * kPiece, hi, dout, ldd, v, acc);
-      O* dst = dtable + r * ldt + (long long)v * W;
+    for (int j = 0; j < W; ++j) red[wid][lane][j] = acc[j];
+    __syncthreads();
+    if (wid > 0 || !here) continue;
+    const auto old = get(sp.id, v);
+    for (int w = 1; w < ET / 32; ++w)
 #pragma unroll
-      for (int j = 0; j < W; ++j) acc[j] *= scale;
-      if (ADD) {
-        float old[W];
-        Vec<O, W>::unpack(Vec<O, W>::load_rw(dst), old);
+      for (int j = 0; j < W; ++j) acc[j] += red[w][lane][j];
+    put(sp.id, v, old, acc);
+  }
+  const long long warps = (long long)gridDim.x * (ET / 32);
+  for (long long task = (long long)blockIdx.x * (ET / 32) + wid;
+       task < (long long)head->spans * cols; task += warps) {
+    const Span sp = spans[task / cols];
+    const int v = (int)(task % cols) * 32 + lane;
+    if (v >= d / W) continue;
+    const auto old = get(sp.id, v);
+    float acc[W];
 #pragma unroll
-        for (int j = 0; j < W; ++j) acc[j] += old[j];
-      }
-      Vec<O, W>::store(dst, Vec<O, W>::pack(acc));
-    }
+    for (int j = 0; j < W; ++j) acc[j] = 0.f;
+    add_parts<W>(sp, 0, sp.pieces, d, v, parts, acc);
+    put(sp.id, v, old, acc);
   }
 }
 
@@ -178,59 +304,75 @@ cudaError_t embed_t(const EmbedArgs& a, cudaStream_t s) {
   return cudaGetLastError();
 }
 
-size_t sort_bytes(long long n) { return align_up((size_t)n * sizeof(int2), 256); }
+// The workspace of a gradient: unsorted pairs, then (byte offsets) these.
+struct TableWs {
+  size_t sorted, head, spans, parts, total;
+};
+TableWs table_ws(long long n, int d) {
+  const size_t pairs = align_up((size_t)n * sizeof(int2), 256), pieces = blocks_for(n, kPiece);
+  TableWs w;
+  w.sorted = pairs;
+  w.head = w.sorted + pairs;
+  w.spans = w.head + align_up(sizeof(SortedHead), 256);
+  w.parts = w.spans + align_up(pieces * sizeof(Span), 256);
+  w.total = w.parts + align_up(pieces * 2 * d * sizeof(float), 256);
+  return w;
+}
 
-template <typename T, typename O, int W, int G>
+template <typename T, typename O, int W, bool ADD>
 cudaError_t table_t(const EmbedArgs& a, void* ws, int* err, cudaStream_t s) {
   uint8_t* p = static_cast<uint8_t*>(ws);
+  const TableWs at = table_ws(a.n, a.d);
   int2* scratch = reinterpret_cast<int2*>(p);
-  int2* sorted = reinterpret_cast<int2*>(p + sort_bytes(a.n));
-  int32_t* live = reinterpret_cast<int32_t*>(p + 2 * sort_bytes(a.n));
-  float* partial = reinterpret_cast<float*>(p + 2 * sort_bytes(a.n) + 256);
-  cudaError_t e = launch_sort_ids(a.ids, a.ids_bytes, (int)a.n, a.V, scratch, sorted, live, err, s);
+  int2* sorted = reinterpret_cast<int2*>(p + at.sorted);
+  SortedHead* head = reinterpret_cast<SortedHead*>(p + at.head);
+  Span* spans = reinterpret_cast<Span*>(p + at.spans);
+  float* parts = reinterpret_cast<float*>(p + at.parts);
+  int shift = 0;
+  cudaError_t e =
+      launch_sort_ids(a.ids, a.ids_bytes, (int)a.n, a.V, scratch, sorted, head, &shift, err, s);
   if (e != cudaSuccess) return e;
-  const long long pieces = a.n / kPiece;
-  const int cols = blocks_for(a.d / W, 32);
-  if (pieces > 0)
-    pieces_kernel<T, W><<<blocks_for(pieces * cols, ET / 32), ET, 0, s>>>(
-        sorted, live, (const T*)a.in.p, a.in.ld, a.d, cols, partial);
-  const int blocks = blocks_for(a.V, ET / G * kOwn);
-  if (a.accumulate)
-    table_rows_kernel<T, O, W, G, true><<<blocks, ET, 0, s>>>(
-        sorted, live, (const T*)a.in.p, a.in.ld, partial, a.V, a.d, a.scale, (O*)a.out.p,
-        a.out.ld);
-  else
-    table_rows_kernel<T, O, W, G, false><<<blocks, ET, 0, s>>>(
-        sorted, live, (const T*)a.in.p, a.in.ld, partial, a.V, a.d, a.scale, (O*)a.out.p,
-        a.out.ld);
-  count_launches(pieces > 0 ? 2 : 1);
-  return cudaGetLastError();
+  const int pieces = blocks_for(a.n, kPiece), cols = blocks_for(a.d / W, 32);
+  const int piece_blocks = blocks_for((long long)pieces * cols, RT / 32);
+  const int blocks = piece_blocks + (ADD ? 0 : blocks_for(a.V, RT / 32 * kOwn));
+  if (blocks > 0)
+    e = launch_after(rows_kernel<T, O, W, ADD>, blocks, RT, s, sorted, head, shift,
+                     (const T*)a.in.p, a.in.ld, a.V, a.d, cols, piece_blocks, a.scale,
+                     (O*)a.out.p, a.out.ld, parts, spans);
+  if (e == cudaSuccess && pieces > 1) {
+    const long long most = (long long)(pieces - 1) * cols;
+    e = launch_after(joined_kernel<O, W, ADD>, (int)(most < 152 * 4 ? most : 152 * 4), ET, s,
+                     head, a.d, cols, a.scale, (O*)a.out.p, a.out.ld, parts, spans);
+  }
+  count_launches((blocks > 0) + (pieces > 1));
+  return e;
 }
 
 template <typename T, typename O, int W>
 cudaError_t by_length(const EmbedArgs& a, bool grad, void* ws, int* err, cudaStream_t s) {
-  if (a.d / W > 64)
-    return grad ? table_t<T, O, W, ET>(a, ws, err, s) : embed_t<T, O, W, ET>(a, s);
-  return grad ? table_t<T, O, W, 32>(a, ws, err, s) : embed_t<T, O, W, 32>(a, s);
+  if (grad)
+    return a.accumulate ? table_t<T, O, W, true>(a, ws, err, s)
+                        : table_t<T, O, W, false>(a, ws, err, s);
+  return a.d / W > 64 ? embed_t<T, O, W, ET>(a, s) : embed_t<T, O, W, 32>(a, s);
 }
 
-// Elements per access: 8 where both sides' rows are 16-byte aligned, 2 where a
-// pair is aligned, else 1.
+// Elements per access: the most of 8, 4, 2 and 1 that both sides' rows are aligned
+// to, up to 16 bytes of the input.
 int width(const EmbedArgs& a) {
   const int si = dtype_bytes(a.in_dtype), so = dtype_bytes(a.out_dtype);
-  for (int w : {8, 2}) {
-    const int bi = w * si < 16 ? w * si : 16, bo = w * so < 16 ? w * so : 16;
-    if (a.d % w == 0 && (uintptr_t)a.in.p % bi == 0 && a.in.ld * si % bi == 0 &&
-        (uintptr_t)a.out.p % bo == 0 && a.out.ld * so % bo == 0)
+  for (int w = 16 / si; w > 1; w /= 2)
+    if (a.d % w == 0 && (uintptr_t)a.in.p % (w * si) == 0 && a.in.ld % w == 0 &&
+        (uintptr_t)a.out.p % (w * so) == 0 && a.out.ld % w == 0)
       return w;
-  }
   return 1;
 }
 
 template <typename T, typename O>
 cudaError_t by_width(const EmbedArgs& a, bool grad, void* ws, int* err, cudaStream_t s) {
   switch (width(a)) {
-    case 8: return by_length<T, O, 8>(a, grad, ws, err, s);
+    case 8:
+      if constexpr (sizeof(T) == 2) return by_length<T, O, 8>(a, grad, ws, err, s);
+    case 4: return by_length<T, O, 4>(a, grad, ws, err, s);
     case 2: return by_length<T, O, 2>(a, grad, ws, err, s);
     default: return by_length<T, O, 1>(a, grad, ws, err, s);
   }
@@ -255,9 +397,7 @@ cudaError_t launch_embed(const EmbedArgs& a, cudaStream_t s) {
   return by_type(a, false, nullptr, nullptr, s);
 }
 
-size_t embed_bwd_ws_bytes(long long n, int d) {
-  return 2 * sort_bytes(n) + 256 + align_up((size_t)(n / kPiece) * d * sizeof(float), 256);
-}
+size_t embed_bwd_ws_bytes(long long n, int d) { return table_ws(n, d).total; }
 
 cudaError_t launch_embed_bwd(const EmbedArgs& a, void* ws, int* err, cudaStream_t s) {
   return by_type(a, true, ws, err, s);

@@ -18,6 +18,22 @@ moe_status_t cuda_failed(cudaError_t e);
 // MOE_CHECK in `flags`, waits for `s` and translates the device error word.
 moe_status_t finish(cudaError_t launched, const int* err_dev, unsigned flags, cudaStream_t s);
 
+// Launches a kernel whose first act is wait_for_previous(): its launch overlaps the
+// end of the kernel before it in the stream.
+template <typename... P, typename... A>
+cudaError_t launch_after(void (*f)(P...), int blocks, int threads, cudaStream_t s, A... a) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(blocks);
+  cfg.blockDim = dim3(threads);
+  cfg.stream = s;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, f, static_cast<P>(a)...);
+}
+
 // Adds n to the process-wide count of kernels launched by the library.
 void count_launches(int n);
 // Record the caller's trace events around stage `stage` (moe_stage_t), if tracing is on.

@@ -203,7 +203,7 @@ __global__ void __launch_bounds__(PT) collect_kernel(
 
 template <typename T, int W, int G, int RM>
 cudaError_t spread_t(const PermuteArgs& a, cudaStream_t s) {
-  const long long units = std::max<long long>(a.T, (a.N + 31) / 32);
+  const long long units = std::max<long long>(a.T, (a.N + 7) / 8);
   const int blocks = (int)((units + PT / G - 1) / (PT / G));
   if (a.dw)
     spread_kernel<T, W, G, RM, true><<<blocks, PT, 0, s>>>(

@@ -17,10 +17,29 @@ template <> __device__ __forceinline__ __nv_bfloat16 from_f32(float v) { return 
 template <> __device__ __forceinline__ __half from_f32(float v) { return __float2half_rn(v); }
 template <> __device__ __forceinline__ float from_f32(float v) { return v; }
 
-// W elements of T as raw bits: one memory access of 2, 4, 8 or 16 bytes, or two of 16.
-struct alignas(16) Raw32 {
+// W elements of T as raw bits: one memory access of 2, 4, 8, 16 or 32 bytes, aligned
+// to its size.
+struct alignas(32) Raw32 {
   uint4 a, b;
 };
+__device__ __forceinline__ Raw32 load32(const void* p) {
+  Raw32 r;
+  asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=r"(r.a.x), "=r"(r.a.y), "=r"(r.a.z), "=r"(r.a.w), "=r"(r.b.x), "=r"(r.b.y),
+                 "=r"(r.b.z), "=r"(r.b.w)
+               : "l"(p) : "memory");
+  return r;
+}
+__device__ __forceinline__ void store32(void* p, const Raw32& r) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(r.a.x),
+               "r"(r.a.y), "r"(r.a.z), "r"(r.a.w), "r"(r.b.x), "r"(r.b.y), "r"(r.b.z), "r"(r.b.w)
+               : "memory");
+}
+// p[0..3] += f[0..3] in memory (fp32, 16-byte aligned; a sum below 2^-126 may become 0).
+__device__ __forceinline__ void add4_in_memory(float* p, const float* f) {
+  asm volatile("red.relaxed.gpu.global.add.v4.f32 [%0], {%1, %2, %3, %4};" ::"l"(p), "f"(f[0]),
+               "f"(f[1]), "f"(f[2]), "f"(f[3]) : "memory");
+}
 template <int BYTES> struct RawOf;
 template <> struct RawOf<32> { using type = Raw32; };
 template <> struct RawOf<16> { using type = uint4; };
@@ -31,24 +50,22 @@ template <> struct RawOf<2> { using type = uint16_t; };
 template <typename T, int W> struct Vec {
   using Raw = typename RawOf<sizeof(T) * W>::type;
   static __device__ __forceinline__ Raw load(const T* p) {   // read-only data
-    if constexpr (sizeof(Raw) == 32) {
-      Raw r;
-      r.a = __ldg(reinterpret_cast<const uint4*>(p));
-      r.b = __ldg(reinterpret_cast<const uint4*>(p) + 1);
-      return r;
-    } else {
-      return __ldg(reinterpret_cast<const Raw*>(p));
-    }
+    if constexpr (sizeof(Raw) == 32) return load32(p);
+    else return __ldg(reinterpret_cast<const Raw*>(p));
   }
   static __device__ __forceinline__ Raw load_rw(const T* p) {   // data this kernel also writes
-    return *reinterpret_cast<const Raw*>(p);
+    if constexpr (sizeof(Raw) == 32) return load32(p);
+    else return *reinterpret_cast<const Raw*>(p);
   }
   static __device__ __forceinline__ Raw zero() {
     Raw r;
     memset(&r, 0, sizeof(r));
     return r;
   }
-  static __device__ __forceinline__ void store(T* p, const Raw& r) { *reinterpret_cast<Raw*>(p) = r; }
+  static __device__ __forceinline__ void store(T* p, const Raw& r) {
+    if constexpr (sizeof(Raw) == 32) store32(p, r);
+    else *reinterpret_cast<Raw*>(p) = r;
+  }
   static __device__ __forceinline__ void unpack(const Raw& r, float* f) {
     T e[W];
     memcpy(e, &r, sizeof(r));

@@ -231,7 +231,7 @@ __global__ void __launch_bounds__(ST) sort_slots_kernel(
 template <typename I>
 __global__ void __launch_bounds__(ST) sort_ids_kernel(
     const I* __restrict__ ids, int n, int V, int bits, int passes, int2* a, int2* b,
-    int32_t* __restrict__ live_out, int* __restrict__ err) {
+    SortedHead* __restrict__ head, int* __restrict__ err) {
   extern __shared__ int sm[];
   __shared__ int warp_sums[32];
   __shared__ int bad_s;
@@ -283,12 +283,18 @@ __global__ void __launch_bounds__(ST) sort_ids_kernel(
     if (tid * 2 < bins) {
       off_s[tid * 2] = off + t.below[tid * 2];
       off_s[tid * 2 + 1] = off + total.x + t.below[tid * 2 + 1];
+      if (rank == 0 && p == passes - 1) {
+        head->top[tid * 2] = off;
+        head->top[tid * 2 + 1] = off + total.x;
+      }
     }
     if (p == 0 && rank == 0 && tid == 0) {
       int any = 0;
       for (uint32_t r = 0; r < nr; ++r) any |= ld_cluster(&bad_s, r);
       *err = any ? kErrBadRouting : 0;
-      *live_out = live;
+      head->live = live;
+      head->spans = head->long_spans = 0;
+      head->top[bins] = live;
     }
     __syncthreads();
     for (long long g = w0; g < w1; g += 32 * kBatch) {
@@ -386,13 +392,14 @@ cudaError_t launch_sort_slots(const int32_t* idx, int n, int E, int align, int c
 }
 
 cudaError_t launch_sort_ids(const void* ids, int ids_bytes, int n, int V, int2* scratch,
-                            int2* sorted, int32_t* live, int* err, cudaStream_t s) {
+                            int2* sorted, SortedHead* head, int* shift, int* err, cudaStream_t s) {
   int key_bits = 1;
   while (key_bits < 31 && (1LL << key_bits) < V) ++key_bits;
   int passes = (key_bits + 9) / 10;
   int bits = (key_bits + passes - 1) / passes;
+  *shift = (passes - 1) * bits;
   const int ctas = cluster_for(n);
-  void* args[] = {&ids, &n, &V, &bits, &passes, &scratch, &sorted, &live, &err};
+  void* args[] = {&ids, &n, &V, &bits, &passes, &scratch, &sorted, &head, &err};
   return launch_cluster(ids_bytes == 8 ? (const void*)sort_ids_kernel<int64_t>
                                        : (const void*)sort_ids_kernel<int32_t>,
                         ctas, table_bytes(1 << bits, 1), args, s);
