@@ -8,9 +8,9 @@
 // summed per thread over its columns, then over the threads in a fixed order, so
 // every result is bitwise reproducible.
 //
-// Both are bound by HBM.  A group of threads (a warp for short rows, a block for
-// long ones) owns a token: x[t] is read once for its R rows (row by row it would
-// be read R times, from all over the sorted order).
+// Both are bound by HBM.  A group of threads owns a token: x[t] is read once for
+// its R rows (row by row it would be read R times, from all over the sorted
+// order).
 #include <algorithm>
 
 #include "kernels.h"
@@ -21,6 +21,9 @@ namespace moe {
 namespace {
 constexpr int PT = 256;              // threads per block
 constexpr int kMaxR = 32;
+constexpr int kGroup = 128;          // threads per token of a long row
+// Threads of a block whose groups of G own a token each.
+constexpr int threads_of(int G) { return G > PT / 8 ? G : PT; }
 
 // Sums each of acc[0..RM) over the warp: every exchange halves the values a lane
 // still holds, RM - 1 + log2(32 / RM) shuffles instead of 5 RM.  Lane
@@ -44,7 +47,7 @@ __device__ __forceinline__ void warp_sums(float (&acc)[RM]) {
   for (; off > 0; off /= 2) acc[0] += __shfl_xor_sync(kFull, acc[0], off);
 }
 
-// dw[r] = acc[r] summed over the group (32 or PT threads); slots without a row
+// dw[r] = acc[r] summed over the group (32 or kGroup threads); slots without a row
 // get 0.  Ends with the group's threads in step when G > 32.
 template <int G, int RM>
 __device__ __forceinline__ void store_dots(float (&acc)[RM], const int* rows_s, int R, float* red,
@@ -67,21 +70,96 @@ __device__ __forceinline__ void store_dots(float (&acc)[RM], const int* rows_s, 
   }
 }
 
-template <typename T, int W, int G, int RM, bool DOTS>
+// Rows without a slot are zero.  They come in runs (the ends of segments), so
+// neighbouring rows go to different groups; a group looks at 32 rows at a time.
+template <typename T, int W, int G, int BT>
+__device__ __forceinline__ void zero_rows(const int32_t* __restrict__ row_slot, int N, int nv,
+                                          T* __restrict__ rows, long long ldr) {
+  constexpr int NG = BT / G;
+  using V = Vec<T, W>;
+  const int grp = threadIdx.x / G, gt = threadIdx.x % G, lane = threadIdx.x & 31;
+  const long long groups = (long long)gridDim.x * NG;
+  for (long long i = (long long)blockIdx.x * NG + grp; i < N; i += groups * 32) {
+    const long long mine = i + lane * groups;
+    unsigned empty = __ballot_sync(kFull, mine < N && row_slot[mine] < 0);
+    while (empty) {
+      const long long row = i + (__ffs(empty) - 1) * groups;
+      empty &= empty - 1;
+      for (int v = gt; v < nv; v += G) V::store(rows + row * ldr + (long long)v * W, V::zero());
+    }
+  }
+}
+
+// Spread without dot products: a warp takes 32 * kWide accesses of a token's row
+// and writes them to its R rows, 2 KB apiece where the row is long: the loads are
+// in flight together and a few tokens still fill the card.  T = 16384, d = 4096,
+// R = 8, weighted, segments of 128: 198 us for 1.34 GB; T = 128, d = 7168, 4864 rows:
+// 13 us, of which the zero rows are four fifths.
+constexpr int kWide = 4;
+
+template <typename T, int W>
 __global__ void __launch_bounds__(PT) spread_kernel(
+    const T* __restrict__ x, long long ldx, const float* __restrict__ w,
+    const int32_t* __restrict__ row_slot, const int32_t* __restrict__ slot_row, int T_, int d,
+    int R, int N, int cols, T* __restrict__ rows, long long ldr) {
+  using V = Vec<T, W>;
+  const int lane = threadIdx.x & 31;
+  const int nv = d / W;
+  const long long unit = (long long)blockIdx.x * (PT / 32) + threadIdx.x / 32;
+  const long long t = unit / cols;
+  if (t < T_) {
+    const int v0 = (int)(unit % cols) * (32 * kWide) + lane;
+    int my_row = -1;
+    float my_w = 1.f;
+    if (lane < R) {
+      my_row = slot_row[t * R + lane];
+      if (w) my_w = w[t * R + lane];
+    }
+    typename V::Raw q[kWide];
+#pragma unroll
+    for (int u = 0; u < kWide; ++u)
+      q[u] = v0 + 32 * u < nv ? V::load(x + t * ldx + (long long)(v0 + 32 * u) * W) : V::zero();
+    for (int r = 0; r < R; ++r) {
+      const int row = __shfl_sync(kFull, my_row, r);
+      const float wr = __shfl_sync(kFull, my_w, r);
+      if ((unsigned)row >= (unsigned)N) continue;
+      T* dst = rows + row * ldr;
+#pragma unroll
+      for (int u = 0; u < kWide; ++u) {
+        if (v0 + 32 * u >= nv) break;
+        if (w) {
+          float f[W];
+          V::unpack(q[u], f);
+#pragma unroll
+          for (int j = 0; j < W; ++j) f[j] *= wr;
+          V::store(dst + (long long)(v0 + 32 * u) * W, V::pack(f));
+        } else {
+          V::store(dst + (long long)(v0 + 32 * u) * W, q[u]);
+        }
+      }
+    }
+  }
+  if (nv > 128) zero_rows<T, W, PT, PT>(row_slot, N, nv, rows, ldr);
+  else zero_rows<T, W, 32, PT>(row_slot, N, nv, rows, ldr);
+}
+
+// Spread with dot products: a group of threads owns a token.
+template <typename T, int W, int G, int RM>
+__global__ void __launch_bounds__(threads_of(G)) spread_dots_kernel(
     const T* __restrict__ x, long long ldx, const float* __restrict__ w,
     const int32_t* __restrict__ row_slot, const int32_t* __restrict__ slot_row, int T_, int d,
     int R, int N, const T* __restrict__ other, long long ldo, T* __restrict__ rows,
     long long ldr, float* __restrict__ dw) {
-  constexpr int NG = PT / G;
+  constexpr int BT = threads_of(G), NG = BT / G;
   __shared__ int rows_s[NG][kMaxR];
   __shared__ float w_s[NG][kMaxR];
-  __shared__ float red[DOTS && G > 32 ? PT / 32 * RM : 1];
+  __shared__ float red[G > 32 ? G / 32 * RM : 1];
   using V = Vec<T, W>;
   const int grp = threadIdx.x / G, gt = threadIdx.x % G;
   const int nv = d / W;
   auto sync = [] { if (G == 32) __syncwarp(); else __syncthreads(); };
-  for (long long t = (long long)blockIdx.x * NG + grp; t < T_; t += (long long)gridDim.x * NG) {
+  const long long t = (long long)blockIdx.x * NG + grp;
+  if (t < T_) {
     if (gt < R) {
       const int row = slot_row[t * R + gt];
       rows_s[grp][gt] = (unsigned)row < (unsigned)N ? row : -1;
@@ -98,12 +176,10 @@ __global__ void __launch_bounds__(PT) spread_kernel(
       for (int r0 = 0; r0 < RM; r0 += 4) {
         if (r0 >= R) break;
         typename V::Raw q[4];
-        if (DOTS) {
 #pragma unroll
-          for (int u = 0; u < 4; ++u) {
-            const int row = r0 + u < R ? rows_s[grp][r0 + u] : -1;
-            q[u] = row >= 0 ? V::load(other + row * ldo + (long long)v * W) : V::zero();
-          }
+        for (int u = 0; u < 4; ++u) {
+          const int row = r0 + u < R ? rows_s[grp][r0 + u] : -1;
+          q[u] = row >= 0 ? V::load(other + row * ldo + (long long)v * W) : V::zero();
         }
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
@@ -112,51 +188,37 @@ __global__ void __launch_bounds__(PT) spread_kernel(
           const int row = rows_s[grp][r];
           if (row < 0) continue;
           const float wr = w_s[grp][r];
-          float out[W];
+          float out[W], o[W];
+          V::unpack(q[u], o);
 #pragma unroll
-          for (int j = 0; j < W; ++j) out[j] = wr * g[j];
-          V::store(rows + row * ldr + (long long)v * W, V::pack(out));
-          if (DOTS) {
-            float o[W];
-            V::unpack(q[u], o);
-#pragma unroll
-            for (int j = 0; j < W; ++j) acc[r] = fmaf(g[j], o[j], acc[r]);
+          for (int j = 0; j < W; ++j) {
+            out[j] = wr * g[j];
+            acc[r] = fmaf(g[j], o[j], acc[r]);
           }
+          V::store(rows + row * ldr + (long long)v * W, V::pack(out));
         }
       }
     }
-    if (DOTS) store_dots<G, RM>(acc, rows_s[grp], R, red, dw + t * R);
-    sync();
+    store_dots<G, RM>(acc, rows_s[grp], R, red, dw + t * R);
   }
-  // Rows without a slot are zero.  They come in runs (the ends of segments), so
-  // neighbouring rows go to different groups; a group looks at 32 rows at a time.
-  const int lane = threadIdx.x & 31;
-  const long long groups = (long long)gridDim.x * NG;
-  for (long long i = (long long)blockIdx.x * NG + grp; i < N; i += groups * 32) {
-    const long long mine = i + lane * groups;
-    unsigned empty = __ballot_sync(kFull, mine < N && row_slot[mine] < 0);
-    while (empty) {
-      const long long row = i + (__ffs(empty) - 1) * groups;
-      empty &= empty - 1;
-      for (int v = gt; v < nv; v += G) V::store(rows + row * ldr + (long long)v * W, V::zero());
-    }
-  }
+  zero_rows<T, W, G, BT>(row_slot, N, nv, rows, ldr);
 }
 
 template <typename T, int W, int G, int RM, bool DOTS>
-__global__ void __launch_bounds__(PT) collect_kernel(
+__global__ void __launch_bounds__(threads_of(G)) collect_kernel(
     const T* __restrict__ rows, long long ldr, const int32_t* __restrict__ slot_row,
     const float* __restrict__ w, int T_, int d, int R, int N, const T* __restrict__ other,
     long long ldo, T* __restrict__ y, long long ldy, float* __restrict__ dw) {
-  constexpr int NG = PT / G;
+  constexpr int BT = threads_of(G), NG = BT / G;
   __shared__ int rows_s[NG][kMaxR];
   __shared__ float w_s[NG][kMaxR];
-  __shared__ float red[DOTS && G > 32 ? PT / 32 * RM : 1];
+  __shared__ float red[DOTS && G > 32 ? G / 32 * RM : 1];
   using V = Vec<T, W>;
   const int grp = threadIdx.x / G, gt = threadIdx.x % G;
   const int nv = d / W;
   auto sync = [] { if (G == 32) __syncwarp(); else __syncthreads(); };
-  for (long long t = (long long)blockIdx.x * NG + grp; t < T_; t += (long long)gridDim.x * NG) {
+  const long long t = (long long)blockIdx.x * NG + grp;
+  if (t < T_) {
     if (gt < R) {
       const int row = slot_row[t * R + gt];
       rows_s[grp][gt] = (unsigned)row < (unsigned)N ? row : -1;
@@ -197,53 +259,65 @@ __global__ void __launch_bounds__(PT) collect_kernel(
       V::store(y + t * ldy + (long long)v * W, V::pack(sum));
     }
     if (DOTS) store_dots<G, RM>(acc, rows_s[grp], R, red, dw + t * R);
-    sync();
   }
 }
 
-template <typename T, int W, int G, int RM>
+template <typename T, int W>
 cudaError_t spread_t(const PermuteArgs& a, cudaStream_t s) {
+  const int cols = std::max(1, (a.d / W + 32 * kWide - 1) / (32 * kWide));
+  const long long warps = std::max((long long)a.T * cols, (a.N + 3LL) / 4);
+  const int blocks = (int)((warps + PT / 32 - 1) / (PT / 32));
+  spread_kernel<T, W><<<blocks, PT, 0, s>>>((const T*)a.tok.p, a.tok.ld, a.w, a.row_slot,
+                                            a.slot_row, a.T, a.d, a.R, a.N, cols, (T*)a.out.p,
+                                            a.out.ld);
+  count_launches(1);
+  return cudaGetLastError();
+}
+
+template <typename T, int W, int G, int RM>
+cudaError_t spread_dots_t(const PermuteArgs& a, cudaStream_t s) {
   const long long units = std::max<long long>(a.T, (a.N + 7) / 8);
-  const int blocks = (int)((units + PT / G - 1) / (PT / G));
-  if (a.dw)
-    spread_kernel<T, W, G, RM, true><<<blocks, PT, 0, s>>>(
-        (const T*)a.tok.p, a.tok.ld, a.w, a.row_slot, a.slot_row, a.T, a.d, a.R, a.N,
-        (const T*)a.other.p, a.other.ld, (T*)a.out.p, a.out.ld, a.dw);
-  else
-    spread_kernel<T, W, G, RM, false><<<blocks, PT, 0, s>>>(
-        (const T*)a.tok.p, a.tok.ld, a.w, a.row_slot, a.slot_row, a.T, a.d, a.R, a.N, nullptr, 0,
-        (T*)a.out.p, a.out.ld, nullptr);
+  constexpr int BT = threads_of(G);
+  const int blocks = (int)((units + BT / G - 1) / (BT / G));
+  spread_dots_kernel<T, W, G, RM><<<blocks, BT, 0, s>>>(
+      (const T*)a.tok.p, a.tok.ld, a.w, a.row_slot, a.slot_row, a.T, a.d, a.R, a.N,
+      (const T*)a.other.p, a.other.ld, (T*)a.out.p, a.out.ld, a.dw);
   count_launches(1);
   return cudaGetLastError();
 }
 
 template <typename T, int W, int G, int RM>
 cudaError_t collect_t(const PermuteArgs& a, cudaStream_t s) {
-  const int blocks = (int)(((long long)a.T + PT / G - 1) / (PT / G));
+  constexpr int BT = threads_of(G);
+  const int blocks = (int)(((long long)a.T + BT / G - 1) / (BT / G));
   if (a.dw)
-    collect_kernel<T, W, G, RM, true><<<blocks, PT, 0, s>>>(
+    collect_kernel<T, W, G, RM, true><<<blocks, BT, 0, s>>>(
         (const T*)a.tok.p, a.tok.ld, a.slot_row, a.w, a.T, a.d, a.R, a.N, (const T*)a.other.p,
         a.other.ld, (T*)a.out.p, a.out.ld, a.dw);
   else
-    collect_kernel<T, W, G, RM, false><<<blocks, PT, 0, s>>>(
+    collect_kernel<T, W, G, RM, false><<<blocks, BT, 0, s>>>(
         (const T*)a.tok.p, a.tok.ld, a.slot_row, a.w, a.T, a.d, a.R, a.N, nullptr, 0,
         (T*)a.out.p, a.out.ld, nullptr);
   count_launches(1);
   return cudaGetLastError();
 }
 
-// A block per token for rows of over 128 accesses, a warp for shorter ones.  At
-// T = 16384, d = 4096 bf16 a block takes 362 us for moe_unpermute_bwd and a warp
-// 373, at T = 4096, d = 2048 moe_permute_bwd 29 and 40 us: a warp's rows wait for
-// one another.
+// A block of 128 per token for rows of over 128 accesses, a warp for shorter ones.
+// moe_permute_bwd, T = 4096, d = 2048, R = 6: 23 us (a warp 40, a block of 256 29:
+// few blocks fit an SM and each waits for its one round of loads);
+// moe_unpermute_bwd, T = 16384, d = 4096, R = 8: 356 us (373, 361);
+// moe_unpermute, T = 65536, d = 7168, R = 8: 1.16 ms (1.23, 1.17).  A block takes one
+// token: persistent blocks were 5 to 15% slower, with or without the next token's
+// plan read ahead.
 template <typename T, int W> cudaError_t by_shape(const PermuteArgs& a, bool spread, cudaStream_t s) {
+  if (spread && !a.dw) return spread_t<T, W>(a, s);
   const bool wide = a.d / W > 128;
   if (a.R <= 8) {
-    if (spread) return wide ? spread_t<T, W, PT, 8>(a, s) : spread_t<T, W, 32, 8>(a, s);
-    return wide ? collect_t<T, W, PT, 8>(a, s) : collect_t<T, W, 32, 8>(a, s);
+    if (spread) return wide ? spread_dots_t<T, W, kGroup, 8>(a, s) : spread_dots_t<T, W, 32, 8>(a, s);
+    return wide ? collect_t<T, W, kGroup, 8>(a, s) : collect_t<T, W, 32, 8>(a, s);
   }
-  if (spread) return wide ? spread_t<T, W, PT, 32>(a, s) : spread_t<T, W, 32, 32>(a, s);
-  return wide ? collect_t<T, W, PT, 32>(a, s) : collect_t<T, W, 32, 32>(a, s);
+  if (spread) return wide ? spread_dots_t<T, W, kGroup, 32>(a, s) : spread_dots_t<T, W, 32, 32>(a, s);
+  return wide ? collect_t<T, W, kGroup, 32>(a, s) : collect_t<T, W, 32, 32>(a, s);
 }
 
 template <typename T> cudaError_t by_width(const PermuteArgs& a, bool spread, cudaStream_t s) {

@@ -6,13 +6,14 @@
 // keys into its own row of a shared-memory table [16 warps][bins]; a prefix
 // over the warps, then over the CTAs (each CTA reads the others' totals through
 // distributed shared memory) and over the bins gives every warp its first
-// position in every bin.  The warps then walk their ranges once more:
-// __match_any_sync ranks equal keys inside a group of 32, so positions follow
-// the keys' order and no atomic decides one.
+// position in every bin.  The warps then walk their ranges once more: ballots
+// rank equal keys inside a group of 32, so positions follow the keys' order and
+// no atomic decides one.
 //
-// One launch does the whole plan.  Separate histogram, scan and rank launches
-// cost about 2 us each in launch latency; the cluster barrier costs well under
-// one.
+// One launch does the whole plan: separate histogram, scan and rank launches
+// would add their latencies.  Bound by latency, 1024 slots over 256 experts take
+// 5.0 us, 131072 over 128 12.5 us, 524288 over 256 37 us (3% of moving their rows
+// of 7168 bf16).
 #include "common.cuh"
 #include "kernels.h"
 #include "sort.cuh"
@@ -104,26 +105,35 @@ __device__ __forceinline__ int2 cluster_totals(const Table& t, int bins, uint32_
   cluster_wait();
   int2 total = make_int2(0, 0), before = make_int2(0, 0);
   if (b < bins) {
-#pragma unroll 4
-    for (uint32_t r = 0; r < nr; ++r) {
-      const int2 c = ld_cluster2(t.mine + b, r);
+    int2 c[kMaxCluster];          // all reads in flight together
+#pragma unroll
+    for (uint32_t r = 0; r < kMaxCluster; ++r)
+      c[r] = r < nr ? ld_cluster2(t.mine + b, r) : make_int2(0, 0);
+#pragma unroll
+    for (uint32_t r = 0; r < kMaxCluster; ++r) {
       if (r < rank) {
-        before.x += c.x;
-        before.y += c.y;
+        before.x += c[r].x;
+        before.y += c[r].y;
       }
-      total.x += c.x;
-      total.y += c.y;
+      total.x += c[r].x;
+      total.y += c[r].y;
     }
     *reinterpret_cast<int2*>(t.below + b) = before;
   }
   return total;
 }
 
-// Position of `key` (this lane's, -1 for none) among the keys of its bin in the
-// warp's range so far; counts them in `my`.
-__device__ __forceinline__ int warp_rank(int key, int* my) {
+// Position of `key` (this lane's, -1 for none, else below 2^bits) among the keys of
+// its bin in the warp's range so far; counts them in `my`.  A ballot per bit finds
+// the equal keys; __match_any_sync took 44 us, this 37, for 524288 keys.
+__device__ __forceinline__ int warp_rank(int key, int* my, int bits) {
   const int lane = threadIdx.x & 31;
-  const unsigned peers = __match_any_sync(kFull, key);
+  unsigned peers = __ballot_sync(kFull, key >= 0);
+  for (int b = 0; b < bits; ++b) {
+    const bool one = key >> b & 1;
+    const unsigned ones = __ballot_sync(kFull, one);
+    peers &= one ? ones : ~ones;
+  }
   int pos = 0;
   if (key >= 0) pos = my[key] + __popc(peers & ((1u << lane) - 1u));
   __syncwarp();
@@ -141,14 +151,15 @@ __global__ void __launch_bounds__(ST) sort_slots_kernel(
   __shared__ int warp_sums[32];
   __shared__ int bad_s;
   const uint32_t rank = cluster_rank(), nr = cluster_size();
-  const int bins = (E + 1) & ~1;
+  const int bins = (E + 1) & ~1, bits = 32 - __clz(E - 1);
   Table t{sm, sm + SW * bins, sm + SW * bins + bins};
-  int* kept_s = sm + SW * bins + 2 * bins;   // [bins]
-  int* off_s = kept_s + bins;                // [bins]
+  int* last_s = sm + SW * bins + 2 * bins;   // [bins] past the last row of the bin
+  int* off_s = last_s + bins;                // [bins] the bin's first row, then this CTA's
   const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
   if (tid == 0) bad_s = 0;
-  for (int i = tid; i < SW * bins; i += ST) t.wcnt[i] = 0;
-  __syncthreads();
+  for (int i = tid; i < SW * bins / 2; i += ST) reinterpret_cast<int2*>(t.wcnt)[i] = make_int2(0, 0);
+  // rows without a slot keep this; the others are written after the cluster's barrier
+  for (long long r = (long long)rank * ST + tid; r < N; r += (long long)nr * ST) row_slot[r] = -1;
   const int per_warp = share / SW;
   const long long w0 = (long long)rank * share + (long long)wid * per_warp;
   const long long w1 = min((long long)n, w0 + per_warp);
@@ -161,11 +172,20 @@ __global__ void __launch_bounds__(ST) sort_slots_kernel(
     }
   };
   bool bad = false;
+  int early[kBatch];            // the first batch stays in registers for the second walk
+  load(w0, early);
+  __syncthreads();
   for (long long g = w0; g < w1; g += 32 * kBatch) {
     int e[kBatch];
-    load(g, e);
+    if (g == w0) {
+#pragma unroll
+      for (int j = 0; j < kBatch; ++j) e[j] = early[j];
+    } else {
+      load(g, e);
+    }
 #pragma unroll
     for (int j = 0; j < kBatch; ++j) {
+      if (g + 32 * j >= w1) break;
       if ((unsigned)e[j] < (unsigned)E) atomicAdd(&my[e[j]], 1);
       else bad |= e[j] != -1;
     }
@@ -187,8 +207,9 @@ __global__ void __launch_bounds__(ST) sort_slots_kernel(
   int end;
   const int off = block_scan(padded.x + padded.y, warp_sums, &end);
   if (b < bins) {
-    *reinterpret_cast<int2*>(kept_s + b) = kept;
-    *reinterpret_cast<int2*>(off_s + b) = make_int2(off, off + padded.x);
+    const int2 before = *reinterpret_cast<const int2*>(t.below + b);
+    *reinterpret_cast<int2*>(last_s + b) = make_int2(off + kept.x, off + padded.x + kept.y);
+    *reinterpret_cast<int2*>(off_s + b) = make_int2(off + before.x, off + padded.x + before.y);
     if (rank == 0) {
       counts[b] = kept.x;
       offsets[b] = off;
@@ -202,28 +223,27 @@ __global__ void __launch_bounds__(ST) sort_slots_kernel(
   __syncthreads();
   for (long long g = w0; g < w1; g += 32 * kBatch) {
     int e[kBatch];
-    load(g, e);
+    if (g == w0) {
+#pragma unroll
+      for (int j = 0; j < kBatch; ++j) e[j] = early[j];
+    } else {
+      load(g, e);
+    }
 #pragma unroll
     for (int j = 0; j < kBatch; ++j) {
       const long long i = g + 32 * j + lane;
       if (g + 32 * j >= w1) break;       // the same for the whole warp
       if ((unsigned)e[j] >= (unsigned)E) e[j] = -1;
-      const int pos = warp_rank(e[j], my);
+      const int pos = warp_rank(e[j], my, bits);
       int row = -1;
       if (e[j] >= 0) {
-        const int p = t.below[e[j]] + pos;
-        if (p < kept_s[e[j]]) row = off_s[e[j]] + p;
+        row = off_s[e[j]] + pos;
+        if (row >= last_s[e[j]]) row = -1;
       }
       if (i < w1) slot_row[i] = row;
       if (row >= 0) row_slot[row] = (int)i;
     }
   }
-  // rows without a slot: the ends of the segments, and what follows the last one
-  for (int e = (int)rank * SW + wid; e < E; e += (int)nr * SW) {
-    const int last = e + 1 < E ? off_s[e + 1] : end;
-    for (int r = off_s[e] + kept_s[e] + lane; r < last; r += 32) row_slot[r] = -1;
-  }
-  for (int r = end + (int)rank * ST + tid; r < N; r += (int)nr * ST) row_slot[r] = -1;
   cluster_wait();   // no CTA leaves while another still reads its totals
 }
 
@@ -248,8 +268,8 @@ __global__ void __launch_bounds__(ST) sort_ids_kernel(
     int2* dst = (passes - 1 - p) & 1 ? a : b;
     const int2* src = dst == a ? b : a;
     const int shift = p * bits;
-    for (int i = tid; i < SW * bins; i += ST) t.wcnt[i] = 0;
-    __syncthreads();
+    for (int i = tid; i < SW * bins / 2; i += ST)
+      reinterpret_cast<int2*>(t.wcnt)[i] = make_int2(0, 0);
     const int per_warp = ((count + (int)nr * SW - 1) / ((int)nr * SW) + 31) / 32 * 32;
     const long long w0 = ((long long)rank * SW + wid) * per_warp;
     const long long w1 = min((long long)count, w0 + per_warp);
@@ -269,9 +289,17 @@ __global__ void __launch_bounds__(ST) sort_ids_kernel(
         }
       }
     };
+    int2 early[kBatch];           // the first batch stays in registers for the second walk
+    load(w0, early);
+    __syncthreads();
     for (long long g = w0; g < w1; g += 32 * kBatch) {
       int2 kv[kBatch];
-      load(g, kv);
+      if (g == w0) {
+#pragma unroll
+        for (int j = 0; j < kBatch; ++j) kv[j] = early[j];
+      } else {
+        load(g, kv);
+      }
 #pragma unroll
       for (int j = 0; j < kBatch; ++j)
         if (kv[j].x >= 0) atomicAdd(&my[(kv[j].x >> shift) & (bins - 1)], 1);
@@ -299,12 +327,17 @@ __global__ void __launch_bounds__(ST) sort_ids_kernel(
     __syncthreads();
     for (long long g = w0; g < w1; g += 32 * kBatch) {
       int2 kv[kBatch];
-      load(g, kv);
+      if (g == w0) {
+#pragma unroll
+        for (int j = 0; j < kBatch; ++j) kv[j] = early[j];
+      } else {
+        load(g, kv);
+      }
 #pragma unroll
       for (int j = 0; j < kBatch; ++j) {
         if (g + 32 * j >= w1) break;     // the same for the whole warp
         const int bin = kv[j].x >= 0 ? (kv[j].x >> shift) & (bins - 1) : -1;
-        const int pos = warp_rank(bin, my);
+        const int pos = warp_rank(bin, my, bits);
         if (bin >= 0) __stcg(&dst[off_s[bin] + pos], kv[j]);
       }
     }
