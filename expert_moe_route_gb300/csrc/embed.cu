@@ -103,7 +103,6 @@ __global__ void __launch_bounds__(RT) rows_kernel(
     Span* spans) {
   using In = typename Vec<T, W>::Raw;
   constexpr bool kAsync = sizeof(In) >= 4;   // a 2-byte access has no asynchronous copy
-  constexpr bool kRed = ADD && W >= 4 && sizeof(O) == 4;   // added to by the memory
   __shared__ In slots[RT / 32][kFlight][32];
   wait_for_previous();
   let_next_start();
@@ -167,6 +166,16 @@ __global__ void __launch_bounds__(RT) rows_kernel(
   for (int j = 0; j < W; ++j) acc[j] = 0.f;
 #pragma unroll 1
   for (int i0 = 0; i0 < count; i0 += kGroup) {
+    typename Vec<O, W>::Raw old[ADD ? kGroup : 1];   // what the rows that end here hold
+    if (ADD) {
+#pragma unroll
+      for (int u = 0; u < kGroup; ++u) {
+        const int id = __shfl_sync(kFull, kv.x, i0 + u);
+        old[u] = here && (ends >> (i0 + u) & 1)
+                     ? Vec<O, W>::load_rw(dtable + id * ldt + (long long)v * W)
+                     : Vec<O, W>::zero();
+      }
+    }
     asm volatile("cp.async.wait_group %0;" ::"n"(kFlight / kGroup - 1) : "memory");
 #pragma unroll
     for (int u = 0; u < kGroup; ++u) {
@@ -183,20 +192,10 @@ __global__ void __launch_bounds__(RT) rows_kernel(
         Vec<float, W>::store(parts + (2LL * k + (inherited ? 0 : 1)) * d + (long long)v * W,
                              Vec<float, W>::pack(acc));
       } else if (here) {
-        O* dst = dtable + id * ldt + (long long)v * W;
+        if (ADD) Vec<O, W>::unpack(old[ADD ? u : 0], f);
 #pragma unroll
-        for (int j = 0; j < W; ++j) acc[j] *= scale;
-        if constexpr (kRed) {
-#pragma unroll
-          for (int j = 0; j < W; j += 4) add4_in_memory(dst + j, acc + j);
-        } else {
-          if (ADD) {
-            Vec<O, W>::unpack(Vec<O, W>::load_rw(dst), f);
-#pragma unroll
-            for (int j = 0; j < W; ++j) acc[j] += f[j];
-          }
-          Vec<O, W>::store(dst, Vec<O, W>::pack(acc));
-        }
+        for (int j = 0; j < W; ++j) acc[j] = ADD ? acc[j] * scale + f[j] : acc[j] * scale;
+        Vec<O, W>::store(dtable + id * ldt + (long long)v * W, Vec<O, W>::pack(acc));
       }
 #pragma unroll
       for (int j = 0; j < W; ++j) acc[j] = 0.f;

@@ -35,11 +35,6 @@ __device__ __forceinline__ void store32(void* p, const Raw32& r) {
                "r"(r.a.y), "r"(r.a.z), "r"(r.a.w), "r"(r.b.x), "r"(r.b.y), "r"(r.b.z), "r"(r.b.w)
                : "memory");
 }
-// p[0..3] += f[0..3] in memory (fp32, 16-byte aligned; a sum below 2^-126 may become 0).
-__device__ __forceinline__ void add4_in_memory(float* p, const float* f) {
-  asm volatile("red.relaxed.gpu.global.add.v4.f32 [%0], {%1, %2, %3, %4};" ::"l"(p), "f"(f[0]),
-               "f"(f[1]), "f"(f[2]), "f"(f[3]) : "memory");
-}
 template <int BYTES> struct RawOf;
 template <> struct RawOf<32> { using type = Raw32; };
 template <> struct RawOf<16> { using type = uint4; };
