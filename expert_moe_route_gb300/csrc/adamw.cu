@@ -498,10 +498,39 @@ __global__ void __launch_bounds__(AT, 4) adamw8_kernel(const __grid_constant__ A
 // 553M fp32 gradients (2.2 GB) in 0.326 ms, 6.8 TB/s.
 __device__ __forceinline__ float square_add(float s, float g) { return fmaf(g, g, s); }
 
+// A sum as two fp32 numbers, hi + lo: an addition's rounding error is itself an
+// fp32 number and goes into lo, which leaves some 46 bits.  The card adds 64
+// fp32 numbers in the time of one fp64: with fp64 sums the norm of 12.6M gradients
+// spent 5 of its 18 us in them.
+struct Sum {
+  float hi, lo;
+  __device__ __forceinline__ void add(float x) {
+    const float s = __fadd_rn(hi, x), t = __fadd_rn(s, -hi);
+    lo += __fadd_rn(__fadd_rn(hi, -__fadd_rn(s, -t)), __fadd_rn(x, -t));
+    hi = s;
+  }
+  __device__ __forceinline__ void add(const Sum& o) {
+    add(o.hi);
+    lo += o.lo;
+  }
+  __device__ __forceinline__ void add_over_warp() {
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) {
+      Sum o;
+      o.hi = __shfl_xor_sync(kFull, hi, off);
+      o.lo = __shfl_xor_sync(kFull, lo, off);
+      // both lanes of a pair must add in the same order
+      Sum a = threadIdx.x & off ? o : *this;
+      a.add(threadIdx.x & off ? *this : o);
+      *this = a;
+    }
+  }
+};
+
 // Squares of four blocks' eight elements a lane (fp32: block b at p + 256 b), all
 // loads issued before the first is used: one instruction block, since the
 // compiler, free to choose, waits for each to save registers.
-__device__ __forceinline__ double squares32(const float* p) {
+__device__ __forceinline__ void squares32(const float* p, Sum& sum) {
   float f[4][8];
   asm volatile(
       "ld.global.v8.f32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%32];\n\t"
@@ -515,18 +544,16 @@ __device__ __forceinline__ double squares32(const float* p) {
         "=f"(f[3][0]), "=f"(f[3][1]), "=f"(f[3][2]), "=f"(f[3][3]), "=f"(f[3][4]), "=f"(f[3][5]),
         "=f"(f[3][6]), "=f"(f[3][7])
       : "l"(p));
-  double sum = 0.0;
 #pragma unroll
   for (int b = 0; b < 4; ++b) {
     float s = 0.f;
 #pragma unroll
     for (int j = 0; j < 8; ++j) s = square_add(s, f[b][j]);
-    sum += (double)s;
+    sum.add(s);
   }
-  return sum;
 }
 
-__device__ __forceinline__ double squares32(const uint16_t* p) {   // bf16
+__device__ __forceinline__ void squares32(const uint16_t* p, Sum& sum) {   // bf16
   uint4 q[4];
   asm volatile(
       "ld.global.v4.u32 {%0, %1, %2, %3}, [%16];\n\t"
@@ -537,78 +564,77 @@ __device__ __forceinline__ double squares32(const uint16_t* p) {   // bf16
         "=r"(q[1].z), "=r"(q[1].w), "=r"(q[2].x), "=r"(q[2].y), "=r"(q[2].z), "=r"(q[2].w),
         "=r"(q[3].x), "=r"(q[3].y), "=r"(q[3].z), "=r"(q[3].w)
       : "l"(p));
-  double sum = 0.0;
 #pragma unroll
   for (int b = 0; b < 4; ++b) {
     float f[8], s = 0.f;
     unpack8(q[b], f);
 #pragma unroll
     for (int j = 0; j < 8; ++j) s = square_add(s, f[j]);
-    sum += (double)s;
+    sum.add(s);
   }
-  return sum;
 }
 
 template <bool WIDE>
-__device__ __forceinline__ double squares8(const NormEntry& e, long long base, int left) {
+__device__ __forceinline__ float squares8(const NormEntry& e, long long base, int left) {
   const Lane<WIDE> l{(int)(threadIdx.x & 31), left};
   float g[8], s = 0.f;
   if (e.kind & kG16) l.get((const uint16_t*)e.g + base, g);
   else l.get((const float*)e.g + base, g);
 #pragma unroll
   for (int j = 0; j < 8; ++j) s = square_add(s, g[j]);
-  return (double)s;
+  return s;
 }
 
-// Block b's sum of squares over its chunks: fp32 over a thread's eight elements
-// of a chunk, double from there.
+// Block b's sum of squares over its chunks.
 __global__ void __launch_bounds__(AT) square_sums_kernel(const __grid_constant__ NormTable t,
-                                                         double* __restrict__ sums) {
-  __shared__ double red[AT / 32];
+                                                         float2* __restrict__ sums) {
+  __shared__ Sum red[AT / 32];
   const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
-  double sum = 0.0;
+  let_next_start();
+  Sum sum{0.f, 0.f};
   Walk w;
   for (w.c = blockIdx.x; w.at(t); w.c += gridDim.x) {
     const NormEntry& e = t.e[w.k];
     const bool wide = e.kind & kWide;
     if (wide && w.left == kBlock * kNormRun) {
       const long long i = w.base + lane * 8;
-      sum += e.kind & kG16 ? squares32((const uint16_t*)e.g + i) : squares32((const float*)e.g + i);
+      if (e.kind & kG16) squares32((const uint16_t*)e.g + i, sum);
+      else squares32((const float*)e.g + i, sum);
       continue;
     }
     for (; w.left > 0; w.left -= kBlock, w.base += kBlock)
-      sum += wide && w.left >= kBlock ? squares8<true>(e, w.base, kBlock)
-                                      : squares8<false>(e, w.base, w.left);
+      sum.add(wide && w.left >= kBlock ? squares8<true>(e, w.base, kBlock)
+                                       : squares8<false>(e, w.base, w.left));
   }
-#pragma unroll
-  for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(kFull, sum, off);
+  sum.add_over_warp();
   if (lane == 0) red[wid] = sum;
   __syncthreads();
   if (threadIdx.x == 0) {
-    double total = 0.0;
-    for (int w = 0; w < AT / 32; ++w) total += red[w];
-    sums[blockIdx.x] = total;
+    for (int k = 1; k < AT / 32; ++k) sum.add(red[k]);
+    sums[blockIdx.x] = make_float2(sum.hi, sum.lo);
   }
 }
 
-__global__ void __launch_bounds__(kNormThreads) norm_kernel(const double* sums, int n,
+__global__ void __launch_bounds__(kNormThreads) norm_kernel(const float2* sums, int n,
                                                             float max_norm, float* norm) {
-  __shared__ double red[kNormThreads / 32];
+  __shared__ Sum red[kNormThreads / 32];
   const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
   wait_for_previous();
-  double s = 0.0;
+  Sum sum{0.f, 0.f};
 #pragma unroll 4
-  for (int i = threadIdx.x; i < n; i += kNormThreads) s += sums[i];
-#pragma unroll
-  for (int off = 16; off > 0; off >>= 1) s += __shfl_xor_sync(kFull, s, off);
-  if (lane == 0) red[wid] = s;
+  for (int i = threadIdx.x; i < n; i += kNormThreads) {
+    const float2 s = sums[i];
+    sum.add(s.x);
+    sum.lo += s.y;
+  }
+  sum.add_over_warp();
+  if (lane == 0) red[wid] = sum;
   __syncthreads();
   if (wid > 0) return;
-  s = red[lane];
-#pragma unroll
-  for (int off = 16; off > 0; off >>= 1) s += __shfl_xor_sync(kFull, s, off);
+  sum = red[lane];
+  sum.add_over_warp();
   if (lane == 0) {
-    const float v = (float)sqrt(s);
+    const float v = (float)sqrt((double)sum.hi + (double)sum.lo);
     norm[0] = v;
     norm[1] = max_norm > 0.f ? fminf(max_norm / (v + 1e-6f), 1.f) : 1.f;
     norm[2] = isfinite(v) ? 1.f : 0.f;
@@ -658,12 +684,12 @@ cudaError_t in_runs(const moe_adamw_tensor_t* x, int n, F launch) {
 size_t grad_norm_ws_bytes(const moe_adamw_tensor_t* x, int n) {
   int runs = 0;
   (void)in_runs(x, n, [&](int, int) { ++runs; return cudaSuccess; });
-  return align_up(sizeof(double) * kNormBlocks * (size_t)(runs > 0 ? runs : 1), 256);
+  return align_up(sizeof(float2) * kNormBlocks * (size_t)(runs > 0 ? runs : 1), 256);
 }
 
 cudaError_t launch_grad_norm(const moe_adamw_tensor_t* x, int n, float max_norm, float* norm,
                              void* ws, cudaStream_t s) {
-  double* sums = static_cast<double*>(ws);
+  float2* sums = static_cast<float2*>(ws);
   int used = 0;
   const cudaError_t e = in_runs(x, n, [&](int i, int j) {
     NormTable t;
