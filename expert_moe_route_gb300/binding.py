@@ -434,15 +434,16 @@ def _rows(t, name, dtype=None):
         return None, 0
     if not t.is_cuda:
         raise ValueError(f"{name} must live on a CUDA device")
-    if t.dim() != 2 or (t.stride(1) != 1 and t.shape[1] > 1):
+    shape, stride = t.shape, t.stride()
+    if len(shape) != 2 or (stride[1] != 1 and shape[1] > 1):
         raise ValueError(f"{name} must be a matrix with contiguous rows")
-    if t.dtype not in DTYPES or (dtype is not None and t.dtype != dtype):
+    if t.dtype is not dtype and (dtype is not None or t.dtype not in DTYPES):
         raise TypeError(f"{name} must be {dtype or 'bf16, fp16 or fp32'}, got {t.dtype}")
-    return t.data_ptr(), t.stride(0) if t.shape[0] > 1 else t.shape[1]
+    return t.data_ptr(), stride[0] if shape[0] > 1 else shape[1]
 
 
 def _shape(t, shape, name):
-    if t is not None and tuple(t.shape) != tuple(shape):
+    if t is not None and t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
 
 
@@ -466,9 +467,12 @@ def moe_sort(topk_idx, E, counts, offsets, row_slot, slot_row, ws, align=1, capa
     """Plan of an expert sort (see include/moe.h); row_slot has at least
     sort_rows_bound(T, R, E, align, capacity) entries."""
     T, R = topk_idx.shape
-    for name, t in (("topk_idx", topk_idx), ("counts", counts), ("offsets", offsets),
-                    ("row_slot", row_slot), ("slot_row", slot_row)):
-        _dt(t, torch.int32, name)
+    i32 = torch.int32
+    if not (topk_idx.dtype is i32 and counts.dtype is i32 and offsets.dtype is i32
+            and row_slot.dtype is i32 and slot_row.dtype is i32):
+        for name, t in (("topk_idx", topk_idx), ("counts", counts), ("offsets", offsets),
+                        ("row_slot", row_slot), ("slot_row", slot_row)):
+            _dt(t, i32, name)
     _shape(counts, (E,), "counts"); _shape(offsets, (E + 1,), "offsets")
     if slot_row.numel() != T * R:
         raise ValueError(f"slot_row must have {T * R} entries")
@@ -480,13 +484,17 @@ def moe_sort(topk_idx, E, counts, offsets, row_slot, slot_row, ws, align=1, capa
 
 
 def _plan_args(T, N, w, slot_row, row_slot=None):
-    _dt(slot_row, torch.int32, "slot_row"); _dt(row_slot, torch.int32, "row_slot")
-    _dt(w, torch.float32, "w")
-    if slot_row.dim() != 2 or slot_row.shape[0] != T:
+    _dt(slot_row, torch.int32, "slot_row")
+    shape = slot_row.shape
+    if len(shape) != 2 or shape[0] != T:
         raise ValueError(f"slot_row must have shape ({T}, R)")
-    _shape(w, slot_row.shape, "w")
-    _shape(row_slot, (N,), "row_slot")
-    return slot_row.shape[1]
+    if w is not None:
+        _dt(w, torch.float32, "w")
+        _shape(w, shape, "w")
+    if row_slot is not None:
+        _dt(row_slot, torch.int32, "row_slot")
+        _shape(row_slot, (N,), "row_slot")
+    return shape[1]
 
 
 def moe_permute(x, w, row_slot, slot_row, rows, stream=None):

@@ -302,7 +302,10 @@ cudaError_t collect_t(const PermuteArgs& a, cudaStream_t s) {
   return cudaGetLastError();
 }
 
-// A block of 128 per token for rows of over 128 accesses, a warp for shorter ones.
+// A block of 128 per token for rows of over 128 accesses, a warp for shorter ones
+// (d = 512, T = 16384, R = 8, moe_unpermute_bwd: 51 us, a block 72) unless the tokens
+// are so few that a warp each does not fill the card (d = 1024, T = 512: 6.2 us, a
+// warp 10.3).
 // moe_permute_bwd, T = 4096, d = 2048, R = 6: 23 us (a warp 40, a block of 256 29:
 // few blocks fit an SM and each waits for its one round of loads);
 // moe_unpermute_bwd, T = 16384, d = 4096, R = 8: 356 us (373, 361);
@@ -311,7 +314,7 @@ cudaError_t collect_t(const PermuteArgs& a, cudaStream_t s) {
 // plan read ahead.
 template <typename T, int W> cudaError_t by_shape(const PermuteArgs& a, bool spread, cudaStream_t s) {
   if (spread && !a.dw) return spread_t<T, W>(a, s);
-  const bool wide = a.d / W > 128;
+  const bool wide = a.d / W > 128 || (a.d / W > 32 && a.T < 152 * 16);
   if (a.R <= 8) {
     if (spread) return wide ? spread_dots_t<T, W, kGroup, 8>(a, s) : spread_dots_t<T, W, 32, 8>(a, s);
     return wide ? collect_t<T, W, kGroup, 8>(a, s) : collect_t<T, W, 32, 8>(a, s);
