@@ -116,8 +116,11 @@ __global__ void __launch_bounds__(RT) rows_kernel(
     for (int k = 0; k < kOwn && r0 + k < V; ++k) {
       if (__shfl_sync(kFull, lo, k) != __shfl_sync(kFull, hi, k)) continue;
       O* dst = dtable + (r0 + k) * ldt;
-      for (int v = lane; v < nv; v += 32)
-        Vec<O, W>::store(dst + (long long)v * W, Vec<O, W>::zero());
+      if (W * sizeof(O) >= 16)
+        for (int v = lane; v < nv; v += 32)
+          Vec<O, W>::store(dst + (long long)v * W, Vec<O, W>::zero());
+      else
+        zero_span<O, 32>(dst, d, lane);
     }
     return;
   }

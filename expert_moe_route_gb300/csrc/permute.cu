@@ -72,11 +72,10 @@ __device__ __forceinline__ void store_dots(float (&acc)[RM], const int* rows_s, 
 
 // Rows without a slot are zero.  They come in runs (the ends of segments), so
 // neighbouring rows go to different groups; a group looks at 32 rows at a time.
-template <typename T, int W, int G, int BT>
-__device__ __forceinline__ void zero_rows(const int32_t* __restrict__ row_slot, int N, int nv,
+template <typename T, int G, int BT>
+__device__ __forceinline__ void zero_rows(const int32_t* __restrict__ row_slot, int N, int d,
                                           T* __restrict__ rows, long long ldr) {
   constexpr int NG = BT / G;
-  using V = Vec<T, W>;
   const int grp = threadIdx.x / G, gt = threadIdx.x % G, lane = threadIdx.x & 31;
   const long long groups = (long long)gridDim.x * NG;
   for (long long i = (long long)blockIdx.x * NG + grp; i < N; i += groups * 32) {
@@ -85,7 +84,7 @@ __device__ __forceinline__ void zero_rows(const int32_t* __restrict__ row_slot, 
     while (empty) {
       const long long row = i + (__ffs(empty) - 1) * groups;
       empty &= empty - 1;
-      for (int v = gt; v < nv; v += G) V::store(rows + row * ldr + (long long)v * W, V::zero());
+      zero_span<T, G>(rows + row * ldr, d, gt);
     }
   }
 }
@@ -139,8 +138,8 @@ __global__ void __launch_bounds__(PT) spread_kernel(
       }
     }
   }
-  if (nv > 128) zero_rows<T, W, PT, PT>(row_slot, N, nv, rows, ldr);
-  else zero_rows<T, W, 32, PT>(row_slot, N, nv, rows, ldr);
+  if (d * sizeof(T) > 2048) zero_rows<T, PT, PT>(row_slot, N, d, rows, ldr);
+  else zero_rows<T, 32, PT>(row_slot, N, d, rows, ldr);
 }
 
 // Spread with dot products: a group of threads owns a token.
@@ -201,7 +200,7 @@ __global__ void __launch_bounds__(threads_of(G)) spread_dots_kernel(
     }
     store_dots<G, RM>(acc, rows_s[grp], R, red, dw + t * R);
   }
-  zero_rows<T, W, G, BT>(row_slot, N, nv, rows, ldr);
+  zero_rows<T, G, BT>(row_slot, N, d, rows, ldr);
 }
 
 template <typename T, int W, int G, int RM, bool DOTS>
@@ -228,45 +227,65 @@ __global__ void __launch_bounds__(threads_of(G)) collect_kernel(
     float acc[RM];
 #pragma unroll
     for (int r = 0; r < RM; ++r) acc[r] = 0.f;
-    for (int v = gt; v < nv; v += G) {
-      float sum[W], g[W];
+    // eight row accesses in flight: RB rows of a column, C columns
+    constexpr int RB = RM < 8 ? RM : 8, C = 8 / RB;
+    for (int v0 = gt; v0 < nv; v0 += G * C) {
+      float sum[C][W];
+      typename V::Raw mine[DOTS ? C : 1];
 #pragma unroll
-      for (int j = 0; j < W; ++j) sum[j] = 0.f;
-      if (DOTS) V::unpack(V::load(other + t * ldo + (long long)v * W), g);
+      for (int c = 0; c < C; ++c) {
+        const int v = v0 + c * G;
 #pragma unroll
-      for (int r0 = 0; r0 < RM; r0 += 8) {
+        for (int j = 0; j < W; ++j) sum[c][j] = 0.f;
+        if (DOTS) mine[c] = v < nv ? V::load(other + t * ldo + (long long)v * W) : V::zero();
+      }
+#pragma unroll
+      for (int r0 = 0; r0 < RM; r0 += RB) {
         if (r0 >= R) break;
-        typename V::Raw q[8];
+        typename V::Raw q[C][RB];
 #pragma unroll
-        for (int u = 0; u < 8; ++u) {
+        for (int u = 0; u < RB; ++u) {
           const int row = r0 + u < R ? rows_s[grp][r0 + u] : -1;
-          q[u] = row >= 0 ? V::load(rows + row * ldr + (long long)v * W) : V::zero();
+#pragma unroll
+          for (int c = 0; c < C; ++c) {
+            const int v = v0 + c * G;
+            q[c][u] = row >= 0 && v < nv ? V::load(rows + row * ldr + (long long)v * W) : V::zero();
+          }
         }
 #pragma unroll
-        for (int u = 0; u < 8; ++u) {
+        for (int u = 0; u < RB; ++u) {
           const int r = r0 + u;
           if (r >= R || rows_s[grp][r] < 0) continue;
           const float wr = w_s[grp][r];
-          float o[W];
-          V::unpack(q[u], o);
 #pragma unroll
-          for (int j = 0; j < W; ++j) {
-            sum[j] = fmaf(wr, o[j], sum[j]);
-            if (DOTS) acc[r] = fmaf(g[j], o[j], acc[r]);
+          for (int c = 0; c < C; ++c) {
+            float o[W], g[W];
+            V::unpack(q[c][u], o);
+            if (DOTS) V::unpack(mine[c], g);
+#pragma unroll
+            for (int j = 0; j < W; ++j) {
+              sum[c][j] = fmaf(wr, o[j], sum[c][j]);
+              if (DOTS) acc[r] = fmaf(g[j], o[j], acc[r]);
+            }
           }
         }
       }
-      V::store(y + t * ldy + (long long)v * W, V::pack(sum));
+#pragma unroll
+      for (int c = 0; c < C; ++c)
+        if (v0 + c * G < nv) V::store(y + t * ldy + (long long)(v0 + c * G) * W, V::pack(sum[c]));
     }
     if (DOTS) store_dots<G, RM>(acc, rows_s[grp], R, red, dw + t * R);
   }
 }
 
+// Blocks that look for rows without a slot: eight an SM, or one for 32 rows.
+long long blocks_for_zeros(int N) { return std::max((N + 31LL) / 32, std::min<long long>(N, 152 * 8)); }
+
 template <typename T, int W>
 cudaError_t spread_t(const PermuteArgs& a, cudaStream_t s) {
   const int cols = std::max(1, (a.d / W + 32 * kWide - 1) / (32 * kWide));
-  const long long warps = std::max((long long)a.T * cols, (a.N + 3LL) / 4);
-  const int blocks = (int)((warps + PT / 32 - 1) / (PT / 32));
+  const long long units = ((long long)a.T * cols + PT / 32 - 1) / (PT / 32);
+  const int blocks = (int)std::max(units, blocks_for_zeros(a.N));
   spread_kernel<T, W><<<blocks, PT, 0, s>>>((const T*)a.tok.p, a.tok.ld, a.w, a.row_slot,
                                             a.slot_row, a.T, a.d, a.R, a.N, cols, (T*)a.out.p,
                                             a.out.ld);
@@ -276,9 +295,9 @@ cudaError_t spread_t(const PermuteArgs& a, cudaStream_t s) {
 
 template <typename T, int W, int G, int RM>
 cudaError_t spread_dots_t(const PermuteArgs& a, cudaStream_t s) {
-  const long long units = std::max<long long>(a.T, (a.N + 7) / 8);
   constexpr int BT = threads_of(G);
-  const int blocks = (int)((units + BT / G - 1) / (BT / G));
+  const long long units = ((long long)a.T + BT / G - 1) / (BT / G);
+  const int blocks = (int)std::max(units, blocks_for_zeros(a.N));
   spread_dots_kernel<T, W, G, RM><<<blocks, BT, 0, s>>>(
       (const T*)a.tok.p, a.tok.ld, a.w, a.row_slot, a.slot_row, a.T, a.d, a.R, a.N,
       (const T*)a.other.p, a.other.ld, (T*)a.out.p, a.out.ld, a.dw);
@@ -315,11 +334,12 @@ cudaError_t collect_t(const PermuteArgs& a, cudaStream_t s) {
 template <typename T, int W> cudaError_t by_shape(const PermuteArgs& a, bool spread, cudaStream_t s) {
   if (spread && !a.dw) return spread_t<T, W>(a, s);
   const bool wide = a.d / W > 128 || (a.d / W > 32 && a.T < 152 * 16);
-  if (a.R <= 8) {
-    if (spread) return wide ? spread_dots_t<T, W, kGroup, 8>(a, s) : spread_dots_t<T, W, 32, 8>(a, s);
-    return wide ? collect_t<T, W, kGroup, 8>(a, s) : collect_t<T, W, 32, 8>(a, s);
+  if (spread) {
+    if (a.R <= 8) return wide ? spread_dots_t<T, W, kGroup, 8>(a, s) : spread_dots_t<T, W, 32, 8>(a, s);
+    return wide ? spread_dots_t<T, W, kGroup, 32>(a, s) : spread_dots_t<T, W, 32, 32>(a, s);
   }
-  if (spread) return wide ? spread_dots_t<T, W, kGroup, 32>(a, s) : spread_dots_t<T, W, 32, 32>(a, s);
+  if (a.R <= 2) return wide ? collect_t<T, W, kGroup, 2>(a, s) : collect_t<T, W, 32, 2>(a, s);
+  if (a.R <= 8) return wide ? collect_t<T, W, kGroup, 8>(a, s) : collect_t<T, W, 32, 8>(a, s);
   return wide ? collect_t<T, W, kGroup, 32>(a, s) : collect_t<T, W, 32, 32>(a, s);
 }
 

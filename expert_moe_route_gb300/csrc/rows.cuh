@@ -77,6 +77,22 @@ template <typename T, int W> struct Vec {
   }
 };
 
+// Zeros n elements from p on, by G threads (this one is t): 16 bytes a store whatever
+// the row's alignment, its ragged ends element by element.
+template <typename T, int G>
+__device__ __forceinline__ void zero_span(T* p, int n, int t) {
+  const int head = min(n, (int)((16 - (reinterpret_cast<uintptr_t>(p) & 15)) % 16 / sizeof(T)));
+  constexpr int E = 16 / sizeof(T);
+  const int body = (n - head) / E;
+  for (int i = t; i < body; i += G)
+    reinterpret_cast<uint4*>(p + head)[i] = make_uint4(0, 0, 0, 0);
+  const int tail = head + body * E;
+  for (int i = t; i < head + n - tail; i += G) {
+    const int at = i < head ? i : tail + i - head;
+    Vec<T, 1>::store(p + at, Vec<T, 1>::zero());
+  }
+}
+
 inline int dtype_bytes(int dtype) {
   return dtype == MOE_F32 ? 4 : (dtype == MOE_BF16 || dtype == MOE_F16) ? 2 : 0;
 }
