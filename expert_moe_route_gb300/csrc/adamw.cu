@@ -20,7 +20,7 @@
 // before they are rounded.
 //
 // Bound by HBM: 24 B an element with 32-bit states (bf16 p, fp32 g), 12 B with
-// 8-bit ones.
+// 8-bit ones, where some 50 instructions an element come close to it.
 #include <math.h>
 
 #include <algorithm>
@@ -60,6 +60,7 @@ struct AdamTable {
   AdamEntry e[kPerLaunch];
   int count, chunks, run;       // a chunk: run blocks a warp
   float b1, b2, c1, c2;         // beta1, beta2, 1 - beta1, 1 - beta2
+  float one;                    // 1
   float step_size, root, eps;   // lr / (1 - beta1^t), 1 / sqrt(1 - beta2^t)
   const float* norm;            // {norm, coef, finite, -} or null
 };
@@ -256,31 +257,38 @@ __device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
 // with 8-bit states the instructions, not the bytes, are what a plain form runs
 // out of.
 struct Factors {
-  float2 b1, b2, c1, c2, root, eps, step, decay;   // c1, c2 with the gradients' factor
+  float2 b1, b2, c1, c2, k, one, root, eps, step, decay;   // k: the gradients' factor
   __device__ __forceinline__ Factors(const AdamTable& t, const AdamEntry& e, float coef)
-      : b1(both(t.b1)), b2(both(t.b2)), c1(both(coef * t.c1)), c2(both(coef * coef * t.c2)),
-        root(both(t.root)), eps(both(t.eps)), step(both(-t.step_size)), decay(both(e.decay)) {}
+      : b1(both(t.b1)), b2(both(t.b2)), c1(both(t.c1)), c2(both(t.c2)), k(both(coef)),
+        one(both(t.one)), root(both(t.root)), eps(both(t.eps)), step(both(-t.step_size)), decay(both(e.decay)) {}
 };
 
 // Eight elements' step.  S8: m and v come as code values and are scaled by ms
-// and vs (v the root's), and u gets sqrt(v).
+// and vs (v the root's), and u gets sqrt(v).  There every operation that reaches
+// the codes rounds by itself, in the order of the formulas: one bit more or less
+// under the dither can turn a code, so results that are to be met bit for bit
+// elsewhere cannot have their factors gathered or their sums fused.  (A sum of two
+// paired products is compiled to a fused one, whatever rounding it names; times
+// `one`, a 1 the compiler does not know, it is fused with that.)
 template <bool S8>
 __device__ __forceinline__ void step8(const Factors& f, const float* g, float* p, float* m,
                                       float* v, float* u, float ms, float vs) {
-  const float2 mb = S8 ? both(ms * f.b1.x) : f.b1, qs = both(vs);
 #pragma unroll
   for (int j = 0; j < 8; j += 2) {
     const float2 gj = make_float2(g[j], g[j + 1]);
-    const float2 mj = __ffma2_rn(gj, f.c1, __fmul2_rn(make_float2(m[j], m[j + 1]), mb));
-    const float2 sq = __fmul2_rn(gj, __fmul2_rn(gj, f.c2));
-    float2 vj = make_float2(v[j], v[j + 1]);
+    float2 mj = make_float2(m[j], m[j + 1]), vj = make_float2(v[j], v[j + 1]), uj;
     if (S8) {
-      const float2 q = __fmul2_rn(vj, qs);
-      vj = __ffma2_rn(q, __fmul2_rn(q, f.b2), sq);
+      const float2 gc = __fmul2_rn(gj, f.k), q = __fmul2_rn(vj, both(vs));
+      mj = __ffma2_rn(__fmul2_rn(__fmul2_rn(mj, both(ms)), f.b1), f.one, __fmul2_rn(gc, f.c1));
+      vj = __ffma2_rn(__fmul2_rn(__fmul2_rn(q, q), f.b2), f.one,
+                      __fmul2_rn(__fmul2_rn(gc, gc), f.c2));
+      uj = make_float2(__fsqrt_rn(vj.x), __fsqrt_rn(vj.y));
     } else {
-      vj = __ffma2_rn(vj, f.b2, sq);
+      const float2 gc = __fmul2_rn(gj, f.k);
+      mj = __ffma2_rn(gc, f.c1, __fmul2_rn(mj, f.b1));
+      vj = __ffma2_rn(gc, __fmul2_rn(gc, f.c2), __fmul2_rn(vj, f.b2));
+      uj = make_float2(root_of(vj.x), root_of(vj.y));
     }
-    const float2 uj = make_float2(root_of(vj.x), root_of(vj.y));
     const float2 den = __ffma2_rn(uj, f.root, f.eps);
     const float2 ratio = __fmul2_rn(mj, make_float2(reciprocal(den.x), reciprocal(den.y)));
     const float2 pj = __ffma2_rn(ratio, f.step, __fmul2_rn(make_float2(p[j], p[j + 1]), f.decay));
@@ -320,10 +328,10 @@ struct Scales {
       am = fmaxf(fmaxf(am, fabsf(mj[j])), fabsf(mj[j + 1]));
       au = fmaxf(fmaxf(au, uj[j]), uj[j + 1]);
     }
-    m = warp_max(am) / 448.f;
-    v = warp_max(au) / 448.f;
-    im = m >= 0x1p-126f ? 1.f / m : 0.f;
-    iu = v >= 0x1p-126f ? 1.f / v : 0.f;
+    m = __fmul_rn(warp_max(am), 1.f / 448.f);
+    v = __fmul_rn(warp_max(au), 1.f / 448.f);
+    im = m >= 0x1p-126f ? __fdiv_rn(1.f, m) : 0.f;
+    iu = v >= 0x1p-126f ? __fdiv_rn(1.f, v) : 0.f;
     if (im == 0.f) m = 0.f;
     if (iu == 0.f) v = 0.f;
   }
@@ -449,13 +457,13 @@ __global__ void __launch_bounds__(AT) adamw32_kernel(const __grid_constant__ Ada
   if (w.left > 0) step_ragged<false>(e, t, coef, w.base, w.left);
 }
 
-// 8-bit states.  553M elements (bf16 p, fp32 g, 6.7 GB): 0.98 ms, 6.8 TB/s.  The
+// 8-bit states.  553M elements (bf16 p, fp32 g, 6.7 GB): 0.985 ms, 6.8 TB/s.  The
 // new scales of a whole chunk go out as lines from shared memory: written block
 // by block, 4 bytes at a time into lines that other CTAs read and write at the
 // same moment, the kernel took 2.3 ms.  Eight blocks a warp, loads not issued
-// ahead: the other warps of four CTAs cover them (one block ahead in registers,
-// three CTAs: 1.02 ms).
-__global__ void __launch_bounds__(AT, 4) adamw8_kernel(const __grid_constant__ AdamTable t) {
+// ahead: the other warps cover them.  Five CTAs an SM although 48 registers spill
+// a little (four with 64: 1.04 ms, three: 1.15, six: 1.09).
+__global__ void __launch_bounds__(AT, 5) adamw8_kernel(const __grid_constant__ AdamTable t) {
   __shared__ float scales[2][kMostRun * (AT / 32)];
   float coef;
   Walk w;
@@ -495,7 +503,7 @@ __global__ void __launch_bounds__(AT, 4) adamw8_kernel(const __grid_constant__ A
 }
 
 // ---------------------------------------------------------------- norm
-// 553M fp32 gradients (2.2 GB) in 0.326 ms, 6.8 TB/s.
+// 553M fp32 gradients (2.2 GB) in 0.314 ms, 7.05 TB/s.
 __device__ __forceinline__ float square_add(float s, float g) { return fmaf(g, g, s); }
 
 // A sum as two fp32 numbers, hi + lo: an addition's rounding error is itself an
@@ -716,6 +724,7 @@ cudaError_t launch_adamw(const moe_adamw_tensor_t* x, int n, const moe_adamw_t& 
                          const float* norm, cudaStream_t s) {
   return in_runs(x, n, [&](int i, int j) {
     AdamTable t;
+    t.one = 1.f;
     t.b1 = (float)h.beta1;
     t.b2 = (float)h.beta2;
     t.c1 = (float)(1.0 - h.beta1);

@@ -632,9 +632,10 @@ moe_status_t moe_grad_norm(const moe_adamw_tensor_t* tensors, int n_tensors, dou
  *       (sqrt(v) / sqrt(1 - beta2^step) + eps)
  * in fp32, p rounded once to its type.  With norm and norm[2] == 0 nothing is
  * changed.  8-bit states are rounded after the update has used them: per block,
- * scale = max / 448 and code = |value| / scale rounded to one of its two E4M3
- * neighbours by adding 20 dither bits below the kept mantissa bits; sqrt(v) > 0
- * never rounds to 0.  Element i of the k-th tensor takes the dither
+ * scale = max * (1/448) and code = |value| * (1/scale) rounded to one of its two
+ * E4M3 neighbours by adding 20 dither bits below the kept mantissa bits; sqrt(v) > 0
+ * never rounds to 0.  m, v, sqrt(v), scales and codes are computed operation by
+ * operation, each rounded to nearest, so they can be reproduced bit for bit.  Element i of the k-th tensor takes the dither
  *   h = mix(floor(i/2) * 0x9E3779B1 + mix(seed + k * 0x9E3779B1))   (mod 2^32)
  *   mix(x): x = (x ^ x>>16) * 0x6A09E667; x = (x ^ x>>15) * 0xBB67AE85; x ^ x>>16
  *   dither = 16 * (i even ? h mod 2^16 : h >> 16) + 8

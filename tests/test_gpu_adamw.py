@@ -268,3 +268,56 @@ def test_same_bits_every_time_and_in_a_graph(lib, bits):
     for other in outs[1:]:
         for a, b in zip(outs[0], other):
             assert torch.equal(a, b)
+
+
+def mix(x):
+    x = (x ^ (x >> np.uint64(16))) * np.uint64(0x6A09E667) & np.uint64(0xFFFFFFFF)
+    x = (x ^ (x >> np.uint64(15))) * np.uint64(0xBB67AE85) & np.uint64(0xFFFFFFFF)
+    return x ^ (x >> np.uint64(16))
+
+
+def stored_on_the_host(x, scale, dither, least):
+    """Codes of x (fp32) by the definition: scale, quotient and rounding operation by operation."""
+    f = np.float32
+    inv = np.where(scale >= f(2.0 ** -126), f(1) / np.maximum(scale, f(2.0 ** -126)), f(0))
+    r = np.minimum(np.abs(x) * np.repeat(inv, 256)[:x.size], f(448))
+    shift = np.where(r < f(2.0 ** -6), f(2.0 ** -6), f(0))
+    kept = ((r + shift).view(np.uint32) + dither) & np.uint32(0xFFF00000)
+    q = np.where(r > 0, np.clip(kept.view(np.float32) - shift, f(least), f(448)), f(0))
+    return np.copysign(q, x)
+
+
+@pytest.mark.parametrize("n,shift", [(1000, 0), (4096, 0), (40000, 0), (40000, 3)])
+def test_eight_bit_states_bit_for_bit(lib, n, shift):
+    """Codes and scales after three steps equal those of the formulas, computed on the host one
+    fp32 operation at a time, bit for bit."""
+    f = np.float32
+    t = tensor(n, True, False, 8, False, shift, seed=n)
+    h = dict(HYPER)
+    f32 = lambda a: a.float().cpu().numpy()  # noqa: E731
+    m8, v8, ms, vs = f32(t["m"]), f32(t["v"]), f32(t["m_scale"]), f32(t["v_scale"])
+    g = f32(t["g"])
+    other = tensor(700, True, False, 8, False, 0, seed=1)        # its place in the list is 0
+    items = lib.AdamWList([make(lib, other, 0.0), make(lib, t, 0.1)])
+    b1, b2 = f(h["beta1"]), f(h["beta2"])
+    c1, c2 = f(1 - h["beta1"]), f(1 - h["beta2"])
+    for step in range(1, 4):
+        h.update(step=step, seed=70 + step)
+        lib.moe_adamw_step(items, **h)
+        place = mix(np.uint64((h["seed"] + 0x9E3779B1) & 0xFFFFFFFF))
+        pair = np.arange((n + 1) // 2, dtype=np.uint64)
+        bits = mix((pair * np.uint64(0x9E3779B1) + place) & np.uint64(0xFFFFFFFF))
+        half = np.stack([bits & np.uint64(0xFFFF), bits >> np.uint64(16)], 1).reshape(-1)[:n]
+        dither = (half * np.uint64(16) + np.uint64(8)).astype(np.uint32)
+        m = m8 * np.repeat(ms, 256)[:n] * b1 + g * c1
+        q = v8 * np.repeat(vs, 256)[:n]
+        u = np.sqrt(q * q * b2 + g * g * c2)
+        full = np.zeros((ms.size * 256, 2), f)
+        full[:n, 0], full[:n, 1] = np.abs(m), u
+        top = full.reshape(-1, 256, 2).max(1) * (f(1) / f(448))
+        ms, vs = (np.where(top[:, k] >= f(2.0 ** -126), top[:, k], f(0)) for k in (0, 1))
+        m8 = stored_on_the_host(m, ms, dither, 0.0)
+        v8 = stored_on_the_host(u, vs, dither, 2.0 ** -9)
+        for name, want in (("m", m8), ("v", v8), ("m_scale", ms), ("v_scale", vs)):
+            got = f32(t[name])
+            assert np.array_equal(got, want), f"step {step} {name}: {(got != want).sum()} differ"
