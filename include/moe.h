@@ -639,6 +639,8 @@ moe_status_t moe_grad_norm(const moe_adamw_tensor_t* tensors, int n_tensors, dou
  *   h = mix(floor(i/2) * 0x9E3779B1 + mix(seed + k * 0x9E3779B1))   (mod 2^32)
  *   mix(x): x = (x ^ x>>16) * 0x6A09E667; x = (x ^ x>>15) * 0xBB67AE85; x ^ x>>16
  *   dither = 16 * (i even ? h mod 2^16 : h >> 16) + 8
+ * Without norm the gradients have to be finite: one that is not makes its
+ * parameter NaN and leaves the states of its block without meaning.
  * No workspace; the list travels in the launch.  Tensors must not overlap.
  * step >= 1, 0 <= beta < 1, eps at least the smallest normal fp32 number.
  */

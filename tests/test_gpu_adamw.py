@@ -321,3 +321,26 @@ def test_eight_bit_states_bit_for_bit(lib, n, shift):
         for name, want in (("m", m8), ("v", v8), ("m_scale", ms), ("v_scale", vs)):
             got = f32(t[name])
             assert np.array_equal(got, want), f"step {step} {name}: {(got != want).sum()} differ"
+
+
+def test_tensor_past_32_bit_offsets(lib):
+    """More than 2^31 elements: the step and the norm reach the end."""
+    n = 2 ** 31 + 1024
+    dev = dict(device="cuda")
+    t = {"p": torch.zeros(n, dtype=torch.bfloat16, **dev), "g": torch.zeros(n, dtype=torch.bfloat16, **dev),
+         "m": torch.zeros(n, dtype=torch.float8_e4m3fn, **dev), "v": torch.zeros(n, dtype=torch.float8_e4m3fn, **dev),
+         "m_scale": torch.zeros(n // 256, **dev), "v_scale": torch.zeros(n // 256, **dev)}
+    t["p"][-512:] = torch.randn(512, **dev).bfloat16()
+    t["g"][-512:] = torch.randn(512, **dev).bfloat16()
+    last = {k: (x[-512:] if x.numel() == n else x[-2:]) for k, x in t.items()}
+    items = lib.AdamWList([make(lib, t, 0.1)])
+    norm = torch.empty(4, **dev)
+    lib.moe_grad_norm(items, 0.0, norm, lib.workspace(lib.grad_norm_ws_bytes(items)))
+    total = float(last["g"].double().square().sum().sqrt())
+    assert abs(float(norm[0]) - total) <= 8 * EPS * total
+    want = expected(last, 0.1)
+    lib.moe_adamw_step(items, **HYPER)
+    check(last, want, "the end")
+    for name in ("p", "m", "v"):
+        for part in t[name].view(torch.int16 if name == "p" else torch.uint8)[:-512].split(2 ** 29):
+            assert not part.any(), name

@@ -149,3 +149,52 @@ def test_same_bits_every_time(lib):
         lib.moe_embed_bwd(dout, ids, grad, ws)
         first = grad if first is None else first
         assert torch.equal(first, grad)
+
+
+@pytest.mark.parametrize("accumulate", [False, True])
+def test_capture(lib, accumulate):
+    """Lookup and gradient replay from a graph on new ids."""
+    n, V, d = 3000, 700, 320
+    ids = ids_of(n, V, "power", 1, torch.int64)
+    table = torch.randn(V, d, device="cuda").bfloat16()
+    dout = torch.randn(n, d, device="cuda").bfloat16()
+    out, grad = torch.empty(n, d, dtype=BF, device="cuda"), torch.zeros(V, d, device="cuda")
+    ws = lib.workspace(lib.embed_bwd_ws_bytes(n, V, d))
+
+    def step():
+        lib.moe_embed(ids, table, out, scale=2.0)
+        lib.moe_embed_bwd(dout, ids, grad, ws, accumulate=accumulate)
+
+    step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    ids.copy_(ids_of(n, V, "masked", 2, torch.int64))
+    grad.zero_()
+    graph.replay()
+    graph.replay()
+    torch.cuda.synchronize()
+    got = [out.clone(), grad.clone()]
+    grad.zero_()
+    step(), step()
+    torch.cuda.synchronize()
+    assert torch.equal(got[0], out) and torch.equal(got[1], grad)
+
+
+def test_table_past_32_bit_offsets(lib):
+    """More than 2^31 elements in the table: lookup and gradient at its end."""
+    V, d = 600_001, 4096
+    table = torch.empty(V, d, dtype=BF, device="cuda")
+    table[-3:] = torch.randn(3, d, device="cuda").bfloat16()
+    ids = torch.tensor([V - 1, V - 3, V - 1, V - 2], device="cuda")
+    out = torch.empty(4, d, dtype=BF, device="cuda")
+    lib.moe_embed(ids, table, out)
+    assert torch.equal(out, table[ids])
+    grad = torch.full((V, d), float("nan"), dtype=BF, device="cuda")
+    lib.moe_embed_bwd(out, ids, grad, lib.workspace(lib.embed_bwd_ws_bytes(4, V, d)),
+                      flags=lib.MOE_CHECK)
+    assert torch.equal(grad[-2:], torch.stack([out[3], (out[0].float() * 2).bfloat16()]))
+    assert torch.equal(grad[-3], out[1])
+    for rows in grad[:-3].split(100_000):
+        assert not rows.any()

@@ -349,3 +349,21 @@ def test_capture(lib):
     torch.cuda.synchronize()
     for a, b in zip(got, (*plan, rows, dx, dw)):
         assert torch.equal(a, b)
+
+
+def test_rows_past_32_bit_offsets(lib):
+    """More than 2^31 elements in the rows: the last tokens' copies, sums and gradients."""
+    T, d, R = 40_000, 8192, 8
+    idx = torch.arange(R, dtype=torch.int32, device="cuda").repeat(T, 1)
+    _, _, row_slot, slot_row = sort(lib, idx, R)
+    assert torch.equal(slot_row[-1], torch.arange(1, R + 1, device="cuda").int() * T - 1)
+    x = torch.randn(T, d, device="cuda").bfloat16()
+    rows = torch.empty(T * R, d, dtype=torch.bfloat16, device="cuda")
+    lib.moe_permute(x, None, row_slot, slot_row, rows)
+    for r in range(R):
+        assert torch.equal(rows[r * T:(r + 1) * T], x)
+    y, dw = torch.empty_like(x), torch.empty(T, R, device="cuda")
+    lib.moe_permute_bwd(rows, slot_row, None, x, y, dw)
+    assert torch.equal(y, (x.float() * R).bfloat16())           # sums of eight equal bf16 are exact
+    exact = x[-100:].double().square().sum(1, keepdim=True)
+    within(dw[-100:], exact.expand(-1, R), (d + 1) * EPS * exact, "dw")
