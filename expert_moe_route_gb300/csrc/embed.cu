@@ -184,10 +184,10 @@ __global__ void __launch_bounds__(RT) rows_kernel(
     for (int u = 0; u < kGroup; ++u) {
       const int i = i0 + u;
       if (i >= count) break;
-      float f[W];
-      if (here) Vec<T, W>::unpack(slot[i % kFlight][lane], f);
+      float f[W];        // lanes past the row's end sum what is there and store nothing
+      Vec<T, W>::unpack(slot[i % kFlight][lane], f);
 #pragma unroll
-      for (int j = 0; j < W; ++j) acc[j] += here ? f[j] : 0.f;
+      for (int j = 0; j < W; ++j) acc[j] += f[j];
       const bool ended = ends >> i & 1;
       if (!ended && i != count - 1) continue;
       const int id = __shfl_sync(kFull, kv.x, i);
