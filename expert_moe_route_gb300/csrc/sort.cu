@@ -87,12 +87,12 @@ struct Table {
 __device__ __forceinline__ int2 cluster_totals(const Table& t, int bins, uint32_t rank,
                                                uint32_t nr) {
   const int b = threadIdx.x * 2;
+  int2 run = make_int2(0, 0);
   __syncthreads();
   if (b < bins) {
     int2 c[SW];
 #pragma unroll
     for (int w = 0; w < SW; ++w) c[w] = *reinterpret_cast<const int2*>(t.wcnt + w * bins + b);
-    int2 run = make_int2(0, 0);
 #pragma unroll
     for (int w = 0; w < SW; ++w) {
       *reinterpret_cast<int2*>(t.wcnt + w * bins + b) = run;
@@ -100,6 +100,10 @@ __device__ __forceinline__ int2 cluster_totals(const Table& t, int bins, uint32_
       run.y += c[w].y;
     }
     *reinterpret_cast<int2*>(t.mine + b) = run;
+  }
+  if (nr == 1) {
+    if (b < bins) *reinterpret_cast<int2*>(t.below + b) = make_int2(0, 0);
+    return run;
   }
   cluster_arrive();
   cluster_wait();
@@ -197,7 +201,7 @@ __global__ void __launch_bounds__(ST) sort_slots_kernel(
     for (uint32_t r = 0; r < nr; ++r) any |= ld_cluster(&bad_s, r);
     *err = any ? kErrBadRouting : 0;
   }
-  cluster_arrive();
+  if (nr > 1) cluster_arrive();
   const int b = tid * 2;
   int2 kept, padded;
   kept.x = capacity > 0 ? min(total.x, capacity) : total.x;
@@ -244,7 +248,7 @@ __global__ void __launch_bounds__(ST) sort_slots_kernel(
       if (row >= 0) row_slot[row] = (int)i;
     }
   }
-  cluster_wait();   // no CTA leaves while another still reads its totals
+  if (nr > 1) cluster_wait();   // no CTA leaves while another still reads its totals
 }
 
 // ---------------------------------------------------------------- id sort
@@ -342,8 +346,12 @@ __global__ void __launch_bounds__(ST) sort_ids_kernel(
       }
     }
     count = live;
-    cluster_arrive();   // the totals are read, this pass's pairs written
-    cluster_wait();
+    if (nr > 1) {
+      cluster_arrive();   // the totals are read, this pass's pairs written
+      cluster_wait();
+    } else {
+      __syncthreads();
+    }
   }
 }
 
