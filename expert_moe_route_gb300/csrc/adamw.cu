@@ -121,6 +121,7 @@ constexpr uint32_t kGolden = 0x9E3779B1u;   // 2^32 / golden ratio
 // moves the code to the top byte and drops the sign; `dither` comes times 16.
 // r <= 448 (1 + 3 * 2^-24) cannot carry past 448: the dither's last bits are 1000.
 constexpr float kToCode = 0x1p-120f;
+constexpr float kLeast = 0x1p-129f;         // of code 1
 __device__ __forceinline__ uint32_t code_top(float scaled, uint32_t dither) {
   return __float_as_uint(scaled) * 16u + dither;
 }
@@ -307,11 +308,13 @@ __device__ __forceinline__ void encode8(const float* m, const float* u, float im
 #pragma unroll
   for (int j = 0; j < 8; j += 2) {
     const float2 rm = __fmul2_rn(__fmul2_rn(make_float2(m[j], m[j + 1]), both(im)), to);
-    const float2 ru = __fmul2_rn(__fmul2_rn(make_float2(u[j], u[j + 1]), both(iu)), to);
+    const float2 qu = __fmul2_rn(make_float2(u[j], u[j + 1]), both(iu)), ru = __fmul2_rn(qu, to);
     wm[j] = code_top(rm.x, d[j]) | (__float_as_uint(rm.x) & 0x80000000u);
     wm[j + 1] = code_top(rm.y, d[j + 1]) | (__float_as_uint(rm.y) & 0x80000000u);
-    wu[j] = max(code_top(ru.x, d[j]), ru.x > 0.f ? 1u << 24 : 0u);
-    wu[j + 1] = max(code_top(ru.y, d[j + 1]), ru.y > 0.f ? 1u << 24 : 0u);
+    // a root above zero is at least 2^-9, of its scale: decided before the factor, below
+    // 2^-30 of the scale ru is zero (max of the codes instead spilled twice as much)
+    wu[j] = code_top(fmaxf(ru.x, qu.x > 0.f ? kLeast : 0.f), d[j]);
+    wu[j + 1] = code_top(fmaxf(ru.y, qu.y > 0.f ? kLeast : 0.f), d[j + 1]);
   }
   *mc = make_uint2(top_bytes(wm), top_bytes(wm + 4));
   *vc = make_uint2(top_bytes(wu), top_bytes(wu + 4));

@@ -1,0 +1,48 @@
+"""GPU: the optimiser step and the norm at the ends of their ranges.  Helpers and bounds are those
+of test_gpu_adamw."""
+import numpy as np
+import pytest
+import torch
+
+from tests.test_gpu_adamw import HYPER, make, mix, stored_on_the_host, tensor
+
+pytestmark = pytest.mark.gpu
+
+
+def dithers(n, place, seed):
+    """The dither of n elements of the place-th tensor, by its definition."""
+    golden, low = np.uint64(0x9E3779B1), np.uint64(0xFFFFFFFF)
+    start = mix(np.uint64((seed + place * 0x9E3779B1) & 0xFFFFFFFF))
+    bits = mix((np.arange((n + 1) // 2, dtype=np.uint64) * golden + start) & low)
+    half = np.stack([bits & np.uint64(0xFFFF), bits >> np.uint64(16)], 1).reshape(-1)[:n]
+    return (half * np.uint64(16) + np.uint64(8)).astype(np.uint32)
+
+
+# whole chunks; a chunk that ends early, its whole blocks and its last one; unaligned
+@pytest.mark.parametrize("n,shift", [(4096, 0), (2048 + 700, 0), (4096, 3)])
+def test_small_roots_beside_large_ones(lib, n, shift):
+    """sqrt(v) > 0 gets a code above 0 however small it is beside its block's largest: gradients of
+    1 and of 1e-13 .. 1e-6 from zero states, codes and scales bit for bit."""
+    f = np.float32
+    t = tensor(n, False, False, 8, False, shift, seed=n, zeros=True)
+    gen = torch.Generator(device="cuda").manual_seed(7)
+    small = torch.rand(n, generator=gen, device="cuda") < 0.7
+    power = torch.rand(n, generator=gen, device="cuda") * 7 - 13
+    sign = torch.where(torch.rand(n, generator=gen, device="cuda") < 0.5, -1.0, 1.0)
+    t["g"].copy_(torch.where(small, 10.0 ** power, 1.0) * sign)
+    t["g"][5::97] = 0
+    h = dict(HYPER, step=1)
+    lib.moe_adamw_step(lib.AdamWList([make(lib, t, 0.0)]), **h)
+    f32 = lambda a: a.float().cpu().numpy()  # noqa: E731
+    g = f32(t["g"])
+    m, u = g * f(1 - h["beta1"]), np.sqrt(g * g * f(1 - h["beta2"]))
+    blocks = -(-n // 256)
+    for name, x, least in (("m", m, 0.0), ("v", u, 2.0 ** -9)):
+        full = np.zeros(blocks * 256, f)
+        full[:n] = np.abs(x)
+        scale = full.reshape(-1, 256).max(1) * (f(1) / f(448))
+        want = stored_on_the_host(x, scale, dithers(n, 0, h["seed"]), least)
+        got = f32(t[name])
+        assert np.array_equal(f32(t[name + "_scale"]), scale), name
+        assert np.array_equal(got, want), f"{name}: {(got != want).sum()} differ"
+    assert ((f32(t["v"]) > 0) == (g != 0)).all()
