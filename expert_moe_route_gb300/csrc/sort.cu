@@ -157,8 +157,8 @@ __global__ void __launch_bounds__(ST) sort_slots_kernel(
   const uint32_t rank = cluster_rank(), nr = cluster_size();
   const int bins = (E + 1) & ~1, bits = 32 - __clz(E - 1);
   Table t{sm, sm + SW * bins, sm + SW * bins + bins};
-  int* last_s = sm + SW * bins + 2 * bins;   // [bins] past the last row of the bin
-  int* off_s = last_s + bins;                // [bins] the bin's first row, then this CTA's
+  int* room_s = sm + SW * bins + 2 * bins;   // [bins] rows left for this CTA's part of the bin (<= 0: none)
+  int* off_s = room_s + bins;                // [bins] first row of this CTA's part of the bin
   const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
   if (tid == 0) bad_s = 0;
   for (int i = tid; i < SW * bins / 2; i += ST) reinterpret_cast<int2*>(t.wcnt)[i] = make_int2(0, 0);
@@ -212,8 +212,11 @@ __global__ void __launch_bounds__(ST) sort_slots_kernel(
   const int off = block_scan(padded.x + padded.y, warp_sums, &end);
   if (b < bins) {
     const int2 before = *reinterpret_cast<const int2*>(t.below + b);
-    *reinterpret_cast<int2*>(last_s + b) = make_int2(off + kept.x, off + padded.x + kept.y);
-    *reinterpret_cast<int2*>(off_s + b) = make_int2(off + before.x, off + padded.x + before.y);
+    // ranks go up to 2^31 also where a limit keeps the rows few: a slot's rank is
+    // compared with the room before the bin's first row is added to it
+    *reinterpret_cast<int2*>(room_s + b) = make_int2(kept.x - before.x, kept.y - before.y);
+    *reinterpret_cast<int2*>(off_s + b) =
+        make_int2(off + min(before.x, kept.x), off + padded.x + min(before.y, kept.y));
     if (rank == 0) {
       counts[b] = kept.x;
       offsets[b] = off;
@@ -240,10 +243,7 @@ __global__ void __launch_bounds__(ST) sort_slots_kernel(
       if ((unsigned)e[j] >= (unsigned)E) e[j] = -1;
       const int pos = warp_rank(e[j], my, bits);
       int row = -1;
-      if (e[j] >= 0) {
-        row = off_s[e[j]] + pos;
-        if (row >= last_s[e[j]]) row = -1;
-      }
+      if (e[j] >= 0 && pos < room_s[e[j]]) row = off_s[e[j]] + pos;
       if (i < w1) slot_row[i] = row;
       if (row >= 0) row_slot[row] = (int)i;
     }
