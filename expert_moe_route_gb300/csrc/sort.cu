@@ -206,8 +206,9 @@ __global__ void __launch_bounds__(ST) sort_slots_kernel(
   int2 kept, padded;
   kept.x = capacity > 0 ? min(total.x, capacity) : total.x;
   kept.y = capacity > 0 ? min(total.y, capacity) : total.y;
-  padded.x = (kept.x + align - 1) / align * align;
-  padded.y = (kept.y + align - 1) / align * align;
+  // kept + align may reach 2^31, what is left of it after rounding does not
+  padded.x = (int)(((unsigned)kept.x + align - 1) / align * align);
+  padded.y = (int)(((unsigned)kept.y + align - 1) / align * align);
   int end;
   const int off = block_scan(padded.x + padded.y, warp_sums, &end);
   if (b < bins) {

@@ -32,3 +32,16 @@ def test_limit_under_an_expert_that_takes_nearly_all(lib):
         assert (part == -1).all()
     rows = row_slot.view(E, align)
     assert torch.equal(rows[:, 0], torch.arange(E, device="cuda").int()) and (rows[:, 1:] == -1).all()
+
+
+def test_one_expert_whose_rows_end_near_2_to_the_31(lib):
+    """2^31 - 2 slots in tiles of three rows: the end of the plan is 2^31 - 2 as well."""
+    T, R, align = 2 ** 30 - 1, 2, 3
+    idx = torch.zeros((T, R), dtype=torch.int32, device="cuda")
+    counts, offsets, row_slot, slot_row = plan_of(lib, idx, 1, align, 0)
+    n = T * R
+    assert counts.tolist() == [n] and offsets.tolist() == [0, n]
+    for of in (row_slot, slot_row.view(-1)):
+        for at in range(0, n, 2 ** 28):
+            part = of[at:at + 2 ** 28]
+            assert torch.equal(part, torch.arange(at, at + part.numel(), device="cuda").int())
