@@ -626,7 +626,7 @@ __global__ void __launch_bounds__(AT) square_sums_kernel(const __grid_constant__
   }
 }
 
-__global__ void __launch_bounds__(kNormThreads) norm_kernel(const float2* sums, int n,
+__global__ void __launch_bounds__(kNormThreads) norm_kernel(const float2* sums, int n, bool clip,
                                                             float max_norm, float* norm) {
   __shared__ Sum red[kNormThreads / 32];
   const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
@@ -647,7 +647,7 @@ __global__ void __launch_bounds__(kNormThreads) norm_kernel(const float2* sums, 
   if (lane == 0) {
     const float v = (float)sqrt((double)sum.hi + (double)sum.lo);
     norm[0] = v;
-    norm[1] = max_norm > 0.f ? fminf(max_norm / (v + 1e-6f), 1.f) : 1.f;
+    norm[1] = clip ? fminf(max_norm / (v + 1e-6f), 1.f) : 1.f;
     norm[2] = isfinite(v) ? 1.f : 0.f;
     norm[3] = 0.f;
   }
@@ -698,7 +698,7 @@ size_t grad_norm_ws_bytes(const moe_adamw_tensor_t* x, int n) {
   return align_up(sizeof(float2) * kNormBlocks * (size_t)(runs > 0 ? runs : 1), 256);
 }
 
-cudaError_t launch_grad_norm(const moe_adamw_tensor_t* x, int n, float max_norm, float* norm,
+cudaError_t launch_grad_norm(const moe_adamw_tensor_t* x, int n, double max_norm, float* norm,
                              void* ws, cudaStream_t s) {
   float2* sums = static_cast<float2*>(ws);
   int used = 0;
@@ -720,7 +720,9 @@ cudaError_t launch_grad_norm(const moe_adamw_tensor_t* x, int n, float max_norm,
   });
   if (e != cudaSuccess) return e;
   count_launches(1);
-  return launch_after(norm_kernel, 1, kNormThreads, s, sums, used, max_norm, norm);
+  // a limit above zero may be zero in fp32: then the factor is, too
+  return launch_after(norm_kernel, 1, kNormThreads, s, sums, used, max_norm > 0, (float)max_norm,
+                      norm);
 }
 
 cudaError_t launch_adamw(const moe_adamw_tensor_t* x, int n, const moe_adamw_t& h,

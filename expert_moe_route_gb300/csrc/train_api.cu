@@ -254,8 +254,8 @@ moe_status_t moe_grad_norm(const moe_adamw_tensor_t* tensors, int n_tensors, dou
   if (*ws_bytes < need || !aligned(ws, 256)) return MOE_ERR_WORKSPACE;
   if (!norm) return MOE_ERR_INVALID_ARG;
   if (!aligned(norm, 16)) return MOE_ERR_UNSUPPORTED;
-  return finish(launch_grad_norm(tensors, n_tensors, (float)max_norm, norm, ws, S(stream)),
-                nullptr, 0, S(stream));
+  return finish(launch_grad_norm(tensors, n_tensors, max_norm, norm, ws, S(stream)), nullptr, 0,
+                S(stream));
 }
 
 moe_status_t moe_adamw_step(const moe_adamw_tensor_t* tensors, int n_tensors,

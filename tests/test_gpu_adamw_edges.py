@@ -46,3 +46,19 @@ def test_small_roots_beside_large_ones(lib, n, shift):
         assert np.array_equal(f32(t[name + "_scale"]), scale), name
         assert np.array_equal(got, want), f"{name}: {(got != want).sum()} differ"
     assert ((f32(t["v"]) > 0) == (g != 0)).all()
+
+
+def norm_of(lib, grads, max_norm):
+    """The record of moe_grad_norm over fp32 gradients."""
+    items = lib.AdamWList([lib.AdamWTensor(g, g, g, g) for g in grads])
+    norm = torch.full((4,), 9.0, device="cuda")
+    lib.moe_grad_norm(items, max_norm, norm, lib.workspace(lib.grad_norm_ws_bytes(items)))
+    return norm.tolist()
+
+
+@pytest.mark.parametrize("max_norm", [1e-46, 1e-60, 5e-324])
+def test_limit_below_the_smallest_fp32_number(lib, max_norm):
+    """A limit above zero clips, however small: the factor rounds to 0, it is not 1."""
+    g = torch.full((1000,), 0.5, device="cuda")
+    norm = norm_of(lib, [g], max_norm)
+    assert norm[1:] == [0.0, 1.0, 0.0]
