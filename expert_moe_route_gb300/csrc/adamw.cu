@@ -21,6 +21,7 @@
 //
 // Bound by HBM: 24 B an element with 32-bit states (bf16 p, fp32 g), 12 B with
 // 8-bit ones, where some 50 instructions an element come close to it.
+#include <float.h>
 #include <math.h>
 
 #include <algorithm>
@@ -645,9 +646,11 @@ __global__ void __launch_bounds__(kNormThreads) norm_kernel(const float2* sums, 
   sum = red[lane];
   sum.add_over_warp();
   if (lane == 0) {
-    const float v = (float)sqrt((double)sum.hi + (double)sum.lo);
+    // past the fp32 range hi is inf, of a NaN it is NaN, and lo has no meaning
+    const float v = isfinite(sum.hi) ? (float)sqrt((double)sum.hi + (double)sum.lo) : sum.hi;
+    const float coef = max_norm / (v + 1e-6f);
     norm[0] = v;
-    norm[1] = clip ? fminf(max_norm / (v + 1e-6f), 1.f) : 1.f;
+    norm[1] = !clip || coef > 1.f ? 1.f : coef;   // a NaN stays
     norm[2] = isfinite(v) ? 1.f : 0.f;
     norm[3] = 0.f;
   }
@@ -720,9 +723,10 @@ cudaError_t launch_grad_norm(const moe_adamw_tensor_t* x, int n, double max_norm
   });
   if (e != cudaSuccess) return e;
   count_launches(1);
-  // a limit above zero may be zero in fp32: then the factor is, too
-  return launch_after(norm_kernel, 1, kNormThreads, s, sums, used, max_norm > 0, (float)max_norm,
-                      norm);
+  // a limit above zero may be zero in fp32: then the factor is, too; one above the fp32
+  // range does not meet an infinite norm as another infinity
+  return launch_after(norm_kernel, 1, kNormThreads, s, sums, used, max_norm > 0,
+                      (float)std::min(max_norm, (double)FLT_MAX), norm);
 }
 
 cudaError_t launch_adamw(const moe_adamw_tensor_t* x, int n, const moe_adamw_t& h,

@@ -618,8 +618,9 @@ typedef struct {
  * tensors: host array of n_tensors (only g, g_dtype and n are used; read before
  * the call returns).  norm: fp32 [4] on the device.  Squares are summed in fp32
  * over eight elements and in pairs of fp32 numbers (46 bits) from there, in a
- * fixed order; a norm above 1.8e19 (its square above the fp32 range) counts as
- * not finite.  Needs a workspace.
+ * fixed order.  A norm above 1.8e19 (its square above the fp32 range) is infinite,
+ * as with an infinite gradient: norm[1] is then 0 with a limit; with a NaN norm[0]
+ * and norm[1] are NaN.  Needs a workspace.
  */
 moe_status_t moe_grad_norm(const moe_adamw_tensor_t* tensors, int n_tensors, double max_norm,
                            float* norm, void* ws, size_t* ws_bytes, moe_stream_t stream);

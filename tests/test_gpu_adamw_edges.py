@@ -62,3 +62,19 @@ def test_limit_below_the_smallest_fp32_number(lib, max_norm):
     g = torch.full((1000,), 0.5, device="cuda")
     norm = norm_of(lib, [g], max_norm)
     assert norm[1:] == [0.0, 1.0, 0.0]
+
+
+@pytest.mark.parametrize("n", [40, 70001])
+@pytest.mark.parametrize("max_norm", [0.0, 2.0, 1e300, float("inf")])
+def test_record_of_norms_that_are_not_finite(lib, n, max_norm):
+    """An infinite gradient or a sum of squares above the fp32 range: norm inf, factor 0; a NaN: both
+    NaN.  Without a limit the factor is 1."""
+    inf, nan = float("inf"), float("nan")
+    for values, want in (((inf,), inf), ((-inf, 3.0), inf), ((1e25,), inf), ((1.5e19, 1.5e19), inf),
+                         ((nan,), nan), ((inf, nan), nan), ((nan, inf), nan)):
+        g = torch.full((n,), 0.01, device="cuda")
+        for k, value in enumerate(values):
+            g[(n - 1) // (k + 1)] = value
+        norm = norm_of(lib, [torch.ones(300, device="cuda"), g], max_norm)
+        factor = 1.0 if max_norm == 0 else 0.0 if want == inf else nan
+        assert np.array_equal(norm, [want, factor, 0.0, 0.0], equal_nan=True), (values, norm)
