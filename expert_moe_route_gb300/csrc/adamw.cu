@@ -768,6 +768,7 @@ cudaError_t launch_adamw(const moe_adamw_tensor_t* x, int n, const moe_adamw_t& 
       if (t.count == 0) continue;
       if (bits == 8) adamw8_kernel<<<t.chunks, AT, 0, s>>>(t);
       else adamw32_kernel<<<t.chunks, AT, 0, s>>>(t);
+      count_launches(1);
       const cudaError_t e = cudaGetLastError();
       if (e != cudaSuccess) return e;
     }

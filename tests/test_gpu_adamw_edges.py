@@ -78,3 +78,23 @@ def test_record_of_norms_that_are_not_finite(lib, n, max_norm):
         norm = norm_of(lib, [torch.ones(300, device="cuda"), g], max_norm)
         factor = 1.0 if max_norm == 0 else 0.0 if want == inf else nan
         assert np.array_equal(norm, [want, factor, 0.0, 0.0], equal_nan=True), (values, norm)
+
+
+def test_launches_are_counted(lib):
+    """A launch for each kind of state in a run of at most 256 tensors; two of the norm at least."""
+    def count(call):
+        before = lib.kernel_launches()
+        call()
+        return lib.kernel_launches() - before
+
+    def items(kinds):
+        return lib.AdamWList([make(lib, tensor(n, False, False, bits, False, 0, seed=n), 0.0)
+                              for n, bits in kinds])
+
+    norm = torch.empty(4, device="cuda")
+    for kinds, steps, norms in (([(100, 32)], 1, 2), ([(100, 8)], 1, 2), ([(100, 8), (7, 32)], 2, 2),
+                                ([(10, 32)] * 300, 2, 3), ([], 0, 1)):
+        x = items(kinds)
+        ws = lib.workspace(lib.grad_norm_ws_bytes(x))
+        assert count(lambda: lib.moe_grad_norm(x, 1.0, norm, ws)) == norms
+        assert count(lambda: lib.moe_adamw_step(x, norm=norm, **HYPER)) == steps
