@@ -645,7 +645,8 @@ def moe_grad_norm(tensors: AdamWList, max_norm, norm, ws, stream=None):
 
 def moe_adamw_step(tensors: AdamWList, lr, beta1=0.9, beta2=0.999, eps=1e-8, step=1, seed=0,
                    norm=None, stream=None):
-    """One AdamW step in place; norm: the record of moe_grad_norm (clip, skip if not finite)."""
+    """One AdamW step in place; norm: the record of moe_grad_norm (clip, skip if not finite).
+    lr, step and seed are values of the launch: replaying a captured call repeats its step."""
     _dt(norm, torch.float32, "norm"); _shape(norm, (4,), "norm")
     h = moe_adamw_t(lr, beta1, beta2, eps, step, seed)
     st = lib().moe_adamw_step(tensors.c, len(tensors), ctypes.byref(h), _p(norm), _stream(stream))

@@ -5,7 +5,10 @@
 //
 // The tensors' pointers travel as a kernel parameter, so a call needs no device
 // copy of its list and can be captured in a graph; a list longer than one
-// parameter holds becomes several launches.  Work is cut into blocks of 256
+// parameter holds becomes several launches.  lr, the step's number and the seed
+// travel with them: a replay is the captured step again (its bias correction, its
+// dither), not the next one, so a training loop launches this call itself or
+// updates the captured graph each step.  Work is cut into blocks of 256
 // elements, `run` consecutive ones a warp, eight warps a chunk, a CTA per chunk.
 //
 // 8-bit states.  Each block of 256 elements keeps one fp32 scale and E4M3 codes:

@@ -642,7 +642,11 @@ moe_status_t moe_grad_norm(const moe_adamw_tensor_t* tensors, int n_tensors, dou
  *   dither = 16 * (i even ? h mod 2^16 : h >> 16) + 8
  * Without norm the gradients have to be finite: one that is not makes its
  * parameter NaN and leaves the states of its block without meaning.
- * No workspace; the list travels in the launch.  Tensors must not overlap.
+ * No workspace; the list and the settings travel in the launch.  In a captured
+ * graph that makes every replay the same step, with the lr, bias correction and
+ * dither of the capture: capture the rest of a training step and call this one
+ * itself, or capture it anew and update the graph before each step.  Tensors must
+ * not overlap.
  * step >= 1, 0 <= beta < 1, eps at least the smallest normal fp32 number.
  */
 moe_status_t moe_adamw_step(const moe_adamw_tensor_t* tensors, int n_tensors,

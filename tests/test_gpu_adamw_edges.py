@@ -98,3 +98,23 @@ def test_launches_are_counted(lib):
         ws = lib.workspace(lib.grad_norm_ws_bytes(x))
         assert count(lambda: lib.moe_grad_norm(x, 1.0, norm, ws)) == norms
         assert count(lambda: lib.moe_adamw_step(x, norm=norm, **HYPER)) == steps
+
+
+@pytest.mark.parametrize("bits", [8, 32])
+def test_replays_repeat_the_captured_step(lib, bits):
+    """lr, step and seed are values of the call: a replay is the same step again, not the next."""
+    start = tensor(5000, True, False, bits, True, 0, seed=2)
+    results = []
+    for captured in (False, True):
+        t = {k: v.clone() for k, v in start.items()}
+        items = lib.AdamWList([make(lib, t, 0.1)])
+        if captured:
+            graph = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(graph):
+                lib.moe_adamw_step(items, **HYPER)
+        for _ in range(3):
+            graph.replay() if captured else lib.moe_adamw_step(items, **HYPER)
+        torch.cuda.synchronize()
+        results.append(t)
+    for k in start:
+        assert torch.equal(*(t[k].view(torch.uint8) for t in results)), k
