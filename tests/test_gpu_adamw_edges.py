@@ -1,10 +1,13 @@
-"""GPU: the optimiser step and the norm at the ends of their ranges.  Helpers and bounds are those
-of test_gpu_adamw."""
+"""GPU: the optimiser step and the norm at the ends of their ranges and over long lists.  Helpers and
+bounds are those of test_gpu_adamw."""
+import math
+
 import numpy as np
 import pytest
 import torch
 
-from tests.test_gpu_adamw import HYPER, make, mix, stored_on_the_host, tensor
+from tests.test_gpu_adamw import (EPS, HYPER, KINDS, check, expected, make, mix, stored_on_the_host,
+                                  tensor)
 
 pytestmark = pytest.mark.gpu
 
@@ -118,3 +121,48 @@ def test_replays_repeat_the_captured_step(lib, bits):
         results.append(t)
     for k in start:
         assert torch.equal(*(t[k].view(torch.uint8) for t in results)), k
+
+
+# what makes a warp take eight blocks in a row (8-bit states), two (32 bits) and the norm four
+LONG = 8 * 2048 * 152 * 8
+
+
+@pytest.mark.parametrize("kind", KINDS)
+def test_long_lists(lib, kind):
+    """The longest runs a warp takes, in a list with a ragged and an unaligned tensor: every element."""
+    p16, g16, bits, master = kind
+    ts = [tensor(n, p16, g16, bits, master, shift, seed=n % 1000)
+          for n, shift in ((LONG, 0), (100_003, 0), (70_001, 3))]
+    items = lib.AdamWList([make(lib, t, 0.1) for t in ts])
+    norm = torch.empty(4, device="cuda")
+    lib.moe_grad_norm(items, 1.0, norm, lib.workspace(lib.grad_norm_ws_bytes(items)))
+    total = math.sqrt(sum(float(t["g"].double().square().sum()) for t in ts))
+    # squares of 8 values in fp32: 8 e of the sum, half that of its root, and the roundings
+    assert abs(float(norm[0]) - total) <= 8 * EPS * total
+    want = [expected(t, 0.1, coef=float(norm[1])) for t in ts]
+    lib.moe_adamw_step(items, norm=norm, **HYPER)
+    for t, w in zip(ts, want):
+        check(t, w, f"n={t['p'].numel()}")
+
+
+def test_long_list_bit_for_bit(lib):
+    """Codes and scales of a list whose warps take eight blocks in a row."""
+    f = np.float32
+    t = tensor(LONG + 300, False, True, 8, False, 0, seed=4)
+    h = dict(HYPER)
+    f32 = lambda a: a.float().cpu().numpy()  # noqa: E731
+    old = {k: f32(t[k]) for k in ("m", "v", "m_scale", "v_scale", "g")}
+    lib.moe_adamw_step(lib.AdamWList([make(lib, t, 0.0)]), **h)
+    n = t["m"].numel()
+    dither = dithers(n, 0, h["seed"])
+    g = old["g"]
+    m = old["m"] * np.repeat(old["m_scale"], 256)[:n] * f(h["beta1"]) + g * f(1 - h["beta1"])
+    q = old["v"] * np.repeat(old["v_scale"], 256)[:n]
+    u = np.sqrt(q * q * f(h["beta2"]) + g * g * f(1 - h["beta2"]))
+    for name, x, least in (("m", m, 0.0), ("v", u, 2.0 ** -9)):
+        full = np.zeros(-(-n // 256) * 256, f)
+        full[:n] = np.abs(x)
+        scale = full.reshape(-1, 256).max(1) * (f(1) / f(448))
+        assert np.array_equal(f32(t[name + "_scale"]), scale), name
+        got, want = f32(t[name]), stored_on_the_host(x, scale, dither, least)
+        assert np.array_equal(got, want), f"{name}: {(got != want).sum()} differ"
