@@ -364,7 +364,9 @@ int max_cluster() {
   return g_max_cluster[dev] > 0 ? g_max_cluster[dev] : 8;
 }
 
-// Two keys a thread before the cluster grows.
+// Two keys a thread before the cluster grows.  4096 slots over 256 experts: 5.4 us (one
+// key 5.0, four 6.3); 1024 slots: 3.9 (one 4.5: two CTAs and their barriers); 16384 over
+// 64: 5.2 (5.2, 6.1); a gradient by 4096 ids of 32003: 21.5 (20.8, 23.5).
 int cluster_for(long long n) {
   const int most = max_cluster();
   int c = 1;

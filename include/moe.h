@@ -631,17 +631,22 @@ moe_status_t moe_grad_norm(const moe_adamw_tensor_t* tensors, int n_tensors, dou
  *   m = beta1 m + (1 - beta1) g',   v = beta2 v + (1 - beta2) g'^2
  *   p = p (1 - lr * weight_decay) - lr / (1 - beta1^step) * m /
  *       (sqrt(v) / sqrt(1 - beta2^step) + eps)
- * in fp32, p rounded once to its type.  With norm and norm[2] == 0 nothing is
- * changed.  8-bit states are rounded after the update has used them: per block,
- * scale = max * (1/448) and code = |value| * (1/scale) rounded to one of its two
- * E4M3 neighbours by adding 20 dither bits below the kept mantissa bits; sqrt(v) > 0
- * never rounds to 0.  m, v, sqrt(v), scales and codes are computed operation by
- * operation, each rounded to nearest, so they can be reproduced bit for bit.  Element i of the k-th tensor takes the dither
+ * in fp32, p rounded once to its type; the quotient by an approximate reciprocal,
+ * with 32-bit states the root too (each within 2^-23 of itself).  With norm and
+ * norm[2] == 0 nothing is changed.
+ * 8-bit states are rounded after the update has used them: per block, scale =
+ * max * (1/448) and code = |value| * (1/scale) rounded to one of its two E4M3
+ * neighbours by adding 20 dither bits below the kept mantissa bits; sqrt(v) > 0
+ * never rounds to 0.  Their m, v, sqrt(v), scales and codes are computed operation
+ * by operation, each rounded to nearest, so they can be reproduced bit for bit.
+ * Element i of the k-th tensor takes the dither
  *   h = mix(floor(i/2) * 0x9E3779B1 + mix(seed + k * 0x9E3779B1))   (mod 2^32)
  *   mix(x): x = (x ^ x>>16) * 0x6A09E667; x = (x ^ x>>15) * 0xBB67AE85; x ^ x>>16
  *   dither = 16 * (i even ? h mod 2^16 : h >> 16) + 8
- * Without norm the gradients have to be finite: one that is not makes its
- * parameter NaN and leaves the states of its block without meaning.
+ * Without norm the gradients and their squares have to be finite in fp32: one that
+ * is not makes its parameter NaN or leaves the states of its block without meaning.
+ * Arrays aligned to eight of their elements move fastest; a tensor with one that is
+ * not takes up to 2.2 times as long.
  * No workspace; the list and the settings travel in the launch.  In a captured
  * graph that makes every replay the same step, with the lr, bias correction and
  * dither of the capture: capture the rest of a training step and call this one
