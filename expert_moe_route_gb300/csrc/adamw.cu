@@ -464,7 +464,7 @@ __global__ void __launch_bounds__(AT) adamw32_kernel(const __grid_constant__ Ada
   if (w.left > 0) step_ragged<false>(e, t, coef, w.base, w.left);
 }
 
-// 8-bit states.  553M elements (bf16 p, fp32 g, 6.7 GB): 0.985 ms, 6.8 TB/s.  The
+// 8-bit states.  553M elements (bf16 p, fp32 g, 6.7 GB): 0.99 ms, 6.7 TB/s.  The
 // new scales of a whole chunk go out as lines from shared memory: written block
 // by block, 4 bytes at a time into lines that other CTAs read and write at the
 // same moment, the kernel took 2.3 ms.  Eight blocks a warp, loads not issued
