@@ -34,7 +34,10 @@ SYMBOLS = ("moe_status_string", "moe_version", "moe_last_cuda_error", "moe_trace
            "moe_prepack_weights", "moe_grouped_ffn", "moe_grouped_ffn_fp8",
            "moe_combine", "moe_layer_fwd", "moe_layer_bwd",
            "moe_sort_rows_bound", "moe_sort", "moe_permute", "moe_permute_bwd", "moe_unpermute",
-           "moe_unpermute_bwd", "moe_embed", "moe_embed_bwd", "moe_grad_norm", "moe_adamw_step")
+           "moe_unpermute_bwd", "moe_embed", "moe_embed_bwd", "moe_grad_norm", "moe_adamw_step",
+           "moe_route_scores", "moe_route_scores_bwd", "moe_quantize_fp8",
+           "moe_quantize_fp8_tiles", "moe_product_fp8", "moe_product_fp8_dx",
+           "moe_product_fp8_dw")
 
 # moe_dtype_t
 DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
@@ -89,6 +92,11 @@ class moe_adamw_tensor_t(ctypes.Structure):
 class moe_adamw_t(ctypes.Structure):
     _fields_ = [("lr", ctypes.c_double), ("beta1", ctypes.c_double), ("beta2", ctypes.c_double),
                 ("eps", ctypes.c_double), ("step", ctypes.c_longlong), ("seed", ctypes.c_uint32)]
+
+
+class moe_router_t(ctypes.Structure):
+    _fields_ = [("score", _i), ("groups", _i), ("top_groups", _i), ("group_keys", _i),
+                ("renormalise", _i), ("scale", ctypes.c_float)]
 
 
 def _declare(lib):
@@ -165,6 +173,23 @@ def _declare(lib):
     lib.moe_grad_norm.argtypes = [_list, _i, ctypes.c_double, _vp, _vp, _szp, _vp]
     lib.moe_adamw_step.restype = _i
     lib.moe_adamw_step.argtypes = [_list, _i, ctypes.POINTER(moe_adamw_t), _vp, _vp]
+    _router = ctypes.POINTER(moe_router_t)
+    lib.moe_route_scores.restype = _i
+    lib.moe_route_scores.argtypes = [_vp, _ll, _i, _vp, _i, _i, _i, _router, _vp, _vp, _vp]
+    lib.moe_route_scores_bwd.restype = _i
+    lib.moe_route_scores_bwd.argtypes = [_vp, _ll, _i, _vp, _vp, _i, _i, _i, _router, _vp, _ll, _vp]
+    lib.moe_quantize_fp8.restype = _i
+    lib.moe_quantize_fp8.argtypes = [_vp, _ll, _i, _i, _i, _vp, _vp, _vp, _vp, _vp]
+    lib.moe_quantize_fp8_tiles.restype = _i
+    lib.moe_quantize_fp8_tiles.argtypes = [_vp, _i, _i, _i, _i, _vp, _vp, _vp]
+    lib.moe_product_fp8.restype = _i
+    lib.moe_product_fp8.argtypes = [_vp, _vp, _vp, _i, _i, _i, _i, _vp, _vp, _vp, _ll, _i, _vp,
+                                    _szp, _u, _vp]
+    lib.moe_product_fp8_dx.restype = _i
+    lib.moe_product_fp8_dx.argtypes = lib.moe_product_fp8.argtypes
+    lib.moe_product_fp8_dw.restype = _i
+    lib.moe_product_fp8_dw.argtypes = [_vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _vp, _i, _vp, _szp,
+                                       _u, _vp]
 
 
 _LIB = None
@@ -651,6 +676,167 @@ def moe_adamw_step(tensors: AdamWList, lr, beta1=0.9, beta2=0.999, eps=1e-8, ste
     h = moe_adamw_t(lr, beta1, beta2, eps, step, seed)
     st = lib().moe_adamw_step(tensors.c, len(tensors), ctypes.byref(h), _p(norm), _stream(stream))
     _check(st, "moe_adamw_step")
+
+
+# ---------------------------------------------------------------- routing by scores
+class Router:
+    """How scores choose experts (moe_router_t): score "softmax" or "sigmoid"; experts in
+    `groups` groups of neighbours, of which the best `top_groups` take part, a group's worth
+    being the sum of its `group_keys` (1 or 2) largest keys; weights divided by their sum
+    (renormalise) and times scale."""
+
+    SCORES = {"softmax": 0, "sigmoid": 1}
+
+    def __init__(self, score="softmax", groups=1, top_groups=1, group_keys=1, renormalise=True,
+                 scale=1.0):
+        if score not in self.SCORES:
+            raise ValueError(f"score must be one of {tuple(self.SCORES)}, got {score!r}")
+        self.c = moe_router_t(self.SCORES[score], groups, top_groups, group_keys,
+                              int(bool(renormalise)), scale)
+
+
+def moe_route_scores(logits, router: Router, topk_idx, topk_w, bias=None, stream=None):
+    """The R experts of each token by score (+ bias) and their weights (see include/moe.h);
+    a logit of -inf closes an expert, slots without one get -1."""
+    pl, ldl = _rows(logits, "logits")
+    T, E = logits.shape
+    _dt(topk_idx, torch.int32, "topk_idx"); _dt(topk_w, torch.float32, "topk_w")
+    _dt(bias, torch.float32, "bias"); _shape(bias, (E,), "bias")
+    R = topk_idx.shape[1]
+    _shape(topk_idx, (T, R), "topk_idx"); _shape(topk_w, (T, R), "topk_w")
+    st = lib().moe_route_scores(pl, ldl, DTYPES[logits.dtype], _p(bias), T, E, R,
+                                ctypes.byref(router.c), _p(topk_idx), _p(topk_w), _stream(stream))
+    _check(st, "moe_route_scores")
+
+
+def moe_route_scores_bwd(logits, router: Router, topk_idx, dw, dlogits, stream=None):
+    """dlogits (every entry) given dw = dL/dtopk_w and the experts that were chosen."""
+    (pl, ldl), (pd, ldd) = _rows(logits, "logits"), _rows(dlogits, "dlogits", logits.dtype)
+    T, E = logits.shape
+    _shape(dlogits, (T, E), "dlogits")
+    _dt(topk_idx, torch.int32, "topk_idx"); _dt(dw, torch.float32, "dw")
+    R = topk_idx.shape[1]
+    _shape(topk_idx, (T, R), "topk_idx"); _shape(dw, (T, R), "dw")
+    st = lib().moe_route_scores_bwd(pl, ldl, DTYPES[logits.dtype], _p(topk_idx), _p(dw), T, E, R,
+                                    ctypes.byref(router.c), pd, ldd, _stream(stream))
+    _check(st, "moe_route_scores_bwd")
+
+
+# ---------------------------------------------------------------- products on block-scaled fp8
+_CODES = (torch.uint8, torch.float8_e4m3fn)
+
+
+def _codes(t, shape, name):
+    if t is None:
+        return None
+    if t.dtype not in _CODES:
+        raise TypeError(f"{name} must be uint8 or float8_e4m3fn, got {t.dtype}")
+    _shape(t, shape, name)
+    return _p(t)
+
+
+def _scales(t, shape, name):
+    if t is None:
+        return None
+    _dt(t, torch.float32, name); _shape(t, shape, name)
+    return _p(t)
+
+
+def fp8_blocks(n: int) -> int:
+    """Blocks of 128 that cover n elements: the length of a scales' axis."""
+    return -(-n // 128)
+
+
+def moe_quantize_fp8(x, codes=None, scales=None, col_codes=None, col_scales=None, stream=None):
+    """E4M3 codes [N, K] and fp32 scales of a matrix: by row (scales [N, ceil(K/128)]), by column
+    (col_scales [ceil(N/128), K]) or both in one pass."""
+    px, ldx = _rows(x, "x")
+    N, K = x.shape
+    b = fp8_blocks
+    st = lib().moe_quantize_fp8(px, ldx, DTYPES[x.dtype], N, K, _codes(codes, (N, K), "codes"),
+                                _scales(scales, (N, b(K)), "scales"),
+                                _codes(col_codes, (N, K), "col_codes"),
+                                _scales(col_scales, (b(N), K), "col_scales"), _stream(stream))
+    _check(st, "moe_quantize_fp8")
+
+
+def moe_quantize_fp8_tiles(w, codes, scales, stream=None):
+    """E4M3 codes of a stack w [E, n, K] with one fp32 scale per 128 x 128 tile
+    (scales [E, ceil(n/128), ceil(K/128)])."""
+    if w.dtype not in DTYPES:
+        raise TypeError(f"w must be bf16, fp16 or fp32, got {w.dtype}")
+    E, n, K = w.shape
+    st = lib().moe_quantize_fp8_tiles(_p(w), DTYPES[w.dtype], E, n, K,
+                                      _codes(codes, (E, n, K), "codes"),
+                                      _scales(scales, (E, fp8_blocks(n), fp8_blocks(K)), "scales"),
+                                      _stream(stream))
+    _check(st, "moe_quantize_fp8_tiles")
+
+
+def product_fp8_ws_bytes(N, n, K, E=1) -> int:
+    """Workspace of the three products of rows [N, K] or [N, n] and weights [E, n, K]."""
+    b = ctypes.c_size_t(0)
+    _check(lib().moe_product_fp8(None, None, None, N, n, K, E, None, None, None, n, 0, None,
+                                 ctypes.byref(b), 0, None), "moe_product_fp8(ws query)")
+    return b.value
+
+
+def _offsets(offsets, E):
+    if offsets is None:
+        if E != 1:
+            raise ValueError(f"{E} experts need offsets")
+        return None
+    _dt(offsets, torch.int32, "offsets"); _shape(offsets, (E + 1,), "offsets")
+    return _p(offsets)
+
+
+def _product(f, name, a, sa, wq, wscale, out, ws, offsets, flags, stream, back):
+    if wq.dim() == 2:
+        wq, wscale = wq[None], wscale[None]
+    E, n, K = wq.shape
+    N = a.shape[0]
+    inner, outer = (n, K) if back else (K, n)
+    po, ldo = _rows(out, "dx" if back else "out")
+    _shape(out, (N, outer), "dx" if back else "out")
+    b = ctypes.c_size_t(ws.numel())
+    st = f(_codes(a, (N, inner), "dy" if back else "x"),
+           _scales(sa, (N, fp8_blocks(inner)), "dy's scales" if back else "x's scales"),
+           _offsets(offsets, E), N, n, K, E, _codes(wq, (E, n, K), "w"),
+           _scales(wscale, (E, fp8_blocks(n), fp8_blocks(K)), "w's scales"), po, ldo,
+           DTYPES[out.dtype], _p(ws), ctypes.byref(b), flags, _stream(stream))
+    _check(st, name)
+
+
+def moe_product_fp8(x, x_scales, w, w_scales, out, ws, offsets=None, flags=0, stream=None):
+    """out[i] = x_i w[e]^T for the rows of each expert; x in the row form, w [E, n, K] (or [n, K])
+    in tiles; offsets None: one expert, all rows."""
+    _product(lib().moe_product_fp8, "moe_product_fp8", x, x_scales, w, w_scales, out, ws, offsets,
+             flags, stream, False)
+
+
+def moe_product_fp8_dx(dy, dy_scales, w, w_scales, dx, ws, offsets=None, flags=0, stream=None):
+    """dx[i] = dy_i w[e]: the product's gradient with respect to its rows."""
+    _product(lib().moe_product_fp8_dx, "moe_product_fp8_dx", dy, dy_scales, w, w_scales, dx, ws,
+             offsets, flags, stream, True)
+
+
+def moe_product_fp8_dw(dy, dy_scales, x, x_scales, dw, ws, offsets=None, accumulate=False, flags=0,
+                       stream=None):
+    """dw[e] (+)= dy^T x over the rows of each expert; dy and x in the column form, offsets in
+    multiples of 128; dw [E, n, K] (or [n, K])."""
+    if dw.dtype not in DTYPES:
+        raise TypeError(f"dw must be bf16, fp16 or fp32, got {dw.dtype}")
+    E, n, K = dw.shape if dw.dim() == 3 else (1, *dw.shape)
+    N = dy.shape[0]
+    b = ctypes.c_size_t(ws.numel())
+    st = lib().moe_product_fp8_dw(_codes(dy, (N, n), "dy"),
+                                  _scales(dy_scales, (fp8_blocks(N), n), "dy's scales"),
+                                  _codes(x, (N, K), "x"),
+                                  _scales(x_scales, (fp8_blocks(N), K), "x's scales"),
+                                  _offsets(offsets, E), N, n, K, E, _p(dw), DTYPES[dw.dtype],
+                                  _p(ws), ctypes.byref(b),
+                                  flags | (MOE_ACCUMULATE if accumulate else 0), _stream(stream))
+    _check(st, "moe_product_fp8_dw")
 
 
 # ---------------------------------------------------------------- layer

@@ -138,6 +138,11 @@ cudaError_t launch_build_tiles(const int32_t* offsets, int E, void* ws, cudaStre
 bool encode_map_2d(void* map, int dtype, const void* base, unsigned long long inner,
                    unsigned long long outer, unsigned long long row_bytes, unsigned box_inner,
                    unsigned box_outer, bool swizzle128);
+// A 3-D tensor map of E4M3 codes [planes, rows, cols] (dense), box {box_cols, box_rows, 1},
+// 128-byte swizzle; elements outside read as zeros.
+bool encode_map_codes(void* map, const void* base, unsigned long long planes,
+                      unsigned long long rows, unsigned long long cols, unsigned box_cols,
+                      unsigned box_rows);
 cudaError_t launch_ffn_fwd(const uint16_t* x_perm, const int32_t* offsets, int N, int d, int f,
                            int E, const uint16_t* W1, const uint16_t* W3, const uint16_t* W2,
                            uint16_t* a_save, uint16_t* b_save, uint16_t* h, uint16_t* out,

@@ -1,0 +1,733 @@
+// The experts' products on E4M3 operands with one fp32 scale per block of 128, on the
+// 5th-generation tensor cores (tcgen05.mma kind::f8f6f4, fp32 accumulation).
+//   PRODUCT     out[i, j] = sum_b xs[i, b] ws[j / 128, b] sum_{k in b} xq[i, k] wq[j, k]
+//   PRODUCT_DX  dx[i, k]  = sum_b dys[i, b] ws[b, k / 128] sum_{j in b} dyq[i, j] wq[j, k]
+//   PRODUCT_DW  dw[j, k]  = sum_b dys[b, j] xs[b, k] sum_{i in b} dyq[i, j] xq[i, k]
+// b runs over blocks of 128 along the contraction, i over an expert's rows.  The tensor
+// cores have no fp32 block scales, so each block's 128 x 256 products are a fresh
+// accumulator in tensor memory, and the epilogue warps add it, times its scales, to sums
+// that stay in registers (128 a thread) until the tile is complete.  Two accumulators take
+// turns, so the MMAs of block b + 1 run while block b is added.
+//
+// Roles of a CTA (320 threads): warp 0 issues the TMA loads of 128-deep k-blocks into a
+// ring, warp 1 the MMAs (four 32-deep steps a block), warps 2-9 add and store: warp w owns
+// TMEM lanes 32 (w % 4) .. and one half of the 256 columns; a thread's lane is one output
+// row.  w and the operands of PRODUCT_DW are read in the layout they have (MN-major
+// descriptors), nothing is transposed in memory.  Pairs of CTAs compute 256 x 256 tiles
+// (cta_group::2): each stages its 128 rows of A and half of B.  Every wait is bounded.
+#include <cudaTypedefs.h>
+
+#include <algorithm>
+
+#include "common.cuh"
+#include "kernels.h"
+#include "product_fp8.cuh"
+#include "rows.cuh"
+
+namespace moe {
+
+namespace {
+constexpr int BM = 128, BN = 256, BK = 128;
+constexpr int BOX = 128 * 128;                 // bytes of one loaded box
+constexpr int EPI_WARPS = 8;
+constexpr int THREADS = 64 + 32 * EPI_WARPS;
+constexpr uint32_t TMEM_COLS = 512;
+constexpr int MAX_STAGES = 6;
+constexpr int MAX_E = 1024;
+constexpr int kSms = 152;
+
+template <bool C2> struct Shape {
+  static constexpr int tile_m = C2 ? 2 * BM : BM;
+  static constexpr int boxes = C2 ? 2 : 3;     // A, and one or two halves of B
+  static constexpr int stage_bytes = boxes * BOX;
+  static constexpr int stages = C2 ? 6 : 4;
+  static constexpr uint32_t stage_tx = (uint32_t)(C2 ? 2 * stage_bytes : stage_bytes);
+  // stages | control block with the tiles' schedule | slack for 1024-byte alignment
+  static constexpr int smem_bytes = stages * stage_bytes + 4608 + 1024;
+};
+
+struct alignas(8) Ctl {
+  uint64_t full[MAX_STAGES];
+  uint64_t empty[MAX_STAGES];
+  uint64_t tfull[2];
+  uint64_t tempty[2];
+  uint64_t mma_done;
+  uint32_t tmem_base;
+  int abort;
+  int warp_sums[THREADS / 32];
+  int start[MAX_E + 1];       // first row tile of each expert
+};
+static_assert(sizeof(Ctl) <= 4608, "control block");
+
+struct Args {
+  int E, N, kblocks;          // kblocks: 128-deep blocks of the contraction (not PRODUCT_DW)
+  int cols, n_tiles_n;        // output columns and their 256-wide tiles
+  int rows, n_tiles_m;        // PRODUCT_DW: output rows an expert and their tiles
+  int splits;                 // CTAs that share a tile's contraction
+  const int32_t* offsets;
+  const float* sa;
+  const float* sb;
+  int sa_ld;                  // scales of a row of A (PRODUCT_DW: of a block)
+  int sb_ld;                  // scales of a row of tiles of w, or of a block of x
+  int sb_plane;               // scales of an expert's w
+  void* out;
+  long long ld_out;
+  int out_dtype, out_align;   // out_align: 32, 16 or the element's bytes
+  bool accumulate;
+  float* parts;               // splits > 1: fp32 [splits, N (PRODUCT_DW: E rows), cols]
+  int* err;
+};
+
+struct Item {
+  int e, row0, row_end;       // rows of the tile and the expert's end
+  int nt, mt, split;
+  int kb0, kb1;               // k-blocks (PRODUCT_DW: 128-row blocks of the whole matrix)
+};
+
+// 32 consecutive fp32 columns of this thread's TMEM lane; the values are there after
+// tmem_wait on the same registers.
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, float (&v)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]),
+        "=f"(v[7]), "=f"(v[8]), "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]),
+        "=f"(v[14]), "=f"(v[15]), "=f"(v[16]), "=f"(v[17]), "=f"(v[18]), "=f"(v[19]),
+        "=f"(v[20]), "=f"(v[21]), "=f"(v[22]), "=f"(v[23]), "=f"(v[24]), "=f"(v[25]),
+        "=f"(v[26]), "=f"(v[27]), "=f"(v[28]), "=f"(v[29]), "=f"(v[30]), "=f"(v[31])
+      : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_wait(float (&v)[32]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3]), "+f"(v[4]), "+f"(v[5]),
+                 "+f"(v[6]), "+f"(v[7]), "+f"(v[8]), "+f"(v[9]), "+f"(v[10]), "+f"(v[11]),
+                 "+f"(v[12]), "+f"(v[13]), "+f"(v[14]), "+f"(v[15]), "+f"(v[16]), "+f"(v[17]),
+                 "+f"(v[18]), "+f"(v[19]), "+f"(v[20]), "+f"(v[21]), "+f"(v[22]), "+f"(v[23]),
+                 "+f"(v[24]), "+f"(v[25]), "+f"(v[26]), "+f"(v[27]), "+f"(v[28]), "+f"(v[29]),
+                 "+f"(v[30]), "+f"(v[31])
+               :: "memory");
+}
+
+// The rows [r0, r1) of expert e; false where the offsets do not describe rows.
+template <int MODE>
+__device__ __forceinline__ bool expert_rows(const Args& g, int e, int& r0, int& r1) {
+  r0 = 0;
+  r1 = g.N;
+  if (!g.offsets) return true;
+  r0 = g.offsets[e];
+  r1 = g.offsets[e + 1];
+  if (r0 < 0 || r1 < r0 || r1 > g.N) return false;
+  return MODE != PRODUCT_DW || r0 == r1 || (r0 % BK == 0 && (r1 % BK == 0 || r1 == g.N));
+}
+
+template <int MODE, bool C2>
+__device__ __forceinline__ void decode(const Args& g, const Ctl* ctl, long long item, Item& it) {
+  const int S = g.splits;
+  const long long tile = item / S;
+  it.split = (int)(item - tile * S);
+  if (MODE == PRODUCT_DW) {
+    const int per_e = g.n_tiles_m * g.n_tiles_n;
+    it.e = (int)(tile / per_e);
+    const int rem = (int)(tile - (long long)it.e * per_e);
+    it.mt = rem / g.n_tiles_n;
+    it.nt = rem - it.mt * g.n_tiles_n;
+    int r0, r1;
+    expert_rows<MODE>(g, it.e, r0, r1);
+    it.row0 = r0;
+    it.row_end = r1;
+    const int nkb = (int)(((long long)r1 - r0 + BK - 1) / BK);
+    it.kb0 = r0 / BK + (int)((long long)nkb * it.split / S);
+    it.kb1 = r0 / BK + (int)((long long)nkb * (it.split + 1) / S);
+    return;
+  }
+  const int mi = (int)(tile / g.n_tiles_n);
+  it.nt = (int)(tile - (long long)mi * g.n_tiles_n);
+  it.mt = mi;
+  int lo = 0, hi = g.E;        // the last expert whose first tile is at most mi
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (ctl->start[mid] <= mi) lo = mid;
+    else hi = mid;
+  }
+  it.e = lo;
+  int r0, r1;
+  expert_rows<MODE>(g, lo, r0, r1);
+  it.row0 = r0 + (mi - ctl->start[lo]) * Shape<C2>::tile_m;
+  it.row_end = r1;
+  it.kb0 = (int)((long long)g.kblocks * it.split / S);
+  it.kb1 = (int)((long long)g.kblocks * (it.split + 1) / S);
+}
+
+// Every thread: the row tiles of each expert, in order; returns their number, or -1
+// where the offsets are not valid (nothing is computed then).
+template <int MODE, bool C2>
+__device__ __forceinline__ int schedule(const Args& g, Ctl* ctl) {
+  constexpr int PER = (MAX_E + THREADS - 1) / THREADS;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int e0 = threadIdx.x * PER;
+  int n[PER], sum = 0;
+  bool bad = false;
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    n[i] = 0;
+    if (e0 + i < g.E) {
+      int r0, r1;
+      if (!expert_rows<MODE>(g, e0 + i, r0, r1)) bad = true;
+      else n[i] = (int)(((long long)r1 - r0 + Shape<C2>::tile_m - 1) / Shape<C2>::tile_m);
+    }
+    sum += n[i];
+  }
+  int incl = sum;
+#pragma unroll
+  for (int off = 1; off < 32; off <<= 1) {
+    const int o = __shfl_up_sync(kFull, incl, off);
+    if (lane >= off) incl += o;
+  }
+  if (lane == 31) ctl->warp_sums[warp] = incl;
+  bad = __syncthreads_or(bad);
+  int at = incl - sum, total = 0;
+  for (int w = 0; w < THREADS / 32; ++w) {
+    if (w < warp) at += ctl->warp_sums[w];
+    total += ctl->warp_sums[w];
+  }
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    if (e0 + i < g.E) ctl->start[e0 + i] = at;
+    at += n[i];
+  }
+  __syncthreads();
+  return bad ? -1 : total;
+}
+
+// 16 finished sums of one row to `p` (a multiple of 16 columns), in the widest stores
+// that the alignment allows.
+template <typename T>
+__device__ __forceinline__ void store16(T* p, const float* v, int align, bool accumulate) {
+  if (align >= 16) {
+    if (sizeof(T) == 4) {
+      float* f = reinterpret_cast<float*>(p);
+      float o[16];
+#pragma unroll
+      for (int i = 0; i < 16; i += 4) {
+        float4 old = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (accumulate) old = *reinterpret_cast<const float4*>(f + i);
+        o[i] = v[i] + old.x; o[i + 1] = v[i + 1] + old.y;
+        o[i + 2] = v[i + 2] + old.z; o[i + 3] = v[i + 3] + old.w;
+      }
+      if (align >= 32) {
+        st_global_v8(f, o);
+        st_global_v8(f + 8, o + 8);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 16; i += 4)
+          *reinterpret_cast<float4*>(f + i) = make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+      }
+      return;
+    }
+    union {
+      T h[16];
+      Raw32 r;
+    } u;
+    if (accumulate) {
+      u.r.a = *reinterpret_cast<const uint4*>(p);
+      u.r.b = *reinterpret_cast<const uint4*>(p + 8);
+#pragma unroll
+      for (int i = 0; i < 16; ++i) u.h[i] = from_f32<T>(v[i] + to_f32(u.h[i]));
+    } else {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) u.h[i] = from_f32<T>(v[i]);
+    }
+    if (align >= 32) {
+      store32(p, u.r);
+    } else {
+      *reinterpret_cast<uint4*>(p) = u.r.a;
+      *reinterpret_cast<uint4*>(p + 8) = u.r.b;
+    }
+    return;
+  }
+  for (int i = 0; i < 16; ++i) p[i] = from_f32<T>(accumulate ? v[i] + to_f32(p[i]) : v[i]);
+}
+
+template <int MODE, bool C2, typename T>
+__global__ void __launch_bounds__(THREADS, 1)
+product_fp8_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
+                   const __grid_constant__ Args g) {
+  using Sh = Shape<C2>;
+  constexpr bool a_mn = MODE == PRODUCT_DW, b_mn = MODE != PRODUCT;
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw_addr = smem_u32(smem_raw);
+  const uint32_t tile_base = (raw_addr + 1023u) & ~1023u;
+  Ctl* ctl = reinterpret_cast<Ctl*>(smem_raw + (tile_base - raw_addr) + Sh::stages * Sh::stage_bytes);
+  volatile int* abort_flag = &ctl->abort;
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  const uint32_t rank = C2 ? cluster_rank() : 0u;   // rank 0 of a pair issues the MMAs
+  const bool leader = rank == 0;
+  const long long first_item = C2 ? cluster_index() : blockIdx.x;
+  const long long item_step = C2 ? cluster_count() : gridDim.x;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < Sh::stages; ++s) {
+      mbar_init(smem_u32(&ctl->full[s]), 1);
+      mbar_init(smem_u32(&ctl->empty[s]), 1);
+    }
+    for (int a = 0; a < 2; ++a) {
+      mbar_init(smem_u32(&ctl->tfull[a]), 1);
+      mbar_init(smem_u32(&ctl->tempty[a]), C2 ? 2 * EPI_WARPS : EPI_WARPS);
+    }
+    mbar_init(smem_u32(&ctl->mma_done), 1);
+    ctl->abort = 0;
+    fence_mbar_init();
+    tma_prefetch_desc(&tmA);
+    tma_prefetch_desc(&tmB);
+  }
+  if (warp == 1) {
+    if (C2) {
+      tmem_alloc_pair(smem_u32(&ctl->tmem_base), TMEM_COLS);
+      tmem_relinquish_pair();
+    } else {
+      tmem_alloc(smem_u32(&ctl->tmem_base), TMEM_COLS);
+      tmem_relinquish();
+    }
+  }
+  const int row_tiles = schedule<MODE, C2>(g, ctl);
+  if (row_tiles < 0 && blockIdx.x == 0 && threadIdx.x == 0 && g.err)
+    atomicOr(g.err, kErrBadRouting);
+  tc_fence_before();
+  __syncthreads();
+  if (C2) cluster_sync_all();
+  tc_fence_after();
+  const uint32_t tmem_base = ctl->tmem_base;
+  const long long total =
+      row_tiles < 0 ? 0
+                    : (MODE == PRODUCT_DW ? (long long)g.E * g.n_tiles_m : (long long)row_tiles) *
+                          g.n_tiles_n * g.splits;
+  const int col_off = (int)rank * (BN / 2);   // this CTA's half of the tile's B columns
+  const int row_off = (int)rank * BM;         // and its rows of the tile
+
+  if (warp == 0) {
+    // ------------------------------------------------------------ TMA producer
+    if (lane == 0) {
+      uint32_t count = 0;
+      bool ok = true;
+      for (long long item = first_item; item < total && ok; item += item_step) {
+        Item it;
+        decode<MODE, C2>(g, ctl, item, it);
+        for (int kb = it.kb0; kb < it.kb1; ++kb, ++count) {
+          const int s = count % Sh::stages;
+          if (!mbar_wait_bounded(smem_u32(&ctl->empty[s]), ((count / Sh::stages) & 1u) ^ 1u,
+                                 abort_flag, g.err)) {
+            ok = false;
+            break;
+          }
+          const uint32_t bar_local = smem_u32(&ctl->full[s]);
+          const uint32_t bar = C2 ? mapa_shared(bar_local, 0) : bar_local;
+          const uint32_t sa = tile_base + s * Sh::stage_bytes;
+          if (leader) mbar_arrive_expect_tx(bar_local, Sh::stage_tx);
+          auto load = [&](uint32_t dst, const CUtensorMap* m, int x, int y, int z) {
+            if (C2) tma_load_3d_pair(dst, m, bar, x, y, z);
+            else tma_load_3d(dst, m, bar, x, y, z);
+          };
+          if (MODE == PRODUCT_DW) load(sa, &tmA, it.mt * Sh::tile_m + row_off, kb * BK, 0);
+          else load(sa, &tmA, kb * BK, it.row0 + row_off, 0);
+#pragma unroll
+          for (int j = 0; j < Sh::boxes - 1; ++j) {
+            const int c = it.nt * BN + col_off + j * 128;
+            const uint32_t sb = sa + BOX + j * BOX;
+            if (MODE == PRODUCT) load(sb, &tmB, kb * BK, c, it.e);
+            else load(sb, &tmB, c, kb * BK, MODE == PRODUCT_DX ? it.e : 0);
+          }
+        }
+      }
+      if (!ok && C2) {
+        // a pair's loads signal rank 0's barriers: give those in flight time to land
+        const unsigned long long t0 = globaltimer();
+        while (globaltimer() - t0 < 200000ull) {
+        }
+      } else if (!ok) {
+        const uint32_t n = count < (uint32_t)Sh::stages ? count : (uint32_t)Sh::stages;
+        for (uint32_t q = 0; q < n; ++q) {
+          const uint32_t c = count - 1 - q;
+          volatile int never = 0;
+          mbar_wait_bounded(smem_u32(&ctl->full[c % Sh::stages]), (c / Sh::stages) & 1u, &never,
+                            nullptr);
+        }
+      }
+    }
+  } else if (warp == 1 && leader) {
+    // ------------------------------------------------------------ MMA issuer
+    constexpr uint32_t idesc = idesc_f8(Sh::tile_m, BN, a_mn, b_mn);
+    uint32_t count = 0;
+    bool ok = true, issued_any = false;
+    for (long long item = first_item; item < total && ok; item += item_step) {
+      Item it;
+      decode<MODE, C2>(g, ctl, item, it);
+      for (int kb = it.kb0; kb < it.kb1; ++kb, ++count) {
+        const int s = count % Sh::stages;
+        const uint32_t buf = count & 1u, bph = (count >> 1) & 1u;
+        ok = C2 ? mbar_wait_bounded_cluster(smem_u32(&ctl->tempty[buf]), bph ^ 1u, abort_flag, g.err)
+                : mbar_wait_bounded(smem_u32(&ctl->tempty[buf]), bph ^ 1u, abort_flag, g.err);
+        ok = ok && mbar_wait_bounded(smem_u32(&ctl->full[s]), (count / Sh::stages) & 1u,
+                                     abort_flag, g.err);
+        ok = __all_sync(kFull, ok);
+        if (!ok) break;
+        if (lane == 0) {
+          tc_fence_after();
+          const uint32_t sa = tile_base + s * Sh::stage_bytes;
+          const uint32_t sb = sa + BOX;
+#pragma unroll
+          for (int ks = 0; ks < BK / 32; ++ks) {
+            // K-major: 32 codes further along each 128-byte row; MN-major: 32 rows of 128
+            // bytes further, blocks of 128 along MN one box apart
+            const uint64_t ad = a_mn ? smem_desc_sw128(sa + ks * 4096, BOX, 1024)
+                                     : smem_desc_sw128(sa + ks * 32, 16, 1024);
+            const uint64_t bd = b_mn ? smem_desc_sw128(sb + ks * 4096, BOX, 1024)
+                                     : smem_desc_sw128(sb + ks * 32, 16, 1024);
+            tc_mma_f8<C2>(tmem_base + buf * BN, ad, bd, idesc, ks > 0 ? 1u : 0u);
+          }
+          issued_any = true;
+          if (C2) {
+            tc_commit_pair(smem_u32(&ctl->empty[s]), 3);
+            tc_commit_pair(smem_u32(&ctl->tfull[buf]), 3);
+          } else {
+            tc_commit(smem_u32(&ctl->empty[s]));
+            tc_commit(smem_u32(&ctl->tfull[buf]));
+          }
+        }
+        __syncwarp();
+      }
+    }
+    if (lane == 0 && issued_any) {   // no MMA is in flight when TMEM is released
+      if (C2) tc_commit_pair(smem_u32(&ctl->mma_done), 1);
+      else tc_commit(smem_u32(&ctl->mma_done));
+      volatile int never = 0;
+      mbar_wait_bounded(smem_u32(&ctl->mma_done), 0, &never, nullptr);
+    }
+    __syncwarp();
+  } else if (warp >= 2) {
+    // ------------------------------------------------------------ scaled sums and stores
+    const int q = warp & 3;                  // TMEM lane quadrant
+    const int half = (warp - 2) >> 2;        // columns 128 half .. of the tile
+    uint32_t count = 0;
+    bool ok = true;
+    for (long long item = first_item; item < total && ok; item += item_step) {
+      Item it;
+      decode<MODE, C2>(g, ctl, item, it);
+      const int c0 = it.nt * BN + half * 128;   // this warp's first column
+      // this thread's output row, whether it is there, and whether any of the warp's is
+      const int lead = MODE == PRODUCT_DW ? it.mt * Sh::tile_m : it.row0;
+      const int row_w = lead + row_off + q * 32;
+      const int row = row_w + lane;
+      const int row_end = MODE == PRODUCT_DW ? g.rows : it.row_end;
+      const bool any = row_w < row_end && c0 < g.cols;
+      const int srow = row < row_end ? row : row_end - 1;
+      const float* pa = MODE == PRODUCT_DW ? g.sa + srow : g.sa + (size_t)srow * g.sa_ld;
+      const float* pb =
+          MODE == PRODUCT_DW ? g.sb + c0
+          : MODE == PRODUCT  ? g.sb + (size_t)it.e * g.sb_plane + (size_t)(c0 / 128) * g.sb_ld
+                             : g.sb + (size_t)it.e * g.sb_plane + c0 / 128;
+      auto scale_a = [&](int kb) {
+        return MODE == PRODUCT_DW ? pa[(size_t)kb * g.sa_ld] : pa[kb];
+      };
+      auto scale_b = [&](int kb) {   // one factor of the whole block (not PRODUCT_DW)
+        return MODE == PRODUCT ? pb[kb] : pb[(size_t)kb * g.sb_ld];
+      };
+      float acc[128];
+#pragma unroll
+      for (int i = 0; i < 128; ++i) acc[i] = 0.f;
+      float next = 0.f;
+      if (any && it.kb0 < it.kb1)
+        next = MODE == PRODUCT_DW ? scale_a(it.kb0) : scale_a(it.kb0) * scale_b(it.kb0);
+      for (int kb = it.kb0; kb < it.kb1; ++kb, ++count) {
+        const uint32_t buf = count & 1u;
+        const float f = next;
+        if (any && kb + 1 < it.kb1)
+          next = MODE == PRODUCT_DW ? scale_a(kb + 1) : scale_a(kb + 1) * scale_b(kb + 1);
+        ok = mbar_wait_bounded(smem_u32(&ctl->tfull[buf]), (count >> 1) & 1u, abort_flag, g.err);
+        ok = __all_sync(kFull, ok);
+        if (!ok) break;
+        tc_fence_after();
+        auto release = [&]() {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) {
+            const uint32_t te = smem_u32(&ctl->tempty[buf]);
+            if (C2 && !leader) mbar_arrive_cluster(mapa_shared(te, 0));
+            else mbar_arrive(te);
+          }
+        };
+        if (!any) {
+          release();
+          continue;
+        }
+        const uint32_t t = tmem_base + ((uint32_t)(q * 32) << 16) + buf * BN + half * 128;
+        auto add = [&](float* to, const float (&v)[32], int c) {
+          if (MODE == PRODUCT_DW) {
+            const float* s = pb + (size_t)kb * g.sb_ld + c;
+#pragma unroll
+            for (int i = 0; i < 32; i += 4) {
+              float4 w = make_float4(0.f, 0.f, 0.f, 0.f);
+              if (c0 + c + i < g.cols) w = __ldg(reinterpret_cast<const float4*>(s + i));
+              to[i] = fmaf(v[i], w.x * f, to[i]);
+              to[i + 1] = fmaf(v[i + 1], w.y * f, to[i + 1]);
+              to[i + 2] = fmaf(v[i + 2], w.z * f, to[i + 2]);
+              to[i + 3] = fmaf(v[i + 3], w.w * f, to[i + 3]);
+            }
+          } else {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) to[i] = fmaf(v[i], f, to[i]);
+          }
+        };
+        float v0[32], v1[32];
+        tmem_ld32(t, v0);
+        tmem_wait(v0);
+        tmem_ld32(t + 32, v1);
+        add(acc, v0, 0);
+        tmem_wait(v1);
+        tmem_ld32(t + 64, v0);
+        add(acc + 32, v1, 32);
+        tmem_wait(v0);
+        tmem_ld32(t + 96, v1);
+        add(acc + 64, v0, 64);
+        tmem_wait(v1);
+        release();
+        add(acc + 96, v1, 96);
+      }
+      if (!ok) break;
+      if (!any || row >= row_end) continue;
+      const size_t out_row = MODE == PRODUCT_DW ? (size_t)it.e * g.rows + row : (size_t)row;
+#pragma unroll
+      for (int c = 0; c < 128; c += 16) {
+        if (c0 + c >= g.cols) break;
+        if (g.splits > 1) {
+          const size_t all = MODE == PRODUCT_DW ? (size_t)g.E * g.rows : (size_t)g.N;
+          store16(g.parts + ((size_t)it.split * all + out_row) * g.cols + c0 + c, acc + c, 16,
+                  false);
+        } else {
+          store16(static_cast<T*>(g.out) + out_row * g.ld_out + c0 + c, acc + c, g.out_align,
+                  MODE == PRODUCT_DW && g.accumulate);
+        }
+      }
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (C2) cluster_sync_all();   // the pair's MMAs, loads and remote arrivals are over
+  if (warp == 1) {
+    tc_fence_after();
+    if (C2) tmem_dealloc_pair(tmem_base, TMEM_COLS);
+    else tmem_dealloc(tmem_base, TMEM_COLS);
+  }
+}
+
+// out = the splits' parts added in order (and to what is there), for the rows that the
+// product computed: [offsets[0], offsets[E]) of the N, or all (PRODUCT_DW).  A thread takes
+// four columns.
+template <typename T, bool DW>
+__global__ void __launch_bounds__(256)
+join_parts_kernel(const float* __restrict__ parts, long long rows, const Args g,
+                  T* __restrict__ out) {
+  wait_for_previous();
+  const int splits = g.splits, cols = g.cols;
+  const long long ld_out = g.ld_out;
+  const bool accumulate = DW && g.accumulate;
+  long long r0 = 0, r1 = rows;
+  if (g.offsets) {   // offsets that are not valid: nothing was computed, nothing is written
+    bool bad = false;
+    for (int e = threadIdx.x; e < g.E; e += blockDim.x) {
+      int a, b;
+      bad |= !expert_rows<DW ? PRODUCT_DW : PRODUCT>(g, e, a, b);
+    }
+    if (__syncthreads_or(bad)) return;
+    if (!DW) {
+      r0 = g.offsets[0];
+      r1 = g.offsets[g.E];
+    }
+  }
+  const int per_row = cols / 4;
+  const long long n = (r1 - r0) * per_row;
+  for (long long i = blockIdx.x * 256LL + threadIdx.x; i < n; i += gridDim.x * 256LL) {
+    const long long r = r0 + i / per_row;
+    const int c = (int)(i % per_row) * 4;
+    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int s = 0; s < splits; ++s) {
+      const float4 p = *reinterpret_cast<const float4*>(parts + (s * rows + r) * cols + c);
+      v.x += p.x; v.y += p.y; v.z += p.z; v.w += p.w;
+    }
+    T* o = out + r * ld_out + c;
+    const float x[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) o[j] = from_f32<T>(accumulate ? x[j] + to_f32(o[j]) : x[j]);
+  }
+}
+
+int device_sms(int dev) {
+  static int n[64] = {0};
+  if (n[dev] == 0) cudaDeviceGetAttribute(&n[dev], cudaDevAttrMultiProcessorCount, dev);
+  return n[dev] > 0 ? n[dev] : kSms;
+}
+
+template <int MODE, bool C2, typename T>
+cudaError_t launch(const CUtensorMap& ma, const CUtensorMap& mb, const Args& g, long long items,
+                   cudaStream_t s) {
+  auto kernel = product_fp8_kernel<MODE, C2, T>;
+  static bool attr_done[64] = {false};
+  static int pair_slots[64] = {0};   // clusters of two that fit on the GPU at once
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.blockDim = dim3(THREADS);
+  cfg.dynamicSmemBytes = Shape<C2>::smem_bytes;
+  cfg.stream = s;
+  if (C2) {
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+  }
+  const int sms = device_sms(dev);
+  if (!attr_done[dev]) {
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             Shape<C2>::smem_bytes);
+    if (e != cudaSuccess) return e;
+    if (C2) {
+      cfg.gridDim = dim3(2 * (sms / 2));
+      int n = 0;
+      e = cudaOccupancyMaxActiveClusters(&n, kernel, &cfg);
+      if (e != cudaSuccess) return e;
+      if (n <= 0) return cudaErrorInvalidConfiguration;
+      pair_slots[dev] = n;
+    }
+    attr_done[dev] = true;
+  }
+  const long long ctas = C2 ? 2 * std::min<long long>(pair_slots[dev], items)
+                            : std::min<long long>(sms, items);
+  cfg.gridDim = dim3((unsigned)ctas);
+  e = cudaLaunchKernelEx(&cfg, kernel, ma, mb, g);
+  count_launches(1);
+  return e;
+}
+
+template <int MODE, bool C2>
+cudaError_t launch_typed(const CUtensorMap& ma, const CUtensorMap& mb, const Args& g,
+                         long long items, cudaStream_t s) {
+  switch (g.out_dtype) {
+    case MOE_BF16: return launch<MODE, C2, __nv_bfloat16>(ma, mb, g, items, s);
+    case MOE_F16: return launch<MODE, C2, __half>(ma, mb, g, items, s);
+    default: return launch<MODE, C2, float>(ma, mb, g, items, s);
+  }
+}
+
+template <typename T>
+cudaError_t join(const Args& g, bool dw, long long rows, cudaStream_t s) {
+  const long long quads = rows * (g.cols / 4);
+  const int blocks = (int)std::max<long long>(1, std::min<long long>((quads + 255) / 256, kSms * 8));
+  T* out = static_cast<T*>(g.out);
+  const cudaError_t e =
+      dw ? launch_after(join_parts_kernel<T, true>, blocks, 256, s, g.parts, rows, g, out)
+         : launch_after(join_parts_kernel<T, false>, blocks, 256, s, g.parts, rows, g, out);
+  count_launches(1);
+  return e;
+}
+
+// How a call is cut: pairs of CTAs or single ones, and over how many CTAs a tile's
+// contraction is split.  Known from the sizes alone.
+struct Cut {
+  bool pairs;
+  int splits;
+  long long items;   // an upper bound
+};
+
+Cut cut_of(int mode, int N, int n, int K, int E) {
+  const int cols = mode == PRODUCT ? n : K;
+  const int nt = ceil_div(cols, BN);
+  Cut c{false, 1, 0};
+  long long tiles;
+  int kblocks;
+  if (mode == PRODUCT_DW) {
+    tiles = (long long)E * ceil_div(n, BM) * nt;
+    kblocks = ceil_div(N, BK);
+  } else {
+    tiles = std::min<long long>(N, ((long long)N + (long long)std::min(E, N) * (BM - 1)) / BM) * nt;
+    kblocks = ceil_div(mode == PRODUCT ? K : n, BK);
+  }
+  if (2 * tiles <= kSms && kblocks >= 2)
+    c.splits = (int)std::min<long long>(kSms / tiles, kblocks);
+  c.items = tiles * c.splits;
+  return c;
+}
+
+size_t parts_bytes(int mode, int N, int n, int K, int E) {
+  const Cut c = cut_of(mode, N, n, K, E);
+  if (c.splits == 1) return 0;
+  const size_t rows = mode == PRODUCT_DW ? (size_t)E * n : (size_t)N;
+  return align_up(c.splits * rows * (mode == PRODUCT ? n : K) * 4, 256);
+}
+}  // namespace
+
+size_t product_fp8_parts_bytes(int N, int n, int K, int E) {
+  return std::max(parts_bytes(PRODUCT, N, n, K, E),
+                  std::max(parts_bytes(PRODUCT_DX, N, n, K, E), parts_bytes(PRODUCT_DW, N, n, K, E)));
+}
+
+cudaError_t launch_product_fp8(const ProductArgs& a, float* parts, int* err, cudaStream_t s) {
+  const bool dw = a.mode == PRODUCT_DW;
+  const int cols = a.mode == PRODUCT ? a.n : a.K;
+  const int inner = a.mode == PRODUCT ? a.K : a.n;   // columns of a
+  if (a.N == 0 && !dw) return cudaSuccess;
+  const Cut cut = cut_of(a.mode, a.N, a.n, a.K, a.E);
+  Args g{};
+  g.E = a.E; g.N = a.N;
+  g.kblocks = ceil_div(inner, BK);
+  g.cols = cols;
+  g.n_tiles_n = ceil_div(cols, BN);
+  g.rows = a.n;
+  g.n_tiles_m = ceil_div(a.n, cut.pairs ? 2 * BM : BM);
+  g.splits = cut.splits;
+  g.offsets = a.offsets;
+  g.sa = a.sa;
+  g.sb = a.sb;
+  g.sa_ld = dw ? a.n : ceil_div(inner, BK);
+  g.sb_ld = dw ? a.K : ceil_div(a.K, BK);
+  g.sb_plane = ceil_div(a.n, BK) * ceil_div(a.K, BK);
+  g.out = a.out;
+  g.ld_out = a.ld_out;
+  g.out_dtype = a.out_dtype;
+  const int es = dtype_bytes(a.out_dtype);
+  const unsigned long long low =
+      reinterpret_cast<uintptr_t>(a.out) | (unsigned long long)(a.ld_out * es);
+  g.out_align = low % 32 == 0 ? 32 : (low % 16 == 0 ? 16 : es);
+  g.accumulate = a.accumulate;
+  g.parts = parts;
+  g.err = err;
+  CUtensorMap ma, mb;
+  // a: [N, inner]; b: w [E, n, K], or x [N, K].  A matrix without rows is not read.
+  const void* pa = a.N > 0 ? a.a : a.out;
+  const void* pb = a.N > 0 || !dw ? a.b : a.out;
+  const int rows = std::max(a.N, 1);
+  if (!encode_map_codes(&ma, pa, 1, rows, inner, 128, 128) ||
+      !encode_map_codes(&mb, pb, dw ? 1 : a.E, dw ? rows : a.n, a.K, 128, 128))
+    return cudaErrorInvalidValue;
+  cudaError_t e;
+  switch (a.mode) {
+    case PRODUCT: e = launch_typed<PRODUCT, false>(ma, mb, g, cut.items, s); break;
+    case PRODUCT_DX: e = launch_typed<PRODUCT_DX, false>(ma, mb, g, cut.items, s); break;
+    default: e = launch_typed<PRODUCT_DW, false>(ma, mb, g, cut.items, s); break;
+  }
+  if (e != cudaSuccess || cut.splits == 1) return e;
+  const long long all = dw ? (long long)a.E * a.n : (long long)a.N;
+  switch (a.out_dtype) {
+    case MOE_BF16: return join<__nv_bfloat16>(g, dw, all, s);
+    case MOE_F16: return join<__half>(g, dw, all, s);
+    default: return join<float>(g, dw, all, s);
+  }
+}
+
+}  // namespace moe

@@ -481,7 +481,8 @@ typedef enum {
   MOE_F32 = 2
 } moe_dtype_t;
 
-#define MOE_ACCUMULATE 0x80u        /* moe_embed_bwd: add to dtable instead of overwriting it */
+#define MOE_ACCUMULATE 0x80u        /* moe_embed_bwd, moe_product_fp8_dw: add to the output instead
+                                       of overwriting it */
 
 /*
  * moe_sort_rows_bound -- the number of rows that holds every plan of moe_sort
@@ -656,6 +657,126 @@ moe_status_t moe_grad_norm(const moe_adamw_tensor_t* tensors, int n_tensors, dou
  */
 moe_status_t moe_adamw_step(const moe_adamw_tensor_t* tensors, int n_tensors,
                             const moe_adamw_t* settings, const float* norm, moe_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * Routing by scores, and products of the experts on block-scaled fp8.  (The pages
+ * name a linear router and block-scaled fp8 rows; scores, groups and products on
+ * those rows are this library's.)  Around experts of the caller's own: moe_route_scores
+ * -> moe_sort -> moe_permute -> moe_quantize_fp8 -> moe_product_fp8 -> ... ->
+ * moe_unpermute, and back.  Outputs must not overlap inputs.
+ */
+typedef enum {
+  MOE_SCORE_SOFTMAX = 0,   /* over all E experts */
+  MOE_SCORE_SIGMOID = 1
+} moe_score_t;
+
+typedef struct {
+  int score;         /* moe_score_t */
+  int groups;        /* groups of E / groups neighbouring experts; 1..32, divides E */
+  int top_groups;    /* groups whose experts may be chosen */
+  int group_keys;    /* 1 or 2: a group's worth is the sum of its so many largest keys */
+  int renormalise;   /* the weights are divided by their sum */
+  float scale;       /* and multiplied by this */
+} moe_router_t;
+
+/*
+ * moe_route_scores -- the experts of each token from its logits:
+ *   s = softmax(l) or sigmoid(l);  key = s + bias (a balance bias, e.g. raised for
+ *   experts with few tokens; NULL: none)
+ *   the top_groups groups of largest worth take part (ties: the lower group)
+ *   idx[t,:] = the R experts of largest key, in that order, ties to the lower expert
+ *   w[t,r] = scale * s[idx]                      renormalise == 0
+ *   w[t,r] = scale * s[idx] / sum_j s[idx[t,j]]  renormalise != 0
+ * The choice is that of keys computed in 64 bits from the logits and biases as they are
+ * stored (without a bias experts are ordered by their logits, which is the same order).
+ * A logit of -inf closes its expert for the token: it has score 0 and is never chosen; nor
+ * is one whose bias is -inf.  Slots that no expert is left for get idx -1, w 0 (as moe_sort
+ * takes them).  A key of NaN comes before all others and its weight is NaN; a logit of +inf
+ * makes a softmax NaN.  bias takes no part in the weights.
+ * logits: [T,E] of bf16, fp16 or fp32, rows ld_logits elements apart; bias fp32 [E];
+ * topk_idx int32 [T,R]; topk_w fp32 [T,R].  R <= 32, E <= 1024, R at most the experts of
+ * top_groups groups; group_keys 2 needs groups of two.  No workspace.
+ */
+moe_status_t moe_route_scores(const void* logits, long long ld_logits, int dtype,
+                              const float* bias, int T, int E, int R, const moe_router_t* router,
+                              int32_t* topk_idx, float* topk_w, moe_stream_t stream);
+
+/*
+ * moe_route_scores_bwd -- dlogits = dL/dlogits given dw = dL/dtopk_w (fp32 [T,R]) and the
+ * experts that the forward chose (constants).  Every logit is written: those of experts
+ * that the weights do not depend on get 0.  Slots with idx outside [0, E) and closed
+ * experts contribute nothing (their dw is not read for an empty slot); an expert named
+ * twice gets the sum.  dlogits: [T,E] of the logits' type, rows ld_dlogits apart.
+ */
+moe_status_t moe_route_scores_bwd(const void* logits, long long ld_logits, int dtype,
+                                  const int32_t* topk_idx, const float* dw, int T, int E, int R,
+                                  const moe_router_t* router, void* dlogits,
+                                  long long ld_dlogits, moe_stream_t stream);
+
+/*
+ * moe_quantize_fp8 -- E4M3 codes and fp32 scales of a matrix x [N,K]:
+ *   scale = largest |x| of a block / 448,  code = E4M3(x / scale)  (the fp32 quotient to
+ *   nearest even, saturating; 0 under a scale of 0)
+ *   row_codes uint8 [N,K],  row_scales fp32 [N, ceil(K/128)]: 128 elements of a row
+ *   col_codes uint8 [N,K],  col_scales fp32 [ceil(N/128), K]: 128 elements of a column
+ * Either pair may be NULL; both are written in one pass over x.  The last block of a row
+ * or column may be shorter.  The row form is that of moe_dispatch_fp8.  A NaN gets the code
+ * NaN and does not enter its block's scale; an infinity makes the scale infinite.
+ * x: bf16, fp16 or fp32, rows ldx elements apart; K a multiple of 16; codes 16-byte
+ * aligned.  No workspace.
+ */
+moe_status_t moe_quantize_fp8(const void* x, long long ldx, int dtype, int N, int K,
+                              uint8_t* row_codes, float* row_scales, uint8_t* col_codes,
+                              float* col_scales, moe_stream_t stream);
+
+/*
+ * moe_quantize_fp8_tiles -- the same of a stack w [E,n,K] (dense) with one scale per tile
+ * of 128 x 128: codes uint8 [E,n,K], scales fp32 [E, ceil(n/128), ceil(K/128)].
+ */
+moe_status_t moe_quantize_fp8_tiles(const void* w, int dtype, int E, int n, int K, uint8_t* codes,
+                                    float* scales, moe_stream_t stream);
+
+/*
+ * moe_product_fp8 -- each expert's product on its rows, on the fp8 tensor cores:
+ *   out[i] = x_i w[e]^T   for the rows i in [offsets[e], offsets[e+1])
+ * with x and w the values of their codes and scales; the codes' products of a block of 128
+ * are summed in fp32, those sums times both scales in fp32, one rounding at the end.
+ * xq, xs: rows [N,K] in the row form; wq, wscale: [E,n,K] in tiles; out: [N,n] of bf16, fp16
+ * or fp32, rows ld_out elements apart.  offsets: int32 [E+1] on the device, not falling, in
+ * [0, N]; NULL with E == 1: all N rows (a plain matrix product).  Rows outside every segment
+ * are not read and left as they are.  Offsets that are not valid are reported
+ * (MOE_ERR_BAD_ROUTING with MOE_CHECK) and nothing is computed.
+ * n and K are multiples of 16, N <= 2^30, E <= 1024; codes 16-byte aligned.  The workspace
+ * (error word; sums of few tiles split over several CTAs) is the same for the three
+ * products of one N, n, K, E.
+ */
+moe_status_t moe_product_fp8(const uint8_t* xq, const float* xs, const int32_t* offsets, int N,
+                             int n, int K, int E, const uint8_t* wq, const float* wscale,
+                             void* out, long long ld_out, int out_dtype, void* ws,
+                             size_t* ws_bytes, unsigned flags, moe_stream_t stream);
+
+/*
+ * moe_product_fp8_dx -- its gradient with respect to the rows:
+ *   dx[i] = dy_i w[e]
+ * dyq, dys: dL/dout [N,n] in the row form; dx: [N,K]; the rest as above.
+ */
+moe_status_t moe_product_fp8_dx(const uint8_t* dyq, const float* dys, const int32_t* offsets,
+                                int N, int n, int K, int E, const uint8_t* wq,
+                                const float* wscale, void* dx, long long ld_dx, int dx_dtype,
+                                void* ws, size_t* ws_bytes, unsigned flags, moe_stream_t stream);
+
+/*
+ * moe_product_fp8_dw -- its gradient with respect to the weights:
+ *   dw[e] = sum over the rows i of e of dy_i^T x_i     (zeros for an expert without rows)
+ * dyq, dys: dL/dout [N,n], xq, xs: [N,K], both in the column form.  Blocks of 128 rows
+ * belong to one expert: offsets are multiples of 128 (moe_sort with align 128), a segment
+ * that ends at N may end anywhere.  dw: [E,n,K] of bf16, fp16 or fp32, dense, 16-byte
+ * aligned; with MOE_ACCUMULATE the sum is added to it.  xs and dys 16-byte aligned.
+ */
+moe_status_t moe_product_fp8_dw(const uint8_t* dyq, const float* dys, const uint8_t* xq,
+                                const float* xs, const int32_t* offsets, int N, int n, int K,
+                                int E, void* dw, int dw_dtype, void* ws, size_t* ws_bytes,
+                                unsigned flags, moe_stream_t stream);
 
 #ifdef __cplusplus
 }
