@@ -30,7 +30,20 @@ namespace {
 constexpr int BM = 128, BN = 256, BK = 128;
 constexpr int BOX = 128 * 128;                 // bytes of one loaded box
 constexpr int EPI_WARPS = 8;
-constexpr int THREADS = 64 + 32 * EPI_WARPS;
+constexpr int CW = 4 * BN / EPI_WARPS;         // columns a warp
+constexpr int SCALE_WARP0 = 2;                 // warps 0, 1: loads, MMAs; 2, 3: scales
+constexpr int EPI_WARP0 = 4;
+constexpr int THREADS = 32 * (EPI_WARP0 + EPI_WARPS);
+// Registers: 384 threads are launched with 168 each (64512); warps 0-3 give some up, the
+// epilogue warps, with 128 sums and 64 loaded values a thread, take them.
+constexpr int REGS = 168, REGS_CONTROL = 72, REGS_EPI = 216;
+static_assert(128 * REGS_CONTROL + 32 * EPI_WARPS * REGS_EPI == THREADS * REGS, "registers");
+template <int N> __device__ __forceinline__ void fewer_registers() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N> __device__ __forceinline__ void more_registers() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
 constexpr uint32_t TMEM_COLS = 512;
 constexpr int MAX_STAGES = 6;
 constexpr int MAX_E = 1024;
@@ -42,9 +55,20 @@ template <bool C2> struct Shape {
   static constexpr int stage_bytes = boxes * BOX;
   static constexpr int stages = C2 ? 6 : 4;
   static constexpr uint32_t stage_tx = (uint32_t)(C2 ? 2 * stage_bytes : stage_bytes);
-  // stages | control block with the tiles' schedule | slack for 1024-byte alignment
-  static constexpr int smem_bytes = stages * stage_bytes + 4608 + 1024;
 };
+// Blocks' scales in shared memory: for each of the CTA's 128 rows the product of both
+// operands' scales, once for either half of the columns; PRODUCT_DW: the rows' scales and the
+// 256 columns'.  A slot is written when the accumulator two blocks before it is full: every
+// epilogue warp has then given back the one four blocks before, so it has read the scales of
+// the one five blocks before.
+template <int MODE> struct Ring {
+  static constexpr int slots = 8;
+  static constexpr int floats = 128 + (MODE == PRODUCT_DW ? BN : 128);
+  static constexpr int bytes = slots * floats * 4;
+};
+// stages | scales | control block with the tiles' schedule | slack for 1024-byte alignment
+template <int MODE, bool C2>
+constexpr int kSmem = Shape<C2>::stages * Shape<C2>::stage_bytes + Ring<MODE>::bytes + 4608 + 1024;
 
 struct alignas(8) Ctl {
   uint64_t full[MAX_STAGES];
@@ -67,6 +91,7 @@ struct Args {
   const int32_t* offsets;
   const float* sa;
   const float* sb;
+  bool sa_vec;                // four scales of a row of A are an aligned vector
   int sa_ld;                  // scales of a row of A (PRODUCT_DW: of a block)
   int sb_ld;                  // scales of a row of tiles of w, or of a block of x
   int sb_plane;               // scales of an expert's w
@@ -85,7 +110,7 @@ struct Item {
 };
 
 // 32 consecutive fp32 columns of this thread's TMEM lane; the values are there after
-// tmem_wait on the same registers.
+// tmem_ld_wait.
 __device__ __forceinline__ void tmem_ld32(uint32_t taddr, float (&v)[32]) {
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
@@ -98,15 +123,18 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, float (&v)[32]) {
         "=f"(v[26]), "=f"(v[27]), "=f"(v[28]), "=f"(v[29]), "=f"(v[30]), "=f"(v[31])
       : "r"(taddr));
 }
-__device__ __forceinline__ void tmem_wait(float (&v)[32]) {
-  asm volatile("tcgen05.wait::ld.sync.aligned;"
-               : "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3]), "+f"(v[4]), "+f"(v[5]),
-                 "+f"(v[6]), "+f"(v[7]), "+f"(v[8]), "+f"(v[9]), "+f"(v[10]), "+f"(v[11]),
-                 "+f"(v[12]), "+f"(v[13]), "+f"(v[14]), "+f"(v[15]), "+f"(v[16]), "+f"(v[17]),
-                 "+f"(v[18]), "+f"(v[19]), "+f"(v[20]), "+f"(v[21]), "+f"(v[22]), "+f"(v[23]),
-                 "+f"(v[24]), "+f"(v[25]), "+f"(v[26]), "+f"(v[27]), "+f"(v[28]), "+f"(v[29]),
-                 "+f"(v[30]), "+f"(v[31])
-               :: "memory");
+// The loads of tmem_ld32 so far have landed.  Their values are used by asm volatile only
+// (add_scaled), which stays behind this; naming the 32 registers here as operands costs a
+// move each.
+// a += b c, in the order of the loads around it.
+__device__ __forceinline__ void add_scaled(float& a, float b, float c) {
+  asm volatile("fma.rn.f32 %0, %1, %2, %0;" : "+f"(a) : "f"(b), "f"(c));
+}
+// Arrive on an mbarrier of the pair's other CTA.  No data goes with it but the accumulator's
+// release, which tcgen05.fence orders: a release at cluster scope would wait for this thread's
+// copies and stores as well (a block of the pair kernel took 1.9 us of its 0.4 with it).
+__device__ __forceinline__ void mbar_arrive_remote(uint32_t cluster_addr) {
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
 }
 
 // The rows [r0, r1) of expert e; false where the offsets do not describe rows.
@@ -121,15 +149,20 @@ __device__ __forceinline__ bool expert_rows(const Args& g, int e, int& r0, int& 
   return MODE != PRODUCT_DW || r0 == r1 || (r0 % BK == 0 && (r1 % BK == 0 || r1 == g.N));
 }
 
+// Where part `i` of S of n blocks begins.
+__device__ __forceinline__ int share(int n, int i, int S) {
+  return S == 1 ? n * i : (int)((long long)n * i / S);
+}
+
 template <int MODE, bool C2>
-__device__ __forceinline__ void decode(const Args& g, const Ctl* ctl, long long item, Item& it) {
+__device__ __forceinline__ void decode(const Args& g, const Ctl* ctl, int item, Item& it) {
   const int S = g.splits;
-  const long long tile = item / S;
-  it.split = (int)(item - tile * S);
+  const int tile = item / S;
+  it.split = item - tile * S;
   if (MODE == PRODUCT_DW) {
     const int per_e = g.n_tiles_m * g.n_tiles_n;
-    it.e = (int)(tile / per_e);
-    const int rem = (int)(tile - (long long)it.e * per_e);
+    it.e = tile / per_e;
+    const int rem = tile - it.e * per_e;
     it.mt = rem / g.n_tiles_n;
     it.nt = rem - it.mt * g.n_tiles_n;
     int r0, r1;
@@ -137,12 +170,12 @@ __device__ __forceinline__ void decode(const Args& g, const Ctl* ctl, long long 
     it.row0 = r0;
     it.row_end = r1;
     const int nkb = (int)(((long long)r1 - r0 + BK - 1) / BK);
-    it.kb0 = r0 / BK + (int)((long long)nkb * it.split / S);
-    it.kb1 = r0 / BK + (int)((long long)nkb * (it.split + 1) / S);
+    it.kb0 = r0 / BK + share(nkb, it.split, S);
+    it.kb1 = r0 / BK + share(nkb, it.split + 1, S);
     return;
   }
-  const int mi = (int)(tile / g.n_tiles_n);
-  it.nt = (int)(tile - (long long)mi * g.n_tiles_n);
+  const int mi = tile / g.n_tiles_n;
+  it.nt = tile - mi * g.n_tiles_n;
   it.mt = mi;
   int lo = 0, hi = g.E;        // the last expert whose first tile is at most mi
   while (hi - lo > 1) {
@@ -155,8 +188,8 @@ __device__ __forceinline__ void decode(const Args& g, const Ctl* ctl, long long 
   expert_rows<MODE>(g, lo, r0, r1);
   it.row0 = r0 + (mi - ctl->start[lo]) * Shape<C2>::tile_m;
   it.row_end = r1;
-  it.kb0 = (int)((long long)g.kblocks * it.split / S);
-  it.kb1 = (int)((long long)g.kblocks * (it.split + 1) / S);
+  it.kb0 = share(g.kblocks, it.split, S);
+  it.kb1 = share(g.kblocks, it.split + 1, S);
 }
 
 // Every thread: the row tiles of each expert, in order; returns their number, or -1
@@ -258,14 +291,15 @@ product_fp8_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constan
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw_addr = smem_u32(smem_raw);
   const uint32_t tile_base = (raw_addr + 1023u) & ~1023u;
-  Ctl* ctl = reinterpret_cast<Ctl*>(smem_raw + (tile_base - raw_addr) + Sh::stages * Sh::stage_bytes);
+  uint8_t* after = smem_raw + (tile_base - raw_addr) + Sh::stages * Sh::stage_bytes;
+  Ctl* ctl = reinterpret_cast<Ctl*>(after + Ring<MODE>::bytes);
   volatile int* abort_flag = &ctl->abort;
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
   const uint32_t rank = C2 ? cluster_rank() : 0u;   // rank 0 of a pair issues the MMAs
   const bool leader = rank == 0;
-  const long long first_item = C2 ? cluster_index() : blockIdx.x;
-  const long long item_step = C2 ? cluster_count() : gridDim.x;
+  const int first_item = C2 ? cluster_index() : blockIdx.x;
+  const int item_step = C2 ? cluster_count() : gridDim.x;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < Sh::stages; ++s) {
@@ -273,7 +307,7 @@ product_fp8_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constan
       mbar_init(smem_u32(&ctl->empty[s]), 1);
     }
     for (int a = 0; a < 2; ++a) {
-      mbar_init(smem_u32(&ctl->tfull[a]), 1);
+      mbar_init(smem_u32(&ctl->tfull[a]), 1 + EPI_WARP0 - SCALE_WARP0);   // MMAs, scales
       mbar_init(smem_u32(&ctl->tempty[a]), C2 ? 2 * EPI_WARPS : EPI_WARPS);
     }
     mbar_init(smem_u32(&ctl->mma_done), 1);
@@ -299,19 +333,20 @@ product_fp8_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constan
   if (C2) cluster_sync_all();
   tc_fence_after();
   const uint32_t tmem_base = ctl->tmem_base;
-  const long long total =
-      row_tiles < 0 ? 0
-                    : (MODE == PRODUCT_DW ? (long long)g.E * g.n_tiles_m : (long long)row_tiles) *
-                          g.n_tiles_n * g.splits;
+  // below 2^30 for all sizes that a call may have
+  const int total = row_tiles < 0 ? 0
+                                  : (MODE == PRODUCT_DW ? g.E * g.n_tiles_m : row_tiles) *
+                                        g.n_tiles_n * g.splits;
   const int col_off = (int)rank * (BN / 2);   // this CTA's half of the tile's B columns
   const int row_off = (int)rank * BM;         // and its rows of the tile
 
+  if (warp < EPI_WARP0) fewer_registers<REGS_CONTROL>();
   if (warp == 0) {
     // ------------------------------------------------------------ TMA producer
     if (lane == 0) {
       uint32_t count = 0;
       bool ok = true;
-      for (long long item = first_item; item < total && ok; item += item_step) {
+      for (int item = first_item; item < total && ok; item += item_step) {
         Item it;
         decode<MODE, C2>(g, ctl, item, it);
         for (int kb = it.kb0; kb < it.kb1; ++kb, ++count) {
@@ -356,156 +391,243 @@ product_fp8_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constan
       }
     }
   } else if (warp == 1 && leader) {
-    // ------------------------------------------------------------ MMA issuer
-    constexpr uint32_t idesc = idesc_f8(Sh::tile_m, BN, a_mn, b_mn);
-    uint32_t count = 0;
-    bool ok = true, issued_any = false;
-    for (long long item = first_item; item < total && ok; item += item_step) {
-      Item it;
-      decode<MODE, C2>(g, ctl, item, it);
-      for (int kb = it.kb0; kb < it.kb1; ++kb, ++count) {
-        const int s = count % Sh::stages;
-        const uint32_t buf = count & 1u, bph = (count >> 1) & 1u;
-        ok = C2 ? mbar_wait_bounded_cluster(smem_u32(&ctl->tempty[buf]), bph ^ 1u, abort_flag, g.err)
-                : mbar_wait_bounded(smem_u32(&ctl->tempty[buf]), bph ^ 1u, abort_flag, g.err);
-        ok = ok && mbar_wait_bounded(smem_u32(&ctl->full[s]), (count / Sh::stages) & 1u,
-                                     abort_flag, g.err);
-        ok = __all_sync(kFull, ok);
-        if (!ok) break;
-        if (lane == 0) {
+    // ------------------------------------------------------------ MMA issuer (one thread)
+    // The tensor pipe holds few MMAs: this thread has to be back with the next block's
+    // within a quarter of a block's time, so its loop does nothing but wait and issue.
+    if (lane == 0) {
+      constexpr uint32_t idesc = idesc_f8(Sh::tile_m, BN, a_mn, b_mn);
+      // K-major: 32 codes further along each 128-byte row; MN-major: 32 rows of 128 bytes
+      // further, blocks of 128 along MN one box apart
+      constexpr uint32_t a_step = (a_mn ? 4096 : 32) >> 4, b_step = (b_mn ? 4096 : 32) >> 4;
+      const uint64_t a_base = smem_desc_sw128(tile_base, a_mn ? BOX : 16, 1024);
+      const uint64_t b_base = smem_desc_sw128(tile_base + BOX, b_mn ? BOX : 16, 1024);
+      const uint32_t full0 = smem_u32(&ctl->full[0]), empty0 = smem_u32(&ctl->empty[0]);
+      const uint32_t tfull0 = smem_u32(&ctl->tfull[0]), tempty0 = smem_u32(&ctl->tempty[0]);
+      uint32_t s = 0, ph = 0, count = 0;      // stage, its phase, blocks so far
+      bool ok = true;
+      for (int item = first_item; item < total && ok; item += item_step) {
+        Item it;
+        decode<MODE, C2>(g, ctl, item, it);
+        for (int kb = it.kb0; kb < it.kb1; ++kb) {
+          const uint32_t buf = count & 1u;
+          ok = mbar_wait_bounded(full0 + 8 * s, ph, abort_flag, g.err) &&
+               mbar_wait_bounded(tempty0 + 8 * buf, ((count >> 1) & 1u) ^ 1u, abort_flag, g.err);
+          if (!ok) break;
           tc_fence_after();
-          const uint32_t sa = tile_base + s * Sh::stage_bytes;
-          const uint32_t sb = sa + BOX;
+          const uint64_t ad = a_base + s * (Sh::stage_bytes >> 4);
+          const uint64_t bd = b_base + s * (Sh::stage_bytes >> 4);
+          const uint32_t d = tmem_base + buf * BN;
 #pragma unroll
-          for (int ks = 0; ks < BK / 32; ++ks) {
-            // K-major: 32 codes further along each 128-byte row; MN-major: 32 rows of 128
-            // bytes further, blocks of 128 along MN one box apart
-            const uint64_t ad = a_mn ? smem_desc_sw128(sa + ks * 4096, BOX, 1024)
-                                     : smem_desc_sw128(sa + ks * 32, 16, 1024);
-            const uint64_t bd = b_mn ? smem_desc_sw128(sb + ks * 4096, BOX, 1024)
-                                     : smem_desc_sw128(sb + ks * 32, 16, 1024);
-            tc_mma_f8<C2>(tmem_base + buf * BN, ad, bd, idesc, ks > 0 ? 1u : 0u);
-          }
-          issued_any = true;
+          for (uint32_t ks = 0; ks < BK / 32; ++ks)
+            tc_mma_f8<C2>(d, ad + ks * a_step, bd + ks * b_step, idesc, ks > 0 ? 1u : 0u);
           if (C2) {
-            tc_commit_pair(smem_u32(&ctl->empty[s]), 3);
-            tc_commit_pair(smem_u32(&ctl->tfull[buf]), 3);
+            tc_commit_pair(tfull0 + 8 * buf, 3);
+            tc_commit_pair(empty0 + 8 * s, 3);
           } else {
-            tc_commit(smem_u32(&ctl->empty[s]));
-            tc_commit(smem_u32(&ctl->tfull[buf]));
+            tc_commit(tfull0 + 8 * buf);
+            tc_commit(empty0 + 8 * s);
+          }
+          ++count;
+          if (++s == Sh::stages) {
+            s = 0;
+            ph ^= 1u;
           }
         }
-        __syncwarp();
       }
-    }
-    if (lane == 0 && issued_any) {   // no MMA is in flight when TMEM is released
-      if (C2) tc_commit_pair(smem_u32(&ctl->mma_done), 1);
-      else tc_commit(smem_u32(&ctl->mma_done));
-      volatile int never = 0;
-      mbar_wait_bounded(smem_u32(&ctl->mma_done), 0, &never, nullptr);
+      if (count > 0) {   // no MMA is in flight when TMEM is released
+        if (C2) tc_commit_pair(smem_u32(&ctl->mma_done), 1);
+        else tc_commit(smem_u32(&ctl->mma_done));
+        volatile int never = 0;
+        mbar_wait_bounded(smem_u32(&ctl->mma_done), 0, &never, nullptr);
+      }
     }
     __syncwarp();
-  } else if (warp >= 2) {
-    // ------------------------------------------------------------ scaled sums and stores
-    const int q = warp & 3;                  // TMEM lane quadrant
-    const int half = (warp - 2) >> 2;        // columns 128 half .. of the tile
+  } else if (warp >= SCALE_WARP0 && warp < EPI_WARP0) {
+    // ------------------------------------------------------------ scales to shared memory
+    using Rg = Ring<MODE>;
+    constexpr int PT = 32 * (EPI_WARP0 - SCALE_WARP0);   // threads; each has rows tid, tid + 64
+    const int tid = threadIdx.x - 32 * SCALE_WARP0;
+    float* const ring = reinterpret_cast<float*>(after);
     uint32_t count = 0;
     bool ok = true;
-    for (long long item = first_item; item < total && ok; item += item_step) {
+    for (int item = first_item; item < total && ok; item += item_step) {
       Item it;
       decode<MODE, C2>(g, ctl, item, it);
-      const int c0 = it.nt * BN + half * 128;   // this warp's first column
-      // this thread's output row, whether it is there, and whether any of the warp's is
-      const int lead = MODE == PRODUCT_DW ? it.mt * Sh::tile_m : it.row0;
-      const int row_w = lead + row_off + q * 32;
-      const int row = row_w + lane;
       const int row_end = MODE == PRODUCT_DW ? g.rows : it.row_end;
-      const bool any = row_w < row_end && c0 < g.cols;
-      const int srow = row < row_end ? row : row_end - 1;
-      const float* pa = MODE == PRODUCT_DW ? g.sa + srow : g.sa + (size_t)srow * g.sa_ld;
-      const float* pb =
-          MODE == PRODUCT_DW ? g.sb + c0
-          : MODE == PRODUCT  ? g.sb + (size_t)it.e * g.sb_plane + (size_t)(c0 / 128) * g.sb_ld
-                             : g.sb + (size_t)it.e * g.sb_plane + c0 / 128;
-      auto scale_a = [&](int kb) {
-        return MODE == PRODUCT_DW ? pa[(size_t)kb * g.sa_ld] : pa[kb];
-      };
-      auto scale_b = [&](int kb) {   // one factor of the whole block (not PRODUCT_DW)
-        return MODE == PRODUCT ? pb[kb] : pb[(size_t)kb * g.sb_ld];
-      };
-      float acc[128];
+      const int row = (MODE == PRODUCT_DW ? it.mt * Sh::tile_m : it.row0) + row_off + tid;
+      const float *pa[2], *pb[2];
 #pragma unroll
-      for (int i = 0; i < 128; ++i) acc[i] = 0.f;
-      float next = 0.f;
-      if (any && it.kb0 < it.kb1)
-        next = MODE == PRODUCT_DW ? scale_a(it.kb0) : scale_a(it.kb0) * scale_b(it.kb0);
-      for (int kb = it.kb0; kb < it.kb1; ++kb, ++count) {
+      for (int i = 0; i < 2; ++i) {
+        const int r = min(row + PT * i, row_end - 1);    // rows past the end: any
+        if (MODE == PRODUCT_DW) {
+          pa[i] = g.sa + (size_t)it.kb0 * g.sa_ld + r;
+          pb[i] = g.sb + (size_t)it.kb0 * g.sb_ld + min(it.nt * BN + 4 * tid, g.cols - 4);
+        } else {
+          pa[i] = g.sa + (size_t)r * g.sa_ld + it.kb0;
+          const int c = min(2 * it.nt + i, (g.cols - 1) / 128);
+          pb[i] = g.sb + (size_t)it.e * g.sb_plane +
+                  (MODE == PRODUCT ? (size_t)c * g.sb_ld + it.kb0 : (size_t)it.kb0 * g.sb_ld + c);
+        }
+      }
+      float a[2][4], b[2][4];
+      float4 cols = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int kb = it.kb0; kb < it.kb1 && ok; ++kb, ++count) {
         const uint32_t buf = count & 1u;
-        const float f = next;
-        if (any && kb + 1 < it.kb1)
-          next = MODE == PRODUCT_DW ? scale_a(kb + 1) : scale_a(kb + 1) * scale_b(kb + 1);
-        ok = mbar_wait_bounded(smem_u32(&ctl->tfull[buf]), (count >> 1) & 1u, abort_flag, g.err);
+        const int left = it.kb1 - kb;
+        if (MODE == PRODUCT_DW) {
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            a[i][0] = __ldg(pa[i]);
+            pa[i] += g.sa_ld;
+          }
+          cols = __ldg(reinterpret_cast<const float4*>(pb[0]));
+          pb[0] += g.sb_ld;
+        } else if (((kb - it.kb0) & 3) == 0) {           // four blocks at a time
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            if (g.sa_vec && left >= 4) {
+              const float4 v = __ldg(reinterpret_cast<const float4*>(pa[i]));
+              a[i][0] = v.x; a[i][1] = v.y; a[i][2] = v.z; a[i][3] = v.w;
+            } else {
+#pragma unroll
+              for (int j = 0; j < 4; ++j) a[i][j] = j < left ? __ldg(pa[i] + j) : 0.f;
+            }
+            pa[i] += 4;
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              b[i][j] = j < left ? __ldg(pb[i] + (MODE == PRODUCT ? j : (size_t)j * g.sb_ld)) : 0.f;
+            pb[i] += MODE == PRODUCT ? 4 : (size_t)4 * g.sb_ld;
+          }
+        }
+        ok = mbar_wait_bounded(smem_u32(&ctl->tfull[buf]), ((count >> 1) & 1u) ^ 1u, abort_flag,
+                               g.err);
         ok = __all_sync(kFull, ok);
         if (!ok) break;
-        tc_fence_after();
-        auto release = [&]() {
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) {
-            const uint32_t te = smem_u32(&ctl->tempty[buf]);
-            if (C2 && !leader) mbar_arrive_cluster(mapa_shared(te, 0));
-            else mbar_arrive(te);
-          }
-        };
-        if (!any) {
-          release();
-          continue;
-        }
-        const uint32_t t = tmem_base + ((uint32_t)(q * 32) << 16) + buf * BN + half * 128;
-        auto add = [&](float* to, const float (&v)[32], int c) {
-          if (MODE == PRODUCT_DW) {
-            const float* s = pb + (size_t)kb * g.sb_ld + c;
+        float* slot = ring + (count % Rg::slots) * Rg::floats;
+        if (MODE == PRODUCT_DW) {
+          slot[tid] = a[0][0];
+          slot[tid + PT] = a[1][0];
+          *reinterpret_cast<float4*>(slot + 128 + 4 * tid) = cols;
+        } else {
 #pragma unroll
-            for (int i = 0; i < 32; i += 4) {
-              float4 w = make_float4(0.f, 0.f, 0.f, 0.f);
-              if (c0 + c + i < g.cols) w = __ldg(reinterpret_cast<const float4*>(s + i));
-              to[i] = fmaf(v[i], w.x * f, to[i]);
-              to[i + 1] = fmaf(v[i + 1], w.y * f, to[i + 1]);
-              to[i + 2] = fmaf(v[i + 2], w.z * f, to[i + 2]);
-              to[i + 3] = fmaf(v[i + 3], w.w * f, to[i + 3]);
+          for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) slot[128 * h + tid + PT * i] = a[i][0] * b[h][0];
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int j = 0; j < 3; ++j) {
+              a[i][j] = a[i][j + 1];
+              b[i][j] = b[i][j + 1];
             }
-          } else {
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&ctl->tfull[buf]));
+      }
+    }
+  } else if (warp >= EPI_WARP0) {
+    more_registers<REGS_EPI>();
+    // ------------------------------------------------------------ scaled sums and stores
+    using Rg = Ring<MODE>;
+    const int q = warp & 3;                  // TMEM lane quadrant
+    const int part = (warp - EPI_WARP0) >> 2;   // columns CW part .. of the tile
+    const float* const ring = reinterpret_cast<const float*>(after);
+    // this thread's output row of an item, whether it is there, and the first column
+    struct Place {
+      int row, row_end, c0;
+      bool any;                              // the warp has something to do
+    };
+    auto place = [&](const Item& it) {
+      Place p;
+      const int row_w = (MODE == PRODUCT_DW ? it.mt * Sh::tile_m : it.row0) + row_off + q * 32;
+      p.row = row_w + lane;
+      p.row_end = MODE == PRODUCT_DW ? g.rows : it.row_end;
+      p.c0 = it.nt * BN + part * CW;
+      p.any = row_w < p.row_end && p.c0 < g.cols;
+      return p;
+    };
+    uint32_t count = 0;
+    bool ok = true;
+    for (int item = first_item; item < total && ok; item += item_step) {
+      Item it;
+      decode<MODE, C2>(g, ctl, item, it);
+      const Place p = place(it);
+      float acc[CW];
 #pragma unroll
-            for (int i = 0; i < 32; ++i) to[i] = fmaf(v[i], f, to[i]);
+      for (int i = 0; i < CW; ++i) acc[i] = 0.f;
+      float v0[32], v1[32], f = 0.f;
+      uint32_t t = 0;
+      const float* w = nullptr;
+      // Waits for the next block's accumulator and scales and starts the first TMEM load.
+      auto open = [&]() {
+        const uint32_t buf = count & 1u;
+        ok = mbar_wait_bounded(smem_u32(&ctl->tfull[buf]), (count >> 1) & 1u, abort_flag, g.err);
+        ok = __all_sync(kFull, ok);
+        tc_fence_after();
+        t = tmem_base + ((uint32_t)(q * 32) << 16) + buf * BN + part * CW;
+        if (ok && p.any) tmem_ld32(t, v0);
+      };
+      // The accumulator may be written again: the loads and their wait are the whole warp's.
+      auto release = [&]() {
+        tc_fence_before();
+        if (lane == 0) {
+          const uint32_t te = smem_u32(&ctl->tempty[count & 1u]);
+          if (C2 && !leader) mbar_arrive_remote(mapa_shared(te, 0));
+          else mbar_arrive(te);
+        }
+      };
+      auto add = [&](float* to, const float (&v)[32], int c, float f, const float* w) {
+#pragma unroll
+        for (int i = 0; i < 32; i += 4) {
+          if (MODE == PRODUCT_DW) {
+            const float4 x = *reinterpret_cast<const float4*>(w + c + i);
+            add_scaled(to[i], v[i], x.x * f);
+            add_scaled(to[i + 1], v[i + 1], x.y * f);
+            add_scaled(to[i + 2], v[i + 2], x.z * f);
+            add_scaled(to[i + 3], v[i + 3], x.w * f);
+          } else {
+            add_scaled(to[i], v[i], f);
+            add_scaled(to[i + 1], v[i + 1], f);
+            add_scaled(to[i + 2], v[i + 2], f);
+            add_scaled(to[i + 3], v[i + 3], f);
           }
-        };
-        float v0[32], v1[32];
-        tmem_ld32(t, v0);
-        tmem_wait(v0);
-        tmem_ld32(t + 32, v1);
-        add(acc, v0, 0);
-        tmem_wait(v1);
-        tmem_ld32(t + 64, v0);
-        add(acc + 32, v1, 32);
-        tmem_wait(v0);
-        tmem_ld32(t + 96, v1);
-        add(acc + 64, v0, 64);
-        tmem_wait(v1);
+        }
+      };
+#pragma unroll 1
+      for (int kb = it.kb0; kb < it.kb1 && ok; ++kb) {
+        open();
+        if (!ok) break;
+        const float* slot = ring + (count % Rg::slots) * Rg::floats;
+        f = slot[MODE == PRODUCT_DW ? q * 32 + lane : part * CW / 128 * 128 + q * 32 + lane];
+        w = slot + 128 + part * CW;
+        if (p.any) {
+          tmem_ld_wait();
+          tmem_ld32(t + 32, v1);
+          add(acc, v0, 0, f, w);
+          tmem_ld_wait();
+          tmem_ld32(t + 64, v0);
+          add(acc + 32, v1, 32, f, w);
+          tmem_ld_wait();
+          tmem_ld32(t + 96, v1);
+          add(acc + 64, v0, 64, f, w);
+          tmem_ld_wait();
+        }
         release();
-        add(acc + 96, v1, 96);
+        ++count;
+        if (p.any) add(acc + 96, v1, 96, f, w);
       }
       if (!ok) break;
-      if (!any || row >= row_end) continue;
-      const size_t out_row = MODE == PRODUCT_DW ? (size_t)it.e * g.rows + row : (size_t)row;
+      if (!p.any || p.row >= p.row_end) continue;
+      const size_t out_row = MODE == PRODUCT_DW ? (size_t)it.e * g.rows + p.row : (size_t)p.row;
 #pragma unroll
-      for (int c = 0; c < 128; c += 16) {
-        if (c0 + c >= g.cols) break;
+      for (int c = 0; c < CW; c += 16) {
+        if (p.c0 + c >= g.cols) break;
         if (g.splits > 1) {
           const size_t all = MODE == PRODUCT_DW ? (size_t)g.E * g.rows : (size_t)g.N;
-          store16(g.parts + ((size_t)it.split * all + out_row) * g.cols + c0 + c, acc + c, 16,
+          store16(g.parts + ((size_t)it.split * all + out_row) * g.cols + p.c0 + c, acc + c, 16,
                   false);
         } else {
-          store16(static_cast<T*>(g.out) + out_row * g.ld_out + c0 + c, acc + c, g.out_align,
+          store16(static_cast<T*>(g.out) + out_row * g.ld_out + p.c0 + c, acc + c, g.out_align,
                   MODE == PRODUCT_DW && g.accumulate);
         }
       }
@@ -586,7 +708,7 @@ cudaError_t launch(const CUtensorMap& ma, const CUtensorMap& mb, const Args& g, 
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
   cfg.blockDim = dim3(THREADS);
-  cfg.dynamicSmemBytes = Shape<C2>::smem_bytes;
+  cfg.dynamicSmemBytes = (kSmem<MODE, C2>);
   cfg.stream = s;
   if (C2) {
     cfg.attrs = attr;
@@ -595,8 +717,12 @@ cudaError_t launch(const CUtensorMap& ma, const CUtensorMap& mb, const Args& g, 
   const int sms = device_sms(dev);
   if (!attr_done[dev]) {
     e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             Shape<C2>::smem_bytes);
+                             (kSmem<MODE, C2>));
     if (e != cudaSuccess) return e;
+    cudaFuncAttributes fa;             // more_registers waits for what the launch brings
+    e = cudaFuncGetAttributes(&fa, kernel);
+    if (e != cudaSuccess) return e;
+    if (fa.numRegs != REGS) return cudaErrorInvalidConfiguration;
     if (C2) {
       cfg.gridDim = dim3(2 * (sms / 2));
       int n = 0;
@@ -649,19 +775,25 @@ Cut cut_of(int mode, int N, int n, int K, int E) {
   const int cols = mode == PRODUCT ? n : K;
   const int nt = ceil_div(cols, BN);
   Cut c{false, 1, 0};
-  long long tiles;
-  int kblocks;
-  if (mode == PRODUCT_DW) {
-    tiles = (long long)E * ceil_div(n, BM) * nt;
-    kblocks = ceil_div(N, BK);
+  auto tiles = [&](int m) -> long long {   // row tiles of m rows times column tiles, at most
+    if (mode == PRODUCT_DW) return (long long)E * ceil_div(n, m) * nt;
+    return std::min<long long>(N, ((long long)N + (long long)std::min(E, N) * (m - 1)) / m) * nt;
+  };
+  const int kblocks = ceil_div(mode == PRODUCT_DW ? N : (mode == PRODUCT ? K : n), BK);
+  if (2 * tiles(BM) <= kSms) {
+    if (kblocks >= 2) c.splits = (int)std::min<long long>(kSms / tiles(BM), kblocks);
   } else {
-    tiles = std::min<long long>(N, ((long long)N + (long long)std::min(E, N) * (BM - 1)) / BM) * nt;
-    kblocks = ceil_div(mode == PRODUCT ? K : n, BK);
+    c.pairs = mode == PRODUCT_DW ? n > BM : N / 2 >= (long long)BM * E;
   }
-  if (2 * tiles <= kSms && kblocks >= 2)
-    c.splits = (int)std::min<long long>(kSms / tiles, kblocks);
-  c.items = tiles * c.splits;
+  c.items = tiles(c.pairs ? 2 * BM : BM) * c.splits;
   return c;
+}
+
+template <int MODE>
+cudaError_t launch_cut(const Cut& c, const CUtensorMap& ma, const CUtensorMap& mb, const Args& g,
+                       cudaStream_t s) {
+  return c.pairs ? launch_typed<MODE, true>(ma, mb, g, c.items, s)
+                 : launch_typed<MODE, false>(ma, mb, g, c.items, s);
 }
 
 size_t parts_bytes(int mode, int N, int n, int K, int E) {
@@ -696,6 +828,7 @@ cudaError_t launch_product_fp8(const ProductArgs& a, float* parts, int* err, cud
   g.sb = a.sb;
   g.sa_ld = dw ? a.n : ceil_div(inner, BK);
   g.sb_ld = dw ? a.K : ceil_div(a.K, BK);
+  g.sa_vec = g.sa_ld % 4 == 0 && reinterpret_cast<uintptr_t>(a.sa) % 16 == 0 && cut.splits == 1;
   g.sb_plane = ceil_div(a.n, BK) * ceil_div(a.K, BK);
   g.out = a.out;
   g.ld_out = a.ld_out;
@@ -717,9 +850,9 @@ cudaError_t launch_product_fp8(const ProductArgs& a, float* parts, int* err, cud
     return cudaErrorInvalidValue;
   cudaError_t e;
   switch (a.mode) {
-    case PRODUCT: e = launch_typed<PRODUCT, false>(ma, mb, g, cut.items, s); break;
-    case PRODUCT_DX: e = launch_typed<PRODUCT_DX, false>(ma, mb, g, cut.items, s); break;
-    default: e = launch_typed<PRODUCT_DW, false>(ma, mb, g, cut.items, s); break;
+    case PRODUCT: e = launch_cut<PRODUCT>(cut, ma, mb, g, s); break;
+    case PRODUCT_DX: e = launch_cut<PRODUCT_DX>(cut, ma, mb, g, s); break;
+    default: e = launch_cut<PRODUCT_DW>(cut, ma, mb, g, s); break;
   }
   if (e != cudaSuccess || cut.splits == 1) return e;
   const long long all = dw ? (long long)a.E * a.n : (long long)a.N;
