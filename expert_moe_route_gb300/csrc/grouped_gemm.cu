@@ -980,6 +980,23 @@ bool encode_map_codes(void* map, const void* base, unsigned long long planes,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+bool encode_map_out(void* map, int dtype, void* base, unsigned long long planes,
+                    unsigned long long rows, unsigned long long cols, unsigned long long ld) {
+  auto fn = encode_fn();
+  if (!fn) return false;
+  const cuuint64_t es = dtype == MOE_F32 ? 4 : 2;
+  cuuint64_t dims[3] = {(cuuint64_t)cols, (cuuint64_t)rows, (cuuint64_t)planes};
+  cuuint64_t strides[2] = {(cuuint64_t)ld * es, (cuuint64_t)(planes > 1 ? rows : 1) * ld * es};
+  cuuint32_t box[3] = {(cuuint32_t)(128 / es), 32u, 1u};
+  cuuint32_t estr[3] = {1u, 1u, 1u};
+  const CUtensorMapDataType t = dtype == MOE_F32    ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
+                                : dtype == MOE_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
+                                                   : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+  return fn(static_cast<CUtensorMap*>(map), t, 3, base, dims, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 namespace {
 int sm_count() {
   static int n[64] = {0};

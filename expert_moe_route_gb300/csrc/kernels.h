@@ -143,6 +143,10 @@ bool encode_map_2d(void* map, int dtype, const void* base, unsigned long long in
 bool encode_map_codes(void* map, const void* base, unsigned long long planes,
                       unsigned long long rows, unsigned long long cols, unsigned box_cols,
                       unsigned box_rows);
+// A 3-D tensor map of an output [planes, rows, cols] of moe_dtype_t `dtype`, rows ld elements
+// apart, box {128 bytes, 32 rows, 1}, 128-byte swizzle.
+bool encode_map_out(void* map, int dtype, void* base, unsigned long long planes,
+                    unsigned long long rows, unsigned long long cols, unsigned long long ld);
 cudaError_t launch_ffn_fwd(const uint16_t* x_perm, const int32_t* offsets, int N, int d, int f,
                            int E, const uint16_t* W1, const uint16_t* W3, const uint16_t* W2,
                            uint16_t* a_save, uint16_t* b_save, uint16_t* h, uint16_t* out,

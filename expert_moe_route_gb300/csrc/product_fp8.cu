@@ -17,6 +17,8 @@
 // (cta_group::2): each stages its 128 rows of A and half of B.  Every wait is bounded.
 #include <cudaTypedefs.h>
 
+#include <stddef.h>
+
 #include <algorithm>
 
 #include "common.cuh"
@@ -45,7 +47,7 @@ template <int N> __device__ __forceinline__ void more_registers() {
   asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
 }
 constexpr uint32_t TMEM_COLS = 512;
-constexpr int MAX_STAGES = 6;
+constexpr int MAX_STAGES = 4;
 constexpr int MAX_E = 1024;
 constexpr int kSms = 152;
 
@@ -53,7 +55,7 @@ template <bool C2> struct Shape {
   static constexpr int tile_m = C2 ? 2 * BM : BM;
   static constexpr int boxes = C2 ? 2 : 3;     // A, and one or two halves of B
   static constexpr int stage_bytes = boxes * BOX;
-  static constexpr int stages = C2 ? 6 : 4;
+  static constexpr int stages = C2 ? 4 : 3;
   static constexpr uint32_t stage_tx = (uint32_t)(C2 ? 2 * stage_bytes : stage_bytes);
 };
 // Blocks' scales in shared memory: for each of the CTA's 128 rows the product of both
@@ -62,13 +64,19 @@ template <bool C2> struct Shape {
 // epilogue warp has then given back the one four blocks before, so it has read the scales of
 // the one five blocks before.
 template <int MODE> struct Ring {
-  static constexpr int slots = 8;
+  static constexpr int slots = 5;
   static constexpr int floats = 128 + (MODE == PRODUCT_DW ? BN : 128);
   static constexpr int bytes = slots * floats * 4;
 };
-// stages | scales | control block with the tiles' schedule | slack for 1024-byte alignment
+// Finished sums on their way out: two boxes of 32 rows of 128 bytes an epilogue warp.
+constexpr int OUT_BOX = 32 * 128;
+constexpr int OUT_BYTES = EPI_WARPS * 2 * OUT_BOX;
+constexpr int CTL_BYTES = 9216;
+// stages | boxes out | scales | control block with the tiles' schedule | slack for 1024-byte
+// alignment
 template <int MODE, bool C2>
-constexpr int kSmem = Shape<C2>::stages * Shape<C2>::stage_bytes + Ring<MODE>::bytes + 4608 + 1024;
+constexpr int kSmem = Shape<C2>::stages * Shape<C2>::stage_bytes + OUT_BYTES +
+                      Ring<MODE>::bytes + CTL_BYTES + 1024;
 
 struct alignas(8) Ctl {
   uint64_t full[MAX_STAGES];
@@ -80,14 +88,33 @@ struct alignas(8) Ctl {
   int abort;
   int warp_sums[THREADS / 32];
   int start[MAX_E + 1];       // first row tile of each expert
+  int row[MAX_E + 1];         // first row
 };
-static_assert(sizeof(Ctl) <= 4608, "control block");
+static_assert(sizeof(Ctl) <= CTL_BYTES, "control block");
+
+// n / d for 0 <= n < 2^31 by a multiplication: m = floor(2^32 (2^l - d) / d) + 1 with
+// 2^(l-1) < d <= 2^l (Granlund and Montgomery, 1994).
+struct Divisor {
+  uint32_t d, m, l;
+};
+Divisor divisor(uint32_t d) {
+  uint32_t l = 0;
+  while ((1ull << l) < d) ++l;
+  return {d, (uint32_t)(((1ull << 32) * ((1ull << l) - d)) / d + 1), l};
+}
+__device__ __forceinline__ int quotient(int n, const Divisor& v) {
+  if (v.l == 0) return n;
+  const uint32_t h = __umulhi((uint32_t)n, v.m);
+  return (int)((h + (((uint32_t)n - h) >> 1)) >> (v.l - 1));
+}
 
 struct Args {
   int E, N, kblocks;          // kblocks: 128-deep blocks of the contraction (not PRODUCT_DW)
-  int cols, n_tiles_n;        // output columns and their 256-wide tiles
-  int rows, n_tiles_m;        // PRODUCT_DW: output rows an expert and their tiles
-  int splits;                 // CTAs that share a tile's contraction
+  int cols;                   // output columns
+  int rows;                   // PRODUCT_DW: output rows an expert
+  Divisor tiles_n;            // 256-wide tiles of the columns
+  Divisor tiles_m;            // PRODUCT_DW: tiles of an expert's rows
+  Divisor splits;             // CTAs that share a tile's contraction
   const int32_t* offsets;
   const float* sa;
   const float* sb;
@@ -99,12 +126,14 @@ struct Args {
   long long ld_out;
   int out_dtype, out_align;   // out_align: 32, 16 or the element's bytes
   bool accumulate;
+  bool boxed;                 // outputs leave as boxes (splits == 1, rows of 16 bytes)
   float* parts;               // splits > 1: fp32 [splits, N (PRODUCT_DW: E rows), cols]
   int* err;
 };
 
 struct Item {
-  int e, row0, row_end;       // rows of the tile and the expert's end
+  int e = 0;
+  int row0, row_end;          // rows of the tile and the expert's end
   int nt, mt, split;
   int kb0, kb1;               // k-blocks (PRODUCT_DW: 128-row blocks of the whole matrix)
 };
@@ -137,6 +166,29 @@ __device__ __forceinline__ void mbar_arrive_remote(uint32_t cluster_addr) {
   asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
 }
 
+// True in one lane of the (converged) warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t e;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(e));
+  return e != 0;
+}
+
+// At most one committed bulk group still reads shared memory.
+__device__ __forceinline__ void bulk_wait_read_1() {
+  asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
+}
+// fp32 box of shared memory added to (x, y, z), each element once: old + new, rounded to
+// nearest, as an add by the thread would be.
+__device__ __forceinline__ void tma_add_3d(const void* tmap, uint32_t src, int x, int y, int z) {
+  asm volatile(
+      "cp.reduce.async.bulk.tensor.3d.global.shared::cta.add.tile.bulk_group [%0, {%2, %3, %4}],"
+      " [%1];"
+      ::"l"(reinterpret_cast<uint64_t>(tmap)), "r"(src), "r"(x), "r"(y), "r"(z)
+      : "memory");
+}
+
 // The rows [r0, r1) of expert e; false where the offsets do not describe rows.
 template <int MODE>
 __device__ __forceinline__ bool expert_rows(const Args& g, int e, int& r0, int& r1) {
@@ -154,40 +206,31 @@ __device__ __forceinline__ int share(int n, int i, int S) {
   return S == 1 ? n * i : (int)((long long)n * i / S);
 }
 
+// Items in order: PRODUCT and PRODUCT_DX by row tile, column tile, split (activations
+// shared by neighbours); PRODUCT_DW by expert, row tile, column tile, split.  it.e is the
+// expert of this role's item before (0 at first): experts only move forward.
 template <int MODE, bool C2>
 __device__ __forceinline__ void decode(const Args& g, const Ctl* ctl, int item, Item& it) {
-  const int S = g.splits;
-  const int tile = item / S;
+  const int S = g.splits.d;
+  const int tile = quotient(item, g.splits);
   it.split = item - tile * S;
+  const int mi = quotient(tile, g.tiles_n);
+  it.nt = tile - mi * g.tiles_n.d;
   if (MODE == PRODUCT_DW) {
-    const int per_e = g.n_tiles_m * g.n_tiles_n;
-    it.e = tile / per_e;
-    const int rem = tile - it.e * per_e;
-    it.mt = rem / g.n_tiles_n;
-    it.nt = rem - it.mt * g.n_tiles_n;
-    int r0, r1;
-    expert_rows<MODE>(g, it.e, r0, r1);
+    it.e = quotient(mi, g.tiles_m);
+    it.mt = mi - it.e * g.tiles_m.d;
+    const int r0 = ctl->row[it.e], r1 = ctl->row[it.e + 1];
     it.row0 = r0;
     it.row_end = r1;
-    const int nkb = (int)(((long long)r1 - r0 + BK - 1) / BK);
+    const int nkb = ceil_div(r1 - r0, BK);
     it.kb0 = r0 / BK + share(nkb, it.split, S);
     it.kb1 = r0 / BK + share(nkb, it.split + 1, S);
     return;
   }
-  const int mi = tile / g.n_tiles_n;
-  it.nt = tile - mi * g.n_tiles_n;
   it.mt = mi;
-  int lo = 0, hi = g.E;        // the last expert whose first tile is at most mi
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (ctl->start[mid] <= mi) lo = mid;
-    else hi = mid;
-  }
-  it.e = lo;
-  int r0, r1;
-  expert_rows<MODE>(g, lo, r0, r1);
-  it.row0 = r0 + (mi - ctl->start[lo]) * Shape<C2>::tile_m;
-  it.row_end = r1;
+  while (ctl->start[it.e + 1] <= mi) ++it.e;
+  it.row0 = ctl->row[it.e] + (mi - ctl->start[it.e]) * Shape<C2>::tile_m;
+  it.row_end = ctl->row[it.e + 1];
   it.kb0 = share(g.kblocks, it.split, S);
   it.kb1 = share(g.kblocks, it.split + 1, S);
 }
@@ -207,7 +250,9 @@ __device__ __forceinline__ int schedule(const Args& g, Ctl* ctl) {
     if (e0 + i < g.E) {
       int r0, r1;
       if (!expert_rows<MODE>(g, e0 + i, r0, r1)) bad = true;
-      else n[i] = (int)(((long long)r1 - r0 + Shape<C2>::tile_m - 1) / Shape<C2>::tile_m);
+      else n[i] = ceil_div(r1 - r0, Shape<C2>::tile_m);
+      ctl->row[e0 + i] = r0;
+      if (e0 + i == g.E - 1) ctl->row[g.E] = r1;
     }
     sum += n[i];
   }
@@ -228,6 +273,7 @@ __device__ __forceinline__ int schedule(const Args& g, Ctl* ctl) {
   for (int i = 0; i < PER; ++i) {
     if (e0 + i < g.E) ctl->start[e0 + i] = at;
     at += n[i];
+    if (e0 + i == g.E - 1) ctl->start[g.E] = at;
   }
   __syncthreads();
   return bad ? -1 : total;
@@ -285,16 +331,17 @@ __device__ __forceinline__ void store16(T* p, const float* v, int align, bool ac
 template <int MODE, bool C2, typename T>
 __global__ void __launch_bounds__(THREADS, 1)
 product_fp8_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
-                   const __grid_constant__ Args g) {
+                   const __grid_constant__ CUtensorMap tmO, const __grid_constant__ Args g) {
   using Sh = Shape<C2>;
   constexpr bool a_mn = MODE == PRODUCT_DW, b_mn = MODE != PRODUCT;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw_addr = smem_u32(smem_raw);
   const uint32_t tile_base = (raw_addr + 1023u) & ~1023u;
-  uint8_t* after = smem_raw + (tile_base - raw_addr) + Sh::stages * Sh::stage_bytes;
+  uint8_t* boxes = smem_raw + (tile_base - raw_addr) + Sh::stages * Sh::stage_bytes;
+  uint8_t* after = boxes + OUT_BYTES;
   Ctl* ctl = reinterpret_cast<Ctl*>(after + Ring<MODE>::bytes);
   volatile int* abort_flag = &ctl->abort;
-  const int warp = threadIdx.x >> 5;
+  const int warp = __shfl_sync(kFull, threadIdx.x >> 5, 0);   // known to be uniform
   const int lane = threadIdx.x & 31;
   const uint32_t rank = C2 ? cluster_rank() : 0u;   // rank 0 of a pair issues the MMAs
   const bool leader = rank == 0;
@@ -315,6 +362,7 @@ product_fp8_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constan
     fence_mbar_init();
     tma_prefetch_desc(&tmA);
     tma_prefetch_desc(&tmB);
+    if (g.boxed) tma_prefetch_desc(&tmO);
   }
   if (warp == 1) {
     if (C2) {
@@ -332,11 +380,15 @@ product_fp8_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constan
   __syncthreads();
   if (C2) cluster_sync_all();
   tc_fence_after();
-  const uint32_t tmem_base = ctl->tmem_base;
   // below 2^30 for all sizes that a call may have
   const int total = row_tiles < 0 ? 0
-                                  : (MODE == PRODUCT_DW ? g.E * g.n_tiles_m : row_tiles) *
-                                        g.n_tiles_n * g.splits;
+                                  : (MODE == PRODUCT_DW ? g.E * (int)g.tiles_m.d : row_tiles) *
+                                        (int)(g.tiles_n.d * g.splits.d);
+  // warp-uniform, so that they stay in uniform registers
+  const uint32_t tmem = __shfl_sync(kFull, ctl->tmem_base, 0);
+  const uint32_t bars = __shfl_sync(kFull, smem_u32(ctl), 0);
+  constexpr uint32_t kFullBar = offsetof(Ctl, full), kEmptyBar = offsetof(Ctl, empty),
+                     kTfull = offsetof(Ctl, tfull), kTempty = offsetof(Ctl, tempty);
   const int col_off = (int)rank * (BN / 2);   // this CTA's half of the tile's B columns
   const int row_off = (int)rank * BM;         // and its rows of the tile
 
@@ -346,8 +398,8 @@ product_fp8_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constan
     if (lane == 0) {
       uint32_t count = 0;
       bool ok = true;
+      Item it;
       for (int item = first_item; item < total && ok; item += item_step) {
-        Item it;
         decode<MODE, C2>(g, ctl, item, it);
         for (int kb = it.kb0; kb < it.kb1; ++kb, ++count) {
           const int s = count % Sh::stages;
@@ -391,55 +443,58 @@ product_fp8_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constan
       }
     }
   } else if (warp == 1 && leader) {
-    // ------------------------------------------------------------ MMA issuer (one thread)
-    // The tensor pipe holds few MMAs: this thread has to be back with the next block's
-    // within a quarter of a block's time, so its loop does nothing but wait and issue.
-    if (lane == 0) {
-      constexpr uint32_t idesc = idesc_f8(Sh::tile_m, BN, a_mn, b_mn);
-      // K-major: 32 codes further along each 128-byte row; MN-major: 32 rows of 128 bytes
-      // further, blocks of 128 along MN one box apart
-      constexpr uint32_t a_step = (a_mn ? 4096 : 32) >> 4, b_step = (b_mn ? 4096 : 32) >> 4;
-      const uint64_t a_base = smem_desc_sw128(tile_base, a_mn ? BOX : 16, 1024);
-      const uint64_t b_base = smem_desc_sw128(tile_base + BOX, b_mn ? BOX : 16, 1024);
-      const uint32_t full0 = smem_u32(&ctl->full[0]), empty0 = smem_u32(&ctl->empty[0]);
-      const uint32_t tfull0 = smem_u32(&ctl->tfull[0]), tempty0 = smem_u32(&ctl->tempty[0]);
-      uint32_t s = 0, ph = 0, count = 0;      // stage, its phase, blocks so far
-      bool ok = true;
-      for (int item = first_item; item < total && ok; item += item_step) {
-        Item it;
-        decode<MODE, C2>(g, ctl, item, it);
-        for (int kb = it.kb0; kb < it.kb1; ++kb) {
-          const uint32_t buf = count & 1u;
-          ok = mbar_wait_bounded(full0 + 8 * s, ph, abort_flag, g.err) &&
-               mbar_wait_bounded(tempty0 + 8 * buf, ((count >> 1) & 1u) ^ 1u, abort_flag, g.err);
-          if (!ok) break;
-          tc_fence_after();
-          const uint64_t ad = a_base + s * (Sh::stage_bytes >> 4);
-          const uint64_t bd = b_base + s * (Sh::stage_bytes >> 4);
-          const uint32_t d = tmem_base + buf * BN;
+    // ------------------------------------------------------------ MMA issuer
+    // The whole warp walks the blocks, so that descriptors and addresses are warp-uniform
+    // values (the MMA takes them from uniform registers); one elected thread issues.
+    constexpr uint32_t idesc = idesc_f8(Sh::tile_m, BN, a_mn, b_mn);
+    // K-major: 32 codes further along each 128-byte row; MN-major: 32 rows of 128 bytes
+    // further, blocks of 128 along MN one box apart
+    constexpr uint32_t a_step = (a_mn ? 4096 : 32) >> 4, b_step = (b_mn ? 4096 : 32) >> 4;
+    const uint32_t base = __shfl_sync(kFull, tile_base, 0);
+    const uint64_t a_base = smem_desc_sw128(base, a_mn ? BOX : 16, 1024);
+    const uint64_t b_base = smem_desc_sw128(base + BOX, b_mn ? BOX : 16, 1024);
+    const bool issues = elect_one();
+    uint32_t s = 0, ph = 0, count = 0;      // stage, its phase, blocks so far
+    bool ok = true;
+    Item it;
+    for (int item = first_item; item < total && ok; item += item_step) {
+      decode<MODE, C2>(g, ctl, item, it);
+      const int blocks = __shfl_sync(kFull, it.kb1 - it.kb0, 0);
+      for (int kb = 0; kb < blocks; ++kb) {
+        const uint32_t buf = count & 1u;
+        ok = mbar_wait_bounded(bars + kFullBar + 8 * s, ph, abort_flag, g.err) &&
+             mbar_wait_bounded(bars + kTempty + 8 * buf, ((count >> 1) & 1u) ^ 1u, abort_flag,
+                               g.err);
+        ok = __all_sync(kFull, ok);
+        if (!ok) break;
+        tc_fence_after();
+        const uint64_t ad = a_base + s * (Sh::stage_bytes >> 4);
+        const uint64_t bd = b_base + s * (Sh::stage_bytes >> 4);
+        const uint32_t d = tmem + buf * BN;
+        if (issues) {
 #pragma unroll
           for (uint32_t ks = 0; ks < BK / 32; ++ks)
             tc_mma_f8<C2>(d, ad + ks * a_step, bd + ks * b_step, idesc, ks > 0 ? 1u : 0u);
           if (C2) {
-            tc_commit_pair(tfull0 + 8 * buf, 3);
-            tc_commit_pair(empty0 + 8 * s, 3);
+            tc_commit_pair(bars + kTfull + 8 * buf, 3);
+            tc_commit_pair(bars + kEmptyBar + 8 * s, 3);
           } else {
-            tc_commit(tfull0 + 8 * buf);
-            tc_commit(empty0 + 8 * s);
-          }
-          ++count;
-          if (++s == Sh::stages) {
-            s = 0;
-            ph ^= 1u;
+            tc_commit(bars + kTfull + 8 * buf);
+            tc_commit(bars + kEmptyBar + 8 * s);
           }
         }
+        ++count;
+        if (++s == Sh::stages) {
+          s = 0;
+          ph ^= 1u;
+        }
       }
-      if (count > 0) {   // no MMA is in flight when TMEM is released
-        if (C2) tc_commit_pair(smem_u32(&ctl->mma_done), 1);
-        else tc_commit(smem_u32(&ctl->mma_done));
-        volatile int never = 0;
-        mbar_wait_bounded(smem_u32(&ctl->mma_done), 0, &never, nullptr);
-      }
+    }
+    if (issues && count > 0) {   // no MMA is in flight when TMEM is released
+      if (C2) tc_commit_pair(smem_u32(&ctl->mma_done), 1);
+      else tc_commit(smem_u32(&ctl->mma_done));
+      volatile int never = 0;
+      mbar_wait_bounded(smem_u32(&ctl->mma_done), 0, &never, nullptr);
     }
     __syncwarp();
   } else if (warp >= SCALE_WARP0 && warp < EPI_WARP0) {
@@ -450,8 +505,8 @@ product_fp8_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constan
     float* const ring = reinterpret_cast<float*>(after);
     uint32_t count = 0;
     bool ok = true;
+    Item it;
     for (int item = first_item; item < total && ok; item += item_step) {
-      Item it;
       decode<MODE, C2>(g, ctl, item, it);
       const int row_end = MODE == PRODUCT_DW ? g.rows : it.row_end;
       const int row = (MODE == PRODUCT_DW ? it.mt * Sh::tile_m : it.row0) + row_off + tid;
@@ -548,30 +603,20 @@ product_fp8_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constan
     };
     uint32_t count = 0;
     bool ok = true;
+    Item it;
     for (int item = first_item; item < total && ok; item += item_step) {
-      Item it;
       decode<MODE, C2>(g, ctl, item, it);
       const Place p = place(it);
       float acc[CW];
 #pragma unroll
       for (int i = 0; i < CW; ++i) acc[i] = 0.f;
-      float v0[32], v1[32], f = 0.f;
-      uint32_t t = 0;
-      const float* w = nullptr;
-      // Waits for the next block's accumulator and scales and starts the first TMEM load.
-      auto open = [&]() {
-        const uint32_t buf = count & 1u;
-        ok = mbar_wait_bounded(smem_u32(&ctl->tfull[buf]), (count >> 1) & 1u, abort_flag, g.err);
-        ok = __all_sync(kFull, ok);
-        tc_fence_after();
-        t = tmem_base + ((uint32_t)(q * 32) << 16) + buf * BN + part * CW;
-        if (ok && p.any) tmem_ld32(t, v0);
-      };
+      float v0[32], v1[32];
+      const uint32_t lanes = tmem + ((uint32_t)(q * 32) << 16) + part * CW;
       // The accumulator may be written again: the loads and their wait are the whole warp's.
       auto release = [&]() {
         tc_fence_before();
         if (lane == 0) {
-          const uint32_t te = smem_u32(&ctl->tempty[count & 1u]);
+          const uint32_t te = bars + kTempty + 8 * (count & 1u);
           if (C2 && !leader) mbar_arrive_remote(mapa_shared(te, 0));
           else mbar_arrive(te);
         }
@@ -595,11 +640,16 @@ product_fp8_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constan
       };
 #pragma unroll 1
       for (int kb = it.kb0; kb < it.kb1 && ok; ++kb) {
-        open();
+        const uint32_t buf = count & 1u, t = lanes + buf * BN;
+        ok = mbar_wait_bounded(bars + kTfull + 8 * buf, (count >> 1) & 1u, abort_flag, g.err);
+        ok = __all_sync(kFull, ok);
         if (!ok) break;
+        tc_fence_after();
+        if (p.any) tmem_ld32(t, v0);
         const float* slot = ring + (count % Rg::slots) * Rg::floats;
-        f = slot[MODE == PRODUCT_DW ? q * 32 + lane : part * CW / 128 * 128 + q * 32 + lane];
-        w = slot + 128 + part * CW;
+        const float f =
+            slot[MODE == PRODUCT_DW ? q * 32 + lane : part * CW / 128 * 128 + q * 32 + lane];
+        const float* w = slot + 128 + part * CW;
         if (p.any) {
           tmem_ld_wait();
           tmem_ld32(t + 32, v1);
@@ -617,12 +667,48 @@ product_fp8_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constan
         if (p.any) add(acc + 96, v1, 96, f, w);
       }
       if (!ok) break;
-      if (!p.any || p.row >= p.row_end) continue;
+      if (!p.any) continue;
+      if (g.boxed && (MODE == PRODUCT_DW || p.row - lane + 32 <= p.row_end)) {
+        // whole groups of 32 rows: boxes of 128 bytes a row through shared memory, sent by
+        // bulk tensor stores (which clip at the matrix's edges)
+        constexpr int BC = 128 / sizeof(T);   // columns a box
+        const uint32_t box0 = smem_u32(boxes) + (warp - EPI_WARP0) * (2 * OUT_BOX);
+        uint8_t* row0 = boxes + (warp - EPI_WARP0) * (2 * OUT_BOX) + lane * 128;
+#pragma unroll
+        for (int c = 0; c < CW; c += BC) {
+          if (p.c0 + c >= g.cols) break;
+          const int slot = c / BC & 1;
+          if (lane == 0) {                    // the box before in this slot has been read
+            if (c < 2 * BC) bulk_wait_read_0();
+            else bulk_wait_read_1();
+          }
+          __syncwarp();
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {       // 16 bytes each, 128-byte swizzle
+            constexpr int W = 16 / sizeof(T);
+            const typename Vec<T, W>::Raw r = Vec<T, W>::pack(acc + c + j * W);
+            *reinterpret_cast<typename Vec<T, W>::Raw*>(row0 + slot * OUT_BOX +
+                                                        ((j ^ (lane & 7)) * 16)) = r;
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            const int z = MODE == PRODUCT_DW ? it.e : 0;
+            if (MODE == PRODUCT_DW && g.accumulate)
+              tma_add_3d(&tmO, box0 + slot * OUT_BOX, p.c0 + c, p.row, z);
+            else
+              tma_store_3d(&tmO, box0 + slot * OUT_BOX, p.c0 + c, p.row, z);
+            bulk_commit();
+          }
+        }
+        continue;
+      }
+      if (p.row >= p.row_end) continue;
       const size_t out_row = MODE == PRODUCT_DW ? (size_t)it.e * g.rows + p.row : (size_t)p.row;
 #pragma unroll
       for (int c = 0; c < CW; c += 16) {
         if (p.c0 + c >= g.cols) break;
-        if (g.splits > 1) {
+        if (g.splits.d > 1) {
           const size_t all = MODE == PRODUCT_DW ? (size_t)g.E * g.rows : (size_t)g.N;
           store16(g.parts + ((size_t)it.split * all + out_row) * g.cols + p.c0 + c, acc + c, 16,
                   false);
@@ -632,6 +718,8 @@ product_fp8_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constan
         }
       }
     }
+    if (lane == 0) bulk_wait_all();          // the boxes have left before shared memory goes
+    __syncwarp();
   }
 
   tc_fence_before();
@@ -639,8 +727,8 @@ product_fp8_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constan
   if (C2) cluster_sync_all();   // the pair's MMAs, loads and remote arrivals are over
   if (warp == 1) {
     tc_fence_after();
-    if (C2) tmem_dealloc_pair(tmem_base, TMEM_COLS);
-    else tmem_dealloc(tmem_base, TMEM_COLS);
+    if (C2) tmem_dealloc_pair(tmem, TMEM_COLS);
+    else tmem_dealloc(tmem, TMEM_COLS);
   }
 }
 
@@ -652,7 +740,7 @@ __global__ void __launch_bounds__(256)
 join_parts_kernel(const float* __restrict__ parts, long long rows, const Args g,
                   T* __restrict__ out) {
   wait_for_previous();
-  const int splits = g.splits, cols = g.cols;
+  const int splits = g.splits.d, cols = g.cols;
   const long long ld_out = g.ld_out;
   const bool accumulate = DW && g.accumulate;
   long long r0 = 0, r1 = rows;
@@ -692,8 +780,8 @@ int device_sms(int dev) {
 }
 
 template <int MODE, bool C2, typename T>
-cudaError_t launch(const CUtensorMap& ma, const CUtensorMap& mb, const Args& g, long long items,
-                   cudaStream_t s) {
+cudaError_t launch(const CUtensorMap& ma, const CUtensorMap& mb, const CUtensorMap& mo,
+                   const Args& g, long long items, cudaStream_t s) {
   auto kernel = product_fp8_kernel<MODE, C2, T>;
   static bool attr_done[64] = {false};
   static int pair_slots[64] = {0};   // clusters of two that fit on the GPU at once
@@ -736,18 +824,18 @@ cudaError_t launch(const CUtensorMap& ma, const CUtensorMap& mb, const Args& g, 
   const long long ctas = C2 ? 2 * std::min<long long>(pair_slots[dev], items)
                             : std::min<long long>(sms, items);
   cfg.gridDim = dim3((unsigned)ctas);
-  e = cudaLaunchKernelEx(&cfg, kernel, ma, mb, g);
+  e = cudaLaunchKernelEx(&cfg, kernel, ma, mb, mo, g);
   count_launches(1);
   return e;
 }
 
 template <int MODE, bool C2>
-cudaError_t launch_typed(const CUtensorMap& ma, const CUtensorMap& mb, const Args& g,
-                         long long items, cudaStream_t s) {
+cudaError_t launch_typed(const CUtensorMap& ma, const CUtensorMap& mb, const CUtensorMap& mo,
+                         const Args& g, long long items, cudaStream_t s) {
   switch (g.out_dtype) {
-    case MOE_BF16: return launch<MODE, C2, __nv_bfloat16>(ma, mb, g, items, s);
-    case MOE_F16: return launch<MODE, C2, __half>(ma, mb, g, items, s);
-    default: return launch<MODE, C2, float>(ma, mb, g, items, s);
+    case MOE_BF16: return launch<MODE, C2, __nv_bfloat16>(ma, mb, mo, g, items, s);
+    case MOE_F16: return launch<MODE, C2, __half>(ma, mb, mo, g, items, s);
+    default: return launch<MODE, C2, float>(ma, mb, mo, g, items, s);
   }
 }
 
@@ -790,10 +878,10 @@ Cut cut_of(int mode, int N, int n, int K, int E) {
 }
 
 template <int MODE>
-cudaError_t launch_cut(const Cut& c, const CUtensorMap& ma, const CUtensorMap& mb, const Args& g,
-                       cudaStream_t s) {
-  return c.pairs ? launch_typed<MODE, true>(ma, mb, g, c.items, s)
-                 : launch_typed<MODE, false>(ma, mb, g, c.items, s);
+cudaError_t launch_cut(const Cut& c, const CUtensorMap& ma, const CUtensorMap& mb,
+                       const CUtensorMap& mo, const Args& g, cudaStream_t s) {
+  return c.pairs ? launch_typed<MODE, true>(ma, mb, mo, g, c.items, s)
+                 : launch_typed<MODE, false>(ma, mb, mo, g, c.items, s);
 }
 
 size_t parts_bytes(int mode, int N, int n, int K, int E) {
@@ -819,16 +907,17 @@ cudaError_t launch_product_fp8(const ProductArgs& a, float* parts, int* err, cud
   g.E = a.E; g.N = a.N;
   g.kblocks = ceil_div(inner, BK);
   g.cols = cols;
-  g.n_tiles_n = ceil_div(cols, BN);
+  g.tiles_n = divisor(ceil_div(cols, BN));
   g.rows = a.n;
-  g.n_tiles_m = ceil_div(a.n, cut.pairs ? 2 * BM : BM);
-  g.splits = cut.splits;
+  g.tiles_m = divisor(ceil_div(a.n, cut.pairs ? 2 * BM : BM));
+  g.splits = divisor(cut.splits);
   g.offsets = a.offsets;
   g.sa = a.sa;
   g.sb = a.sb;
   g.sa_ld = dw ? a.n : ceil_div(inner, BK);
   g.sb_ld = dw ? a.K : ceil_div(a.K, BK);
-  g.sa_vec = g.sa_ld % 4 == 0 && reinterpret_cast<uintptr_t>(a.sa) % 16 == 0 && cut.splits == 1;
+  g.sa_vec = g.sa_ld % 4 == 0 && reinterpret_cast<uintptr_t>(a.sa) % 16 == 0 &&
+             cut.splits == 1;
   g.sb_plane = ceil_div(a.n, BK) * ceil_div(a.K, BK);
   g.out = a.out;
   g.ld_out = a.ld_out;
@@ -840,7 +929,10 @@ cudaError_t launch_product_fp8(const ProductArgs& a, float* parts, int* err, cud
   g.accumulate = a.accumulate;
   g.parts = parts;
   g.err = err;
-  CUtensorMap ma, mb;
+  // boxes out: rows of 16-byte aligned pieces; sums added to 16-bit outputs are rounded once,
+  // by the thread that reads them
+  g.boxed = cut.splits == 1 && g.out_align >= 16 && !(a.accumulate && es == 2);
+  CUtensorMap ma, mb, mo;
   // a: [N, inner]; b: w [E, n, K], or x [N, K].  A matrix without rows is not read.
   const void* pa = a.N > 0 ? a.a : a.out;
   const void* pb = a.N > 0 || !dw ? a.b : a.out;
@@ -848,11 +940,15 @@ cudaError_t launch_product_fp8(const ProductArgs& a, float* parts, int* err, cud
   if (!encode_map_codes(&ma, pa, 1, rows, inner, 128, 128) ||
       !encode_map_codes(&mb, pb, dw ? 1 : a.E, dw ? rows : a.n, a.K, 128, 128))
     return cudaErrorInvalidValue;
+  mo = ma;
+  if (g.boxed &&
+      !encode_map_out(&mo, a.out_dtype, a.out, dw ? a.E : 1, dw ? a.n : rows, cols, a.ld_out))
+    return cudaErrorInvalidValue;
   cudaError_t e;
   switch (a.mode) {
-    case PRODUCT: e = launch_cut<PRODUCT>(cut, ma, mb, g, s); break;
-    case PRODUCT_DX: e = launch_cut<PRODUCT_DX>(cut, ma, mb, g, s); break;
-    default: e = launch_cut<PRODUCT_DW>(cut, ma, mb, g, s); break;
+    case PRODUCT: e = launch_cut<PRODUCT>(cut, ma, mb, mo, g, s); break;
+    case PRODUCT_DX: e = launch_cut<PRODUCT_DX>(cut, ma, mb, mo, g, s); break;
+    default: e = launch_cut<PRODUCT_DW>(cut, ma, mb, mo, g, s); break;
   }
   if (e != cudaSuccess || cut.splits == 1) return e;
   const long long all = dw ? (long long)a.E * a.n : (long long)a.N;
