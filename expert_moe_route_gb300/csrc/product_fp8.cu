@@ -9,12 +9,20 @@
 // that stay in registers (128 a thread) until the tile is complete.  Two accumulators take
 // turns, so the MMAs of block b + 1 run while block b is added.
 //
-// Roles of a CTA (320 threads): warp 0 issues the TMA loads of 128-deep k-blocks into a
-// ring, warp 1 the MMAs (four 32-deep steps a block), warps 2-9 add and store: warp w owns
-// TMEM lanes 32 (w % 4) .. and one half of the 256 columns; a thread's lane is one output
-// row.  w and the operands of PRODUCT_DW are read in the layout they have (MN-major
-// descriptors), nothing is transposed in memory.  Pairs of CTAs compute 256 x 256 tiles
-// (cta_group::2): each stages its 128 rows of A and half of B.  Every wait is bounded.
+// Roles of a CTA (384 threads, one CTA an SM): warp 0 issues the TMA loads of 128-deep
+// k-blocks into a ring, warp 1 the MMAs (four 32-deep steps a block), warps 2 and 3 bring each
+// block's scales to shared memory, warps 4-11 add and store: warp w owns TMEM lanes
+// 32 (w % 4) .. and one half of the 256 columns; a thread's lane is one output row.  w and the
+// operands of PRODUCT_DW are read in the layout they have (MN-major descriptors), nothing is
+// transposed in memory.  Every wait is bounded.
+//
+// What bounds it (GB300, 131072 rows, 128 experts, K 4096, n 1536, 410 us at twice the measured
+// bf16 rate): loads and MMAs alone 535 us, with the handshakes of the two accumulators 605, with
+// the sums 652: a block's MMAs take 540 cycles, reading its accumulator and adding it about as
+// long, and each begins some 400 cycles after the other ended.  PRODUCT_DW has a scale a column
+// too, two operations a sum: 1306 us.  Measured against it: 16 epilogue warps +26 to +50%;
+// paired fma (f32x2) +12%; pairs of CTAs (cta_group::2, 256 x 256 tiles) -5% to +4%, and -6%
+// where experts' rows do not fill their tiles; scales copied by the epilogue warps +40%.
 #include <cudaTypedefs.h>
 
 #include <stddef.h>
@@ -47,17 +55,11 @@ template <int N> __device__ __forceinline__ void more_registers() {
   asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
 }
 constexpr uint32_t TMEM_COLS = 512;
-constexpr int MAX_STAGES = 4;
 constexpr int MAX_E = 1024;
 constexpr int kSms = 152;
 
-template <bool C2> struct Shape {
-  static constexpr int tile_m = C2 ? 2 * BM : BM;
-  static constexpr int boxes = C2 ? 2 : 3;     // A, and one or two halves of B
-  static constexpr int stage_bytes = boxes * BOX;
-  static constexpr int stages = C2 ? 4 : 3;
-  static constexpr uint32_t stage_tx = (uint32_t)(C2 ? 2 * stage_bytes : stage_bytes);
-};
+constexpr int STAGES = 3;                      // of one box of A and two of B
+constexpr int STAGE_BYTES = 3 * BOX;
 // Blocks' scales in shared memory: for each of the CTA's 128 rows the product of both
 // operands' scales, once for either half of the columns; PRODUCT_DW: the rows' scales and the
 // 256 columns'.  A slot is written when the accumulator two blocks before it is full: every
@@ -74,13 +76,12 @@ constexpr int OUT_BYTES = EPI_WARPS * 2 * OUT_BOX;
 constexpr int CTL_BYTES = 9216;
 // stages | boxes out | scales | control block with the tiles' schedule | slack for 1024-byte
 // alignment
-template <int MODE, bool C2>
-constexpr int kSmem = Shape<C2>::stages * Shape<C2>::stage_bytes + OUT_BYTES +
-                      Ring<MODE>::bytes + CTL_BYTES + 1024;
+template <int MODE>
+constexpr int kSmem = STAGES * STAGE_BYTES + OUT_BYTES + Ring<MODE>::bytes + CTL_BYTES + 1024;
 
 struct alignas(8) Ctl {
-  uint64_t full[MAX_STAGES];
-  uint64_t empty[MAX_STAGES];
+  uint64_t full[STAGES];
+  uint64_t empty[STAGES];
   uint64_t tfull[2];
   uint64_t tempty[2];
   uint64_t mma_done;
@@ -159,13 +160,6 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, float (&v)[32]) {
 __device__ __forceinline__ void add_scaled(float& a, float b, float c) {
   asm volatile("fma.rn.f32 %0, %1, %2, %0;" : "+f"(a) : "f"(b), "f"(c));
 }
-// Arrive on an mbarrier of the pair's other CTA.  No data goes with it but the accumulator's
-// release, which tcgen05.fence orders: a release at cluster scope would wait for this thread's
-// copies and stores as well (a block of the pair kernel took 1.9 us of its 0.4 with it).
-__device__ __forceinline__ void mbar_arrive_remote(uint32_t cluster_addr) {
-  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
-}
-
 // True in one lane of the (converged) warp.
 __device__ __forceinline__ bool elect_one() {
   uint32_t e;
@@ -209,7 +203,7 @@ __device__ __forceinline__ int share(int n, int i, int S) {
 // Items in order: PRODUCT and PRODUCT_DX by row tile, column tile, split (activations
 // shared by neighbours); PRODUCT_DW by expert, row tile, column tile, split.  it.e is the
 // expert of this role's item before (0 at first): experts only move forward.
-template <int MODE, bool C2>
+template <int MODE>
 __device__ __forceinline__ void decode(const Args& g, const Ctl* ctl, int item, Item& it) {
   const int S = g.splits.d;
   const int tile = quotient(item, g.splits);
@@ -229,7 +223,7 @@ __device__ __forceinline__ void decode(const Args& g, const Ctl* ctl, int item, 
   }
   it.mt = mi;
   while (ctl->start[it.e + 1] <= mi) ++it.e;
-  it.row0 = ctl->row[it.e] + (mi - ctl->start[it.e]) * Shape<C2>::tile_m;
+  it.row0 = ctl->row[it.e] + (mi - ctl->start[it.e]) * BM;
   it.row_end = ctl->row[it.e + 1];
   it.kb0 = share(g.kblocks, it.split, S);
   it.kb1 = share(g.kblocks, it.split + 1, S);
@@ -237,7 +231,7 @@ __device__ __forceinline__ void decode(const Args& g, const Ctl* ctl, int item, 
 
 // Every thread: the row tiles of each expert, in order; returns their number, or -1
 // where the offsets are not valid (nothing is computed then).
-template <int MODE, bool C2>
+template <int MODE>
 __device__ __forceinline__ int schedule(const Args& g, Ctl* ctl) {
   constexpr int PER = (MAX_E + THREADS - 1) / THREADS;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -250,7 +244,7 @@ __device__ __forceinline__ int schedule(const Args& g, Ctl* ctl) {
     if (e0 + i < g.E) {
       int r0, r1;
       if (!expert_rows<MODE>(g, e0 + i, r0, r1)) bad = true;
-      else n[i] = ceil_div(r1 - r0, Shape<C2>::tile_m);
+      else n[i] = ceil_div(r1 - r0, BM);
       ctl->row[e0 + i] = r0;
       if (e0 + i == g.E - 1) ctl->row[g.E] = r1;
     }
@@ -328,34 +322,30 @@ __device__ __forceinline__ void store16(T* p, const float* v, int align, bool ac
   for (int i = 0; i < 16; ++i) p[i] = from_f32<T>(accumulate ? v[i] + to_f32(p[i]) : v[i]);
 }
 
-template <int MODE, bool C2, typename T>
+template <int MODE, typename T>
 __global__ void __launch_bounds__(THREADS, 1)
 product_fp8_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                    const __grid_constant__ CUtensorMap tmO, const __grid_constant__ Args g) {
-  using Sh = Shape<C2>;
   constexpr bool a_mn = MODE == PRODUCT_DW, b_mn = MODE != PRODUCT;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw_addr = smem_u32(smem_raw);
   const uint32_t tile_base = (raw_addr + 1023u) & ~1023u;
-  uint8_t* boxes = smem_raw + (tile_base - raw_addr) + Sh::stages * Sh::stage_bytes;
+  uint8_t* boxes = smem_raw + (tile_base - raw_addr) + STAGES * STAGE_BYTES;
   uint8_t* after = boxes + OUT_BYTES;
   Ctl* ctl = reinterpret_cast<Ctl*>(after + Ring<MODE>::bytes);
   volatile int* abort_flag = &ctl->abort;
   const int warp = __shfl_sync(kFull, threadIdx.x >> 5, 0);   // known to be uniform
   const int lane = threadIdx.x & 31;
-  const uint32_t rank = C2 ? cluster_rank() : 0u;   // rank 0 of a pair issues the MMAs
-  const bool leader = rank == 0;
-  const int first_item = C2 ? cluster_index() : blockIdx.x;
-  const int item_step = C2 ? cluster_count() : gridDim.x;
+  const int first_item = blockIdx.x, item_step = gridDim.x;
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < Sh::stages; ++s) {
+    for (int s = 0; s < STAGES; ++s) {
       mbar_init(smem_u32(&ctl->full[s]), 1);
       mbar_init(smem_u32(&ctl->empty[s]), 1);
     }
     for (int a = 0; a < 2; ++a) {
       mbar_init(smem_u32(&ctl->tfull[a]), 1 + EPI_WARP0 - SCALE_WARP0);   // MMAs, scales
-      mbar_init(smem_u32(&ctl->tempty[a]), C2 ? 2 * EPI_WARPS : EPI_WARPS);
+      mbar_init(smem_u32(&ctl->tempty[a]), EPI_WARPS);
     }
     mbar_init(smem_u32(&ctl->mma_done), 1);
     ctl->abort = 0;
@@ -365,20 +355,14 @@ product_fp8_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constan
     if (g.boxed) tma_prefetch_desc(&tmO);
   }
   if (warp == 1) {
-    if (C2) {
-      tmem_alloc_pair(smem_u32(&ctl->tmem_base), TMEM_COLS);
-      tmem_relinquish_pair();
-    } else {
-      tmem_alloc(smem_u32(&ctl->tmem_base), TMEM_COLS);
-      tmem_relinquish();
-    }
+    tmem_alloc(smem_u32(&ctl->tmem_base), TMEM_COLS);
+    tmem_relinquish();
   }
-  const int row_tiles = schedule<MODE, C2>(g, ctl);
+  const int row_tiles = schedule<MODE>(g, ctl);
   if (row_tiles < 0 && blockIdx.x == 0 && threadIdx.x == 0 && g.err)
     atomicOr(g.err, kErrBadRouting);
   tc_fence_before();
   __syncthreads();
-  if (C2) cluster_sync_all();
   tc_fence_after();
   // below 2^30 for all sizes that a call may have
   const int total = row_tiles < 0 ? 0
@@ -389,8 +373,6 @@ product_fp8_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constan
   const uint32_t bars = __shfl_sync(kFull, smem_u32(ctl), 0);
   constexpr uint32_t kFullBar = offsetof(Ctl, full), kEmptyBar = offsetof(Ctl, empty),
                      kTfull = offsetof(Ctl, tfull), kTempty = offsetof(Ctl, tempty);
-  const int col_off = (int)rank * (BN / 2);   // this CTA's half of the tile's B columns
-  const int row_off = (int)rank * BM;         // and its rows of the tile
 
   if (warp < EPI_WARP0) fewer_registers<REGS_CONTROL>();
   if (warp == 0) {
@@ -400,53 +382,43 @@ product_fp8_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constan
       bool ok = true;
       Item it;
       for (int item = first_item; item < total && ok; item += item_step) {
-        decode<MODE, C2>(g, ctl, item, it);
+        decode<MODE>(g, ctl, item, it);
         for (int kb = it.kb0; kb < it.kb1; ++kb, ++count) {
-          const int s = count % Sh::stages;
-          if (!mbar_wait_bounded(smem_u32(&ctl->empty[s]), ((count / Sh::stages) & 1u) ^ 1u,
+          const int s = count % STAGES;
+          if (!mbar_wait_bounded(smem_u32(&ctl->empty[s]), ((count / STAGES) & 1u) ^ 1u,
                                  abort_flag, g.err)) {
             ok = false;
             break;
           }
-          const uint32_t bar_local = smem_u32(&ctl->full[s]);
-          const uint32_t bar = C2 ? mapa_shared(bar_local, 0) : bar_local;
-          const uint32_t sa = tile_base + s * Sh::stage_bytes;
-          if (leader) mbar_arrive_expect_tx(bar_local, Sh::stage_tx);
-          auto load = [&](uint32_t dst, const CUtensorMap* m, int x, int y, int z) {
-            if (C2) tma_load_3d_pair(dst, m, bar, x, y, z);
-            else tma_load_3d(dst, m, bar, x, y, z);
-          };
-          if (MODE == PRODUCT_DW) load(sa, &tmA, it.mt * Sh::tile_m + row_off, kb * BK, 0);
-          else load(sa, &tmA, kb * BK, it.row0 + row_off, 0);
-#pragma unroll
-          for (int j = 0; j < Sh::boxes - 1; ++j) {
-            const int c = it.nt * BN + col_off + j * 128;
+          const uint32_t bar = smem_u32(&ctl->full[s]);
+          const uint32_t sa = tile_base + s * STAGE_BYTES;
+          // the last tile of an odd number of 128-column halves has one of them
+          const int c = it.nt * BN, halves = c + 128 < g.cols ? 2 : 1;
+          mbar_arrive_expect_tx(bar, (1 + halves) * BOX);
+          if (MODE == PRODUCT_DW) tma_load_3d(sa, &tmA, bar, it.mt * BM, kb * BK, 0);
+          else tma_load_3d(sa, &tmA, bar, kb * BK, it.row0, 0);
+          for (int j = 0; j < halves; ++j) {
             const uint32_t sb = sa + BOX + j * BOX;
-            if (MODE == PRODUCT) load(sb, &tmB, kb * BK, c, it.e);
-            else load(sb, &tmB, c, kb * BK, MODE == PRODUCT_DX ? it.e : 0);
+            if (MODE == PRODUCT) tma_load_3d(sb, &tmB, bar, kb * BK, c + j * 128, it.e);
+            else tma_load_3d(sb, &tmB, bar, c + j * 128, kb * BK, MODE == PRODUCT_DX ? it.e : 0);
           }
         }
       }
-      if (!ok && C2) {
-        // a pair's loads signal rank 0's barriers: give those in flight time to land
-        const unsigned long long t0 = globaltimer();
-        while (globaltimer() - t0 < 200000ull) {
-        }
-      } else if (!ok) {
-        const uint32_t n = count < (uint32_t)Sh::stages ? count : (uint32_t)Sh::stages;
+      if (!ok) {   // the loads in flight land before the CTA ends
+        const uint32_t n = count < (uint32_t)STAGES ? count : (uint32_t)STAGES;
         for (uint32_t q = 0; q < n; ++q) {
           const uint32_t c = count - 1 - q;
           volatile int never = 0;
-          mbar_wait_bounded(smem_u32(&ctl->full[c % Sh::stages]), (c / Sh::stages) & 1u, &never,
-                            nullptr);
+          mbar_wait_bounded(smem_u32(&ctl->full[c % STAGES]), (c / STAGES) & 1u, &never, nullptr);
         }
       }
     }
-  } else if (warp == 1 && leader) {
+  } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer
     // The whole warp walks the blocks, so that descriptors and addresses are warp-uniform
     // values (the MMA takes them from uniform registers); one elected thread issues.
-    constexpr uint32_t idesc = idesc_f8(Sh::tile_m, BN, a_mn, b_mn);
+    constexpr uint32_t idesc_full = idesc_f8(BM, BN, a_mn, b_mn),
+                       idesc_half = idesc_f8(BM, BN / 2, a_mn, b_mn);
     // K-major: 32 codes further along each 128-byte row; MN-major: 32 rows of 128 bytes
     // further, blocks of 128 along MN one box apart
     constexpr uint32_t a_step = (a_mn ? 4096 : 32) >> 4, b_step = (b_mn ? 4096 : 32) >> 4;
@@ -458,8 +430,10 @@ product_fp8_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constan
     bool ok = true;
     Item it;
     for (int item = first_item; item < total && ok; item += item_step) {
-      decode<MODE, C2>(g, ctl, item, it);
+      decode<MODE>(g, ctl, item, it);
       const int blocks = __shfl_sync(kFull, it.kb1 - it.kb0, 0);
+      const uint32_t idesc =
+          __shfl_sync(kFull, it.nt * BN + 128 < g.cols ? idesc_full : idesc_half, 0);
       for (int kb = 0; kb < blocks; ++kb) {
         const uint32_t buf = count & 1u;
         ok = mbar_wait_bounded(bars + kFullBar + 8 * s, ph, abort_flag, g.err) &&
@@ -468,31 +442,25 @@ product_fp8_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constan
         ok = __all_sync(kFull, ok);
         if (!ok) break;
         tc_fence_after();
-        const uint64_t ad = a_base + s * (Sh::stage_bytes >> 4);
-        const uint64_t bd = b_base + s * (Sh::stage_bytes >> 4);
+        const uint64_t ad = a_base + s * (STAGE_BYTES >> 4);
+        const uint64_t bd = b_base + s * (STAGE_BYTES >> 4);
         const uint32_t d = tmem + buf * BN;
         if (issues) {
 #pragma unroll
           for (uint32_t ks = 0; ks < BK / 32; ++ks)
-            tc_mma_f8<C2>(d, ad + ks * a_step, bd + ks * b_step, idesc, ks > 0 ? 1u : 0u);
-          if (C2) {
-            tc_commit_pair(bars + kTfull + 8 * buf, 3);
-            tc_commit_pair(bars + kEmptyBar + 8 * s, 3);
-          } else {
-            tc_commit(bars + kTfull + 8 * buf);
-            tc_commit(bars + kEmptyBar + 8 * s);
-          }
+            tc_mma_f8(d, ad + ks * a_step, bd + ks * b_step, idesc, ks > 0 ? 1u : 0u);
+          tc_commit(bars + kTfull + 8 * buf);
+          tc_commit(bars + kEmptyBar + 8 * s);
         }
         ++count;
-        if (++s == Sh::stages) {
+        if (++s == STAGES) {
           s = 0;
           ph ^= 1u;
         }
       }
     }
     if (issues && count > 0) {   // no MMA is in flight when TMEM is released
-      if (C2) tc_commit_pair(smem_u32(&ctl->mma_done), 1);
-      else tc_commit(smem_u32(&ctl->mma_done));
+      tc_commit(smem_u32(&ctl->mma_done));
       volatile int never = 0;
       mbar_wait_bounded(smem_u32(&ctl->mma_done), 0, &never, nullptr);
     }
@@ -507,9 +475,9 @@ product_fp8_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constan
     bool ok = true;
     Item it;
     for (int item = first_item; item < total && ok; item += item_step) {
-      decode<MODE, C2>(g, ctl, item, it);
+      decode<MODE>(g, ctl, item, it);
       const int row_end = MODE == PRODUCT_DW ? g.rows : it.row_end;
-      const int row = (MODE == PRODUCT_DW ? it.mt * Sh::tile_m : it.row0) + row_off + tid;
+      const int row = (MODE == PRODUCT_DW ? it.mt * BM : it.row0) + tid;
       const float *pa[2], *pb[2];
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
@@ -594,7 +562,7 @@ product_fp8_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constan
     };
     auto place = [&](const Item& it) {
       Place p;
-      const int row_w = (MODE == PRODUCT_DW ? it.mt * Sh::tile_m : it.row0) + row_off + q * 32;
+      const int row_w = (MODE == PRODUCT_DW ? it.mt * BM : it.row0) + q * 32;
       p.row = row_w + lane;
       p.row_end = MODE == PRODUCT_DW ? g.rows : it.row_end;
       p.c0 = it.nt * BN + part * CW;
@@ -605,7 +573,7 @@ product_fp8_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constan
     bool ok = true;
     Item it;
     for (int item = first_item; item < total && ok; item += item_step) {
-      decode<MODE, C2>(g, ctl, item, it);
+      decode<MODE>(g, ctl, item, it);
       const Place p = place(it);
       float acc[CW];
 #pragma unroll
@@ -615,11 +583,7 @@ product_fp8_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constan
       // The accumulator may be written again: the loads and their wait are the whole warp's.
       auto release = [&]() {
         tc_fence_before();
-        if (lane == 0) {
-          const uint32_t te = bars + kTempty + 8 * (count & 1u);
-          if (C2 && !leader) mbar_arrive_remote(mapa_shared(te, 0));
-          else mbar_arrive(te);
-        }
+        if (lane == 0) mbar_arrive(bars + kTempty + 8 * (count & 1u));
       };
       auto add = [&](float* to, const float (&v)[32], int c, float f, const float* w) {
 #pragma unroll
@@ -724,11 +688,9 @@ product_fp8_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constan
 
   tc_fence_before();
   __syncthreads();
-  if (C2) cluster_sync_all();   // the pair's MMAs, loads and remote arrivals are over
   if (warp == 1) {
     tc_fence_after();
-    if (C2) tmem_dealloc_pair(tmem, TMEM_COLS);
-    else tmem_dealloc(tmem, TMEM_COLS);
+    tmem_dealloc(tmem, TMEM_COLS);
   }
 }
 
@@ -779,63 +741,37 @@ int device_sms(int dev) {
   return n[dev] > 0 ? n[dev] : kSms;
 }
 
-template <int MODE, bool C2, typename T>
+template <int MODE, typename T>
 cudaError_t launch(const CUtensorMap& ma, const CUtensorMap& mb, const CUtensorMap& mo,
                    const Args& g, long long items, cudaStream_t s) {
-  auto kernel = product_fp8_kernel<MODE, C2, T>;
+  auto kernel = product_fp8_kernel<MODE, T>;
   static bool attr_done[64] = {false};
-  static int pair_slots[64] = {0};   // clusters of two that fit on the GPU at once
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
-  cudaLaunchConfig_t cfg = {};
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = 2;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  cfg.blockDim = dim3(THREADS);
-  cfg.dynamicSmemBytes = (kSmem<MODE, C2>);
-  cfg.stream = s;
-  if (C2) {
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-  }
-  const int sms = device_sms(dev);
   if (!attr_done[dev]) {
-    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             (kSmem<MODE, C2>));
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem<MODE>);
     if (e != cudaSuccess) return e;
     cudaFuncAttributes fa;             // more_registers waits for what the launch brings
     e = cudaFuncGetAttributes(&fa, kernel);
     if (e != cudaSuccess) return e;
     if (fa.numRegs != REGS) return cudaErrorInvalidConfiguration;
-    if (C2) {
-      cfg.gridDim = dim3(2 * (sms / 2));
-      int n = 0;
-      e = cudaOccupancyMaxActiveClusters(&n, kernel, &cfg);
-      if (e != cudaSuccess) return e;
-      if (n <= 0) return cudaErrorInvalidConfiguration;
-      pair_slots[dev] = n;
-    }
     attr_done[dev] = true;
   }
-  const long long ctas = C2 ? 2 * std::min<long long>(pair_slots[dev], items)
-                            : std::min<long long>(sms, items);
-  cfg.gridDim = dim3((unsigned)ctas);
-  e = cudaLaunchKernelEx(&cfg, kernel, ma, mb, mo, g);
+  const int grid = (int)std::min<long long>(device_sms(dev), items);
+  kernel<<<grid, THREADS, kSmem<MODE>, s>>>(ma, mb, mo, g);
   count_launches(1);
-  return e;
+  return cudaGetLastError();
 }
 
-template <int MODE, bool C2>
+template <int MODE>
 cudaError_t launch_typed(const CUtensorMap& ma, const CUtensorMap& mb, const CUtensorMap& mo,
                          const Args& g, long long items, cudaStream_t s) {
   switch (g.out_dtype) {
-    case MOE_BF16: return launch<MODE, C2, __nv_bfloat16>(ma, mb, mo, g, items, s);
-    case MOE_F16: return launch<MODE, C2, __half>(ma, mb, mo, g, items, s);
-    default: return launch<MODE, C2, float>(ma, mb, mo, g, items, s);
+    case MOE_BF16: return launch<MODE, __nv_bfloat16>(ma, mb, mo, g, items, s);
+    case MOE_F16: return launch<MODE, __half>(ma, mb, mo, g, items, s);
+    default: return launch<MODE, float>(ma, mb, mo, g, items, s);
   }
 }
 
@@ -851,37 +787,24 @@ cudaError_t join(const Args& g, bool dw, long long rows, cudaStream_t s) {
   return e;
 }
 
-// How a call is cut: pairs of CTAs or single ones, and over how many CTAs a tile's
-// contraction is split.  Known from the sizes alone.
+// Over how many CTAs a tile's contraction is split, and the items' number at most.  Known
+// from the sizes alone.
 struct Cut {
-  bool pairs;
   int splits;
-  long long items;   // an upper bound
+  long long items;
 };
 
 Cut cut_of(int mode, int N, int n, int K, int E) {
-  const int cols = mode == PRODUCT ? n : K;
-  const int nt = ceil_div(cols, BN);
-  Cut c{false, 1, 0};
-  auto tiles = [&](int m) -> long long {   // row tiles of m rows times column tiles, at most
-    if (mode == PRODUCT_DW) return (long long)E * ceil_div(n, m) * nt;
-    return std::min<long long>(N, ((long long)N + (long long)std::min(E, N) * (m - 1)) / m) * nt;
-  };
+  const int nt = ceil_div(mode == PRODUCT ? n : K, BN);
+  long long tiles = (long long)E * ceil_div(n, BM) * nt;
+  if (mode != PRODUCT_DW)
+    tiles = std::min<long long>(N, ((long long)N + (long long)std::min(E, N) * (BM - 1)) / BM) * nt;
   const int kblocks = ceil_div(mode == PRODUCT_DW ? N : (mode == PRODUCT ? K : n), BK);
-  if (2 * tiles(BM) <= kSms) {
-    if (kblocks >= 2) c.splits = (int)std::min<long long>(kSms / tiles(BM), kblocks);
-  } else {
-    c.pairs = mode == PRODUCT_DW ? n > BM : N / 2 >= (long long)BM * E;
-  }
-  c.items = tiles(c.pairs ? 2 * BM : BM) * c.splits;
+  Cut c{1, tiles};
+  if (tiles > 0 && 2 * tiles <= kSms && kblocks >= 2)
+    c.splits = (int)std::min<long long>(kSms / tiles, kblocks);
+  c.items *= c.splits;
   return c;
-}
-
-template <int MODE>
-cudaError_t launch_cut(const Cut& c, const CUtensorMap& ma, const CUtensorMap& mb,
-                       const CUtensorMap& mo, const Args& g, cudaStream_t s) {
-  return c.pairs ? launch_typed<MODE, true>(ma, mb, mo, g, c.items, s)
-                 : launch_typed<MODE, false>(ma, mb, mo, g, c.items, s);
 }
 
 size_t parts_bytes(int mode, int N, int n, int K, int E) {
@@ -909,7 +832,7 @@ cudaError_t launch_product_fp8(const ProductArgs& a, float* parts, int* err, cud
   g.cols = cols;
   g.tiles_n = divisor(ceil_div(cols, BN));
   g.rows = a.n;
-  g.tiles_m = divisor(ceil_div(a.n, cut.pairs ? 2 * BM : BM));
+  g.tiles_m = divisor(ceil_div(a.n, BM));
   g.splits = divisor(cut.splits);
   g.offsets = a.offsets;
   g.sa = a.sa;
@@ -946,9 +869,9 @@ cudaError_t launch_product_fp8(const ProductArgs& a, float* parts, int* err, cud
     return cudaErrorInvalidValue;
   cudaError_t e;
   switch (a.mode) {
-    case PRODUCT: e = launch_cut<PRODUCT>(cut, ma, mb, mo, g, s); break;
-    case PRODUCT_DX: e = launch_cut<PRODUCT_DX>(cut, ma, mb, mo, g, s); break;
-    default: e = launch_cut<PRODUCT_DW>(cut, ma, mb, mo, g, s); break;
+    case PRODUCT: e = launch_typed<PRODUCT>(ma, mb, mo, g, cut.items, s); break;
+    case PRODUCT_DX: e = launch_typed<PRODUCT_DX>(ma, mb, mo, g, cut.items, s); break;
+    default: e = launch_typed<PRODUCT_DW>(ma, mb, mo, g, cut.items, s); break;
   }
   if (e != cudaSuccess || cut.splits == 1) return e;
   const long long all = dw ? (long long)a.E * a.n : (long long)a.N;

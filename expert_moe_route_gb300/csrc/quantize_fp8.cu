@@ -1,16 +1,17 @@
 // E4M3 codes and fp32 scales of a matrix, one scale per block of 128:
 //   scale = largest |x| of the block / 448,   code = E4M3(x / scale)   (nearest even)
 // A block is 128 elements of a row, 128 of a column, or a tile of 128 x 128.  Bound by HBM.
-// A block of 256 threads takes one 128 x 128 tile: a thread holds eight neighbouring
-// columns of eight rows, so the matrix is read once whichever forms are wanted, rows' maxima
-// are shuffles among 16 lanes and columns' go through 4 KB of shared memory.
+// A block of 256 threads takes one 128 x 128 tile: a thread holds 16 neighbouring columns of
+// four rows, so the matrix is read once whichever forms are wanted, rows' maxima are shuffles
+// among eight lanes (16-bit types: two rows a shuffle, two elements a maximum) and columns' go
+// through 4 KB of shared memory.
 //
 // The quotient is computed as q = x r, q + (x - q s) r with r = 1/s rounded to nearest
 // (Markstein's correction of a quotient, 1990: the remainder is exact under fma): the
 // rounded quotient, three operations where the compiler's division takes about ten, which
 // would be more than the memory allows.  Scales whose remainders could leave the normal
 // range are divided.
-#include <algorithm>
+#include <type_traits>
 
 #include "kernels.h"
 #include "product_fp8.cuh"
@@ -40,160 +41,212 @@ __device__ __forceinline__ uint32_t codes4(float a, float b, float c, float d) {
   return lo | (hi << 16);
 }
 
-// Eight codes of v with one scale.
-__device__ __forceinline__ uint2 codes8(const float* v, float s, float r) {
-  float q[8];
-  if (plain_range(s)) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) q[i] = quotient(v[i], s, r);
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) q[i] = v[i] / s;
-  }
-  return make_uint2(codes4(q[0], q[1], q[2], q[3]), codes4(q[4], q[5], q[6], q[7]));
+// x / s, 0 under a scale of zero (rare: kept out of the way of the kernel's registers).
+__device__ __noinline__ float divided(float x, float s) { return s == 0.f ? x * 0.f : x / s; }
+
+// Four codes of v with a scale each.
+__device__ __forceinline__ uint32_t codes4_of(const float* v, const float4& s, const float4& r,
+                                              bool plain) {
+  if (plain)
+    return codes4(quotient(v[0], s.x, r.x), quotient(v[1], s.y, r.y), quotient(v[2], s.z, r.z),
+                  quotient(v[3], s.w, r.w));
+  return codes4(divided(v[0], s.x), divided(v[1], s.y), divided(v[2], s.z), divided(v[3], s.w));
 }
 
-// Eight codes of v with a scale each.
-__device__ __forceinline__ uint2 codes8(const float* v, const float* s, const float* r,
-                                        bool plain) {
-  float q[8];
-  if (plain) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) q[i] = quotient(v[i], s[i], r[i]);
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      if (plain_range(s[i])) q[i] = quotient(v[i], s[i], r[i]);
-      else q[i] = v[i] / s[i];
+// 16 codes of v with one scale.
+__device__ __forceinline__ uint4 codes16(const float* v, float s, float r) {
+  const float4 s4 = make_float4(s, s, s, s), r4 = make_float4(r, r, r, r);
+  const bool plain = plain_range(s);
+  return make_uint4(codes4_of(v, s4, r4, plain), codes4_of(v + 4, s4, r4, plain),
+                    codes4_of(v + 8, s4, r4, plain), codes4_of(v + 12, s4, r4, plain));
+}
+
+// 16 elements as 32-bit words, and maxima of magnitudes on words: two elements of a 16-bit
+// type or one float.  NaN never wins.
+template <typename T> struct Words {
+  static constexpr int n = 16 * sizeof(T) / 4;
+  static constexpr int per = 4 / sizeof(T);      // elements a word
+  static __device__ __forceinline__ uint32_t magnitude(uint32_t w) {
+    return w & (per == 2 ? 0x7fff7fffu : 0x7fffffffu);
+  }
+  static __device__ __forceinline__ uint32_t larger(uint32_t a, uint32_t b) {
+    if constexpr (per == 1) {
+      return __float_as_uint(fmaxf(__uint_as_float(a), __uint_as_float(b)));
+    } else {
+      using P = typename std::conditional<std::is_same<T, __half>::value, __half2,
+                                          __nv_bfloat162>::type;
+      const P m = __hmax2(*reinterpret_cast<const P*>(&a), *reinterpret_cast<const P*>(&b));
+      return *reinterpret_cast<const uint32_t*>(&m);
     }
   }
-  return make_uint2(codes4(q[0], q[1], q[2], q[3]), codes4(q[4], q[5], q[6], q[7]));
-}
+  // element i (0 or 1) of a word
+  static __device__ __forceinline__ float value(uint32_t w, int i) {
+    if constexpr (per == 1) {
+      return __uint_as_float(w);
+    } else {
+      const uint16_t h = (uint16_t)(w >> (16 * i));
+      return to_f32(*reinterpret_cast<const T*>(&h));
+    }
+  }
+  static __device__ __forceinline__ void unpack(const uint32_t* w, float* f) {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) f[i] = value(w[i / per], i % per);
+  }
+};
 
-// VEC: eight elements of x are one or two aligned accesses.
+// VEC: 16 elements of x are aligned vectors of 16 bytes.
 template <typename T, int FORM, bool VEC>
-__global__ void __launch_bounds__(QT)
+__global__ void __launch_bounds__(QT, sizeof(T) == 2 && FORM != (ROWS | COLS) ? 4 : 2)
 quantize_fp8_kernel(const T* __restrict__ x, long long ldx, long long n, int K, long long plane,
                     int row_tiles, int col_tiles, uint8_t* __restrict__ row_codes,
                     float* __restrict__ row_scales, uint8_t* __restrict__ col_codes,
                     float* __restrict__ col_scales) {
-  using V = Vec<T, 8>;
+  using W = Words<T>;
   __shared__ float part[QT / 32][BLK];
-  __shared__ float scales[BLK];
+  __shared__ float4 scales[BLK / 4], inverses[BLK / 4];   // of the columns
   const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
   const long long id = blockIdx.x;
   const int ct = (int)(id % col_tiles);
   const long long rest = id / col_tiles;
   const int rt = (int)(rest % row_tiles);
   const long long e = rest / row_tiles;            // TILES: the matrix of the stack
-  const long long r0 = (long long)rt * BLK;
-  const int c = ct * BLK + (t & 15) * 8;
+  const int c = ct * BLK + (t & 7) * 16;
   const bool in_cols = c < K;
-  const T* xe = x + e * plane;
+  const long long r0 = (long long)rt * BLK + (t >> 3);   // rows r0, r0 + 32, ...
+  const T* xe = x + e * plane + r0 * ldx + c;
 
-  typename V::Raw raw[8];
+  uint32_t raw[4][W::n];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const long long r = r0 + (t >> 4) + 16 * i;
-    raw[i] = V::zero();
-    if (in_cols && r < n) {
-      const T* p = xe + r * ldx + c;
+  for (int i = 0; i < 4; ++i) {
+#pragma unroll
+    for (int j = 0; j < W::n; ++j) raw[i][j] = 0;
+    if (in_cols && r0 + 32 * i < n) {
+      const T* p = xe + 32 * i * ldx;
       if (VEC) {
-        raw[i] = V::load(p);
-      } else {
-        T one[8];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) one[j] = p[j];
-        memcpy(&raw[i], one, sizeof(one));
+        for (int j = 0; j < W::n; j += 4) {
+          const uint4 v = ldg_nc_v4(p + j * W::per);
+          raw[i][j] = v.x; raw[i][j + 1] = v.y; raw[i][j + 2] = v.z; raw[i][j + 3] = v.w;
+        }
+      } else {
+        T one[16];
+#pragma unroll
+        for (int j = 0; j < 16; ++j) one[j] = p[j];
+        memcpy(raw[i], one, sizeof(one));
       }
     }
   }
 
-  float top[8];                                    // per column (COLS), or top[0] (TILES)
+  if (FORM & (ROWS | TILES)) {
+    float m[4];                                    // each row's largest magnitude
+    {
+      uint32_t top[4];
 #pragma unroll
-  for (int j = 0; j < 8; ++j) top[j] = 0.f;
+      for (int i = 0; i < 4; ++i) {
+        top[i] = 0;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    float v[8];
-    V::unpack(raw[i], v);
-    if (FORM & COLS) {
+        for (int j = 0; j < W::n; ++j) top[i] = W::larger(top[i], W::magnitude(raw[i][j]));
+      }
+      if (W::per == 2) {                           // rows in pairs, one a half of a word
 #pragma unroll
-      for (int j = 0; j < 8; ++j) top[j] = fmaxf(top[j], fabsf(v[j]));
-    }
-    if (FORM & (ROWS | TILES)) {
-      float m = 0.f;
+        for (int i = 0; i < 4; i += 2) {
+          uint32_t both = W::larger(__byte_perm(top[i], top[i + 1], 0x5410),
+                                    __byte_perm(top[i], top[i + 1], 0x7632));
 #pragma unroll
-      for (int j = 0; j < 8; ++j) m = fmaxf(m, fabsf(v[j]));
-      if (FORM & TILES) {
-        top[0] = fmaxf(top[0], m);
+          for (int off = 4; off > 0; off >>= 1)
+            both = W::larger(both, __shfl_xor_sync(kFull, both, off));
+          m[i] = W::value(both, 0);
+          m[i + 1] = W::value(both, 1);
+        }
       } else {
 #pragma unroll
-        for (int off = 8; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, off));
-        const long long r = r0 + (t >> 4) + 16 * i;
-        const float s = m / kMax;
-        const uint2 q = codes8(v, s, inverse(s));
-        if (in_cols && r < n) {
-          *reinterpret_cast<uint2*>(row_codes + r * K + c) = q;
-          if ((t & 15) == 0) row_scales[r * col_tiles + ct] = s;
+        for (int i = 0; i < 4; ++i) {
+#pragma unroll
+          for (int off = 4; off > 0; off >>= 1)
+            top[i] = W::larger(top[i], __shfl_xor_sync(kFull, top[i], off));
+          m[i] = W::value(top[i], 0);
         }
       }
     }
-  }
-
-  if (FORM & TILES) {
-    float m = top[0];
+    if (FORM & TILES) {
+      float all = fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
 #pragma unroll
-    for (int off = 16; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, off));
-    if (lane == 0) part[warp][0] = m;
-    __syncthreads();
+      for (int off = 16; off >= 8; off >>= 1) all = fmaxf(all, __shfl_xor_sync(kFull, all, off));
+      if (lane == 0) part[warp][0] = all;
+      __syncthreads();
 #pragma unroll
-    for (int w = 0; w < QT / 32; ++w) m = fmaxf(m, part[w][0]);
-    const float s = m / kMax, inv = inverse(s);
-    if (t == 0) row_scales[id] = s;
+      for (int w = 0; w < QT / 32; ++w) all = fmaxf(all, part[w][0]);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const long long r = r0 + (t >> 4) + 16 * i;
-      float v[8];
-      V::unpack(raw[i], v);
-      const uint2 q = codes8(v, s, inv);
-      if (in_cols && r < n) *reinterpret_cast<uint2*>(row_codes + e * plane + r * K + c) = q;
+      for (int i = 0; i < 4; ++i) m[i] = all;
+    }
+    float s = m[0] / kMax, inv = inverse(s);
+    if ((FORM & TILES) && t == 0) row_scales[id] = s;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const long long r = r0 + 32 * i;
+      if (i > 0 && !(FORM & TILES)) {
+        s = m[i] / kMax;
+        inv = inverse(s);
+      }
+      float v[16];
+      W::unpack(raw[i], v);
+      const uint4 q = codes16(v, s, inv);
+      if (in_cols && r < n) {
+        *reinterpret_cast<uint4*>(row_codes + e * plane + r * K + c) = q;
+        if (!(FORM & TILES) && (t & 7) == 0) row_scales[r * col_tiles + ct] = s;
+      }
     }
   }
 
   if (FORM & COLS) {
+    uint32_t top[W::n];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) top[j] = fmaxf(top[j], __shfl_xor_sync(kFull, top[j], 16));
-    if (lane < 16) {
+    for (int j = 0; j < W::n; ++j) {
+      top[j] = 0;
 #pragma unroll
-      for (int j = 0; j < 8; j += 4)
-        *reinterpret_cast<float4*>(&part[warp][lane * 8 + j]) =
-            make_float4(top[j], top[j + 1], top[j + 2], top[j + 3]);
+      for (int i = 0; i < 4; ++i) top[j] = W::larger(top[j], W::magnitude(raw[i][j]));
+      top[j] = W::larger(top[j], __shfl_xor_sync(kFull, top[j], 8));
+      top[j] = W::larger(top[j], __shfl_xor_sync(kFull, top[j], 16));
+    }
+    if (lane < 8) {
+      float f[16];
+      W::unpack(top, f);
+#pragma unroll
+      for (int j = 0; j < 16; j += 4)
+        *reinterpret_cast<float4*>(&part[warp][lane * 16 + j]) =
+            make_float4(f[j], f[j + 1], f[j + 2], f[j + 3]);
     }
     __syncthreads();
+    bool plain = true;
     if (t < BLK) {
       float m = 0.f;
 #pragma unroll
       for (int w = 0; w < QT / 32; ++w) m = fmaxf(m, part[w][t]);
       const float s = m / kMax;
-      scales[t] = s;
+      reinterpret_cast<float*>(scales)[t] = s;
+      reinterpret_cast<float*>(inverses)[t] = inverse(s);
+      plain = plain_range(s);
       if (ct * BLK + t < K) col_scales[(size_t)rt * K + ct * BLK + t] = s;
     }
-    __syncthreads();
-    float s[8], inv[8];
-    bool plain = true;
+    plain = __syncthreads_and(plain);
+    uint32_t out[4][4];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      s[j] = scales[(t & 15) * 8 + j];
-      inv[j] = inverse(s[j]);
-      plain = plain && plain_range(s[j]);
+    for (int j = 0; j < 4; ++j) {                  // four columns of the four rows
+      const float4 s = scales[(t & 7) * 4 + j], inv = inverses[(t & 7) * 4 + j];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        float v[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) v[k] = W::value(raw[i][(4 * j + k) / W::per], (4 * j + k) % W::per);
+        out[i][j] = codes4_of(v, s, inv, plain);
+      }
     }
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const long long r = r0 + (t >> 4) + 16 * i;
-      float v[8];
-      V::unpack(raw[i], v);
-      const uint2 q = codes8(v, s, inv, plain);
-      if (in_cols && r < n) *reinterpret_cast<uint2*>(col_codes + r * K + c) = q;
+    for (int i = 0; i < 4; ++i) {
+      const long long r = r0 + 32 * i;
+      if (in_cols && r < n)
+        *reinterpret_cast<uint4*>(col_codes + r * K + c) =
+            make_uint4(out[i][0], out[i][1], out[i][2], out[i][3]);
     }
   }
 }
@@ -214,9 +267,8 @@ cudaError_t launch_form(const Call& a, cudaStream_t s) {
   const long long blocks = (long long)a.E * rt * ct;
   if (blocks == 0) return cudaSuccess;
   if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
-  const int align = sizeof(T) == 4 ? 32 : 16;      // of eight elements
-  const bool vec = reinterpret_cast<uintptr_t>(a.x) % align == 0 &&
-                   a.ldx * (long long)sizeof(T) % align == 0;
+  const bool vec = reinterpret_cast<uintptr_t>(a.x) % 16 == 0 &&
+                   a.ldx * (long long)sizeof(T) % 16 == 0;
   const T* x = static_cast<const T*>(a.x);
   if (vec)
     quantize_fp8_kernel<T, FORM, true><<<(unsigned)blocks, QT, 0, s>>>(

@@ -8,14 +8,18 @@
 // and w = 0.
 //
 // The choice is that of c in 64 bits: two scores can lie closer to each other than 32 bits
-// tell, about one token in two thousand at 256 experts.  The scores are computed in 32
-// bits; a token two of whose values that decide lie within the error bound of each other
-// (kNear below) is done again in 64 bits by choose_exact.  Equal logits under equal biases
-// are equal in any precision and need no second look.
+// tell, about one token in five hundred at 384 experts.  The scores are computed in 32 bits;
+// where two that follow each other lie within the error bound (kNear below), experts are taken
+// on until a gap, and those taken are put in order by their keys in 64 bits, a lane each.
+// Equal logits under equal biases are equal in any precision and need no second look.
 //
-// A warp takes a token, a lane ceil(E/32) neighbouring experts, so the lower lane holds the
-// lower experts and a ballot's first lane is the tie's winner.  Keys are compared as
-// integers in the order of the floats (redux.sync).
+// A warp takes a token, a lane up to EPL of its experts.  A key becomes one 32-bit integer:
+// its distance below the token's largest key in 2^23 (E > 512: 2^22) steps of the keys' range,
+// then the expert, so that the warp's smallest integer (redux.sync) is the next expert and ties
+// go to the lower one by themselves.  A lane keeps its three smallest in order and finds the
+// next three when they are taken (8% of the tokens of 8 in 384).  A token whose keys are not
+// finite, whose groups lie within the error bound or with more than 32 experts in a row that
+// do, goes to choose_exact, all of it in 64 bits (15 us at 256 experts; a lane's one key 3 us).
 #include <math.h>
 
 #include <algorithm>
@@ -44,7 +48,6 @@ __device__ __forceinline__ unsigned long long ordered(double v) {
   const unsigned long long o = b ^ ((unsigned long long)((long long)b >> 63) | (1ull << 63));
   return v != v ? ~0ull : (v == -INFINITY ? 0ull : o);
 }
-__device__ __forceinline__ uint32_t warp_max(uint32_t v) { return __reduce_max_sync(kFull, v); }
 __device__ __forceinline__ unsigned long long warp_max(unsigned long long v) {
 #pragma unroll
   for (int off = 16; off > 0; off >>= 1) {
@@ -70,28 +73,34 @@ __device__ __forceinline__ double warp_sum(double v) {
 //   kNear * (largest score) + kRound * (larger key)
 // are in the right order.
 constexpr float kNearSigmoid = 1.0e-6f, kNearSoftmax = 2.5e-6f, kRound = 2.5e-7f;
+constexpr uint32_t kNone = 0xffffffffu;   // no expert
 
 struct RouteParams {
   long long ld;
   int T, E, R;
-  int per;              // experts a lane
   int sigmoid, groups, top_groups, group_keys, renormalise;
   float scale;
   const float* bias;
 };
 
+// A lane's expert j.  VEC: vectors of four neighbours, 128 experts a warp's load; else 32.
+template <bool VEC> __device__ __forceinline__ int expert_of(int j) {
+  const int lane = threadIdx.x & 31;
+  return VEC ? (j / 4) * 128 + lane * 4 + j % 4 : j * 32 + lane;
+}
+
 // The whole choice in 64 bits, lane r < R receives its expert (or -1).
-template <typename T, int EPL>
+template <typename T>
 __device__ __noinline__ int choose_exact(const T* row, const RouteParams& p) {
   const int lane = threadIdx.x & 31;
-  const int e0 = lane * p.per;
-  double key[EPL], by[EPL];     // what groups are worth by, what experts are ordered by
+  const int n = (p.E + 31) / 32;          // this lane's experts are lane, lane + 32, ...
+  double key[32], by[32];       // what groups are worth by, what experts are ordered by
   double top = -INFINITY;
   bool nan = false;
-#pragma unroll
-  for (int j = 0; j < EPL; ++j) {
-    const bool here = j < p.per && e0 + j < p.E;
-    by[j] = here ? (double)to_f32(row[e0 + j]) : -INFINITY;
+#pragma unroll 1
+  for (int j = 0; j < n; ++j) {
+    const int e = j * 32 + lane;
+    by[j] = e < p.E ? (double)to_f32(row[e]) : -INFINITY;
     nan |= by[j] != by[j];
     top = fmax(top, by[j]);
   }
@@ -100,19 +109,20 @@ __device__ __noinline__ int choose_exact(const T* row, const RouteParams& p) {
   if (__any_sync(kFull, nan)) top = NAN;
   double sum = 0.0;
   if (!p.sigmoid) {
-#pragma unroll
-    for (int j = 0; j < EPL; ++j) {
+#pragma unroll 1
+    for (int j = 0; j < n; ++j) {
       key[j] = by[j] == -INFINITY ? 0.0 : exp(by[j] - top);
       sum += key[j];
     }
     sum = warp_sum(sum);
   }
-#pragma unroll
-  for (int j = 0; j < EPL; ++j) {
+#pragma unroll 1
+  for (int j = 0; j < n; ++j) {
+    const int e = j * 32 + lane;
     double k = by[j];
     if (p.bias || p.group_keys == 2) {
       k = p.sigmoid ? 1.0 / (1.0 + exp(-by[j])) : key[j] / sum;
-      if (p.bias && j < p.per && e0 + j < p.E) k += (double)p.bias[e0 + j];
+      if (p.bias && e < p.E) k += (double)p.bias[e];
       if (by[j] == -INFINITY) k = -INFINITY;
     }
     key[j] = k;
@@ -121,13 +131,14 @@ __device__ __noinline__ int choose_exact(const T* row, const RouteParams& p) {
   if (p.groups > 1) {
     const int per_group = p.E / p.groups;
     unsigned long long mine = 0;          // worth of group `lane`
+#pragma unroll 1
     for (int g = 0; g < p.groups; ++g) {
       double a = -INFINITY, b = -INFINITY;
       bool bad = false;
-#pragma unroll
-      for (int j = 0; j < EPL; ++j) {
-        const int e = e0 + j;
-        if (j < p.per && e < p.E && e / per_group == g) {
+#pragma unroll 1
+      for (int j = 0; j < n; ++j) {
+        const int e = j * 32 + lane;
+        if (e < p.E && e / per_group == g) {
           bad |= key[j] != key[j];
           b = fmax(b, fmin(a, key[j]));
           a = fmax(a, key[j]);
@@ -149,71 +160,115 @@ __device__ __noinline__ int choose_exact(const T* row, const RouteParams& p) {
       before += o > mine || (o == mine && g < lane);
     }
     const uint32_t kept = __ballot_sync(kFull, lane < p.groups && before < p.top_groups);
-#pragma unroll
-    for (int j = 0; j < EPL; ++j) {
-      const int e = e0 + j;
-      if (j < p.per && e < p.E && !((kept >> (e / per_group)) & 1u)) by[j] = -INFINITY;
+#pragma unroll 1
+    for (int j = 0; j < n; ++j) {
+      const int e = j * 32 + lane;
+      if (e < p.E && !((kept >> (e / per_group)) & 1u)) by[j] = -INFINITY;
     }
   }
   uint32_t taken = 0;
   int mine = -1;
+#pragma unroll 1
   for (int r = 0; r < p.R; ++r) {
     unsigned long long best = 0;
-    int at = 0;
-#pragma unroll
-    for (int j = EPL - 1; j >= 0; --j) {
+    int at = 0;                           // this lane's lowest expert with its best key
+#pragma unroll 1
+    for (int j = 0; j < n; ++j) {
       const unsigned long long o = (taken >> j) & 1u ? 0ull : ordered(by[j]);
-      if (o != 0 && o >= best) {
+      if (o > best) {
         best = o;
         at = j;
       }
     }
     const unsigned long long all = warp_max(best);
     if (all == 0) break;
-    const int src = __ffs(__ballot_sync(kFull, best == all)) - 1;
-    if (lane == src) taken |= 1u << at;
-    const int e = __shfl_sync(kFull, e0 + at, src);
+    const int e = __reduce_min_sync(kFull, best == all ? at * 32 + lane : 0x7fffffff);
+    if (best == all && e == at * 32 + lane) taken |= 1u << at;
     if (lane == r) mine = e;
   }
   return mine;
 }
 
-// w of lane r < R's expert with logit x (here: it has one); m, sum: the token's largest
-// logit and sum of exp(l - m), for a softmax over all experts.
-__device__ __forceinline__ float weight_of(const RouteParams& p, float x, bool here, float m,
-                                           float sum) {
-  if (!p.renormalise) {
-    float v;
+// Experts of the lanes (or -1) in the order of their keys in 64 bits: lane r receives the r-th.
+template <typename T>
+__device__ __noinline__ int order_exact(const T* row, const RouteParams& p, int e) {
+  const int lane = threadIdx.x & 31;
+  const double l = e >= 0 ? (double)to_f32(row[e]) : -INFINITY;
+  double key = l;
+  if (p.bias) {
     if (p.sigmoid) {
-      const float z = expf(-fabsf(x));
-      v = (x < 0.f ? z : 1.f) / (1.f + z);
+      key = 1.0 / (1.0 + exp(-l));
     } else {
-      v = expf(x - m) / sum;
-    }
-    return here ? v * p.scale : 0.f;
-  }
-  // shares of the chosen scores, scaled by the largest one's exponential: no sum underflows
-  const float y = p.sigmoid ? fminf(x, 0.f) : x;
-  float top = here ? y : -INFINITY;
+      double top = -INFINITY, sum = 0.0;
+      for (int j = lane; j < p.E; j += 32) top = fmax(top, (double)to_f32(row[j]));
 #pragma unroll
-  for (int off = 16; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, off));
-  float v = here ? expf(y - top) : 0.f;
-  if (p.sigmoid && here) v = v / (1.f + expf(-fabsf(x)));
-  const float total = warp_sum(v);
+      for (int off = 16; off > 0; off >>= 1) top = fmax(top, __shfl_xor_sync(kFull, top, off));
+      for (int j = lane; j < p.E; j += 32) sum += exp((double)to_f32(row[j]) - top);
+      key = exp(l - top) / warp_sum(sum);
+    }
+    key += e >= 0 ? (double)p.bias[e] : 0.0;
+  }
+  int place = 0;
+  for (int j = 0; j < 32; ++j) {
+    const double o = __shfl_sync(kFull, key, j);
+    const int oe = __shfl_sync(kFull, e, j);
+    place += oe >= 0 && (o > key || (o == key && oe < e));
+  }
+  int mine = -1;
+  for (int j = 0; j < 32; ++j) {
+    const int at = __shfl_sync(kFull, place, j), oe = __shfl_sync(kFull, e, j);
+    if (oe >= 0 && at == lane) mine = oe;
+  }
+  return mine;
+}
+
+// Sum over a token's slots (lanes 0 .. R - 1, R <= 2 half), the same in every lane.
+__device__ __forceinline__ float slot_sum(float v, int half) {
+  for (int off = half; off > 0; off >>= 1) v += __shfl_xor_sync(kFull, v, off);
+  return __shfl_sync(kFull, v, 0);
+}
+
+// w of lane r < R's expert with logit x (here: it has one); m, sum: the token's largest
+// logit and sum of exp(l - m), for a softmax over all experts.  half: see slot_sum.
+__device__ __forceinline__ float weight_of(const RouteParams& p, float x, bool here, float m,
+                                           float sum, int half) {
+  float v = 0.f;
+  if (p.sigmoid) {
+    const float z = expf(-fabsf(x));
+    v = here ? (x < 0.f ? z : 1.f) / (1.f + z) : 0.f;
+    if (!p.renormalise) return v * p.scale;
+  } else if (!p.renormalise) {
+    return here ? expf(x - m) / sum * p.scale : 0.f;
+  }
+  float total = p.sigmoid ? slot_sum(v, half) : 0.f;
+  if (!(total >= 1e-20f)) {
+    // shares of the chosen scores (of a softmax, or so small that their sum underflows),
+    // scaled by the largest one's exponential
+    const float y = p.sigmoid ? fminf(x, 0.f) : x;
+    float top = here ? y : -INFINITY;
+    for (int off = half; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, off));
+    v = here ? expf(y - top) : 0.f;
+    if (p.sigmoid && here) v = v / (1.f + expf(-fabsf(x)));
+    total = slot_sum(v, half);
+  }
   return here ? v / total * p.scale : 0.f;
 }
 
-// VEC: a lane's experts are EPL = per elements in aligned vectors of four.
 template <typename T, int EPL, bool VEC>
 __device__ __forceinline__ void load_row(const T* row, const RouteParams& p, float (&x)[EPL]) {
-  const int e0 = (threadIdx.x & 31) * p.per;
   if constexpr (VEC) {
 #pragma unroll
-    for (int j = 0; j < EPL; j += 4) Vec<T, 4>::unpack(Vec<T, 4>::load(row + e0 + j), x + j);
+    for (int j = 0; j < EPL; j += 4) {
+      x[j] = x[j + 1] = x[j + 2] = x[j + 3] = -INFINITY;
+      const int e = expert_of<VEC>(j);
+      if (e < p.E) Vec<T, 4>::unpack(Vec<T, 4>::load(row + e), x + j);
+    }
   } else {
 #pragma unroll
-    for (int j = 0; j < EPL; ++j)
-      x[j] = j < p.per && e0 + j < p.E ? to_f32(row[e0 + j]) : -INFINITY;
+    for (int j = 0; j < EPL; ++j) {
+      const int e = expert_of<VEC>(j);
+      x[j] = e < p.E ? to_f32(row[e]) : -INFINITY;
+    }
   }
 }
 
@@ -236,142 +291,232 @@ __device__ __forceinline__ void softmax_parts(const float (&x)[EPL], float& m, f
   sum = warp_sum(sum);
 }
 
-template <typename T, int EPL, bool VEC>
-__global__ void __launch_bounds__(RT)
+// 1 / (1 + exp(-x)) within 2.5e-7 + 6e-8 of itself, 0 for -inf.
+__device__ __forceinline__ float fast_sigmoid(float x) {
+  float z, r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(z) : "f"(x * -1.4426950408889634f));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + z));
+  return r;
+}
+
+// The three smallest of those of v that are above `floor` (all: floor = 0, for v > 0), in
+// order.
+template <int EPL>
+__device__ __forceinline__ void smallest_three(const uint32_t (&v)[EPL], uint32_t floor,
+                                               uint32_t (&s)[3]) {
+  s[0] = s[1] = s[2] = kNone;
+#pragma unroll
+  for (int j = 0; j < EPL; ++j) {
+    uint32_t x = floor == 0 || v[j] > floor ? v[j] : kNone;
+#pragma unroll
+    for (int i = 0; i < 3; ++i) {
+      if (i > j) break;
+      const uint32_t lo = min(s[i], x);
+      x = max(s[i], x);
+      s[i] = lo;
+    }
+  }
+}
+
+// GROUPS: groups > 1.  Blocks an SM: choose_exact, rare, would else set the registers of all.
+template <typename T, int EPL, bool VEC, bool GROUPS>
+__global__ void __launch_bounds__(RT, EPL <= 8 ? 4 : (EPL <= 16 ? 3 : 2))
 route_scores_kernel(const T* __restrict__ logits, const RouteParams p, int32_t* __restrict__ idx,
                     float* __restrict__ w) {
-  extern __shared__ float group_keys_s[];    // groups > 1: a token's keys, E + 32 a warp
+  extern __shared__ float group_keys_s[];    // GROUPS: a token's keys, E + 32 a warp
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int e0 = lane * p.per;
-  const bool scored = p.bias != nullptr || p.group_keys == 2;   // keys are scores, not logits
+  const bool biased = p.bias != nullptr;
+  const bool scored = biased || p.group_keys == 2;   // keys are scores, not logits
+  const int bits = p.E > 512 ? 10 : 9;
+  const float steps = (p.E > 512 ? 4194304.f : 8388608.f) - 72.f;
+  constexpr float kMagic = 8388608.f + 64.f; // distances start at 64: the first is near none
+  int half = 1;
+  while (2 * half < p.R) half *= 2;
+  float bias[EPL];
+  bool bad_bias = false;
+  float b_hi = -INFINITY, b_lo = INFINITY;
+#pragma unroll
+  for (int j = 0; j < EPL; ++j) {
+    const int e = expert_of<VEC>(j);
+    bias[j] = biased && e < p.E ? p.bias[e] : 0.f;
+    bad_bias |= !(bias[j] < INFINITY) || bias[j] == -INFINITY;
+    if (e < p.E) {
+      b_hi = fmaxf(b_hi, bias[j]);
+      b_lo = fminf(b_lo, bias[j]);
+    }
+  }
+  bad_bias = __any_sync(kFull, bad_bias);
+  b_hi = unordered(__reduce_max_sync(kFull, ordered(b_hi)));
+  b_lo = unordered(__reduce_min_sync(kFull, ordered(b_lo)));
+  // Sigmoid scores and a bias: every key is in [b_lo, 1 + b_hi], the same for all tokens, and
+  // a key's integer is one fma of its score.
+  const bool fixed = !GROUPS && p.sigmoid && biased && !bad_bias;
+  const float f_scale = steps / (1.f + b_hi - b_lo);
+  if (fixed) {
+#pragma unroll
+    for (int j = 0; j < EPL; ++j) bias[j] = fmaf(1.f + b_hi - bias[j], f_scale, kMagic);
+  }
+  int P = 1, per_group = p.E;                // groups: lanes each, and experts
+  uint8_t place[GROUPS ? EPL : 1];           // P times the expert's group
+  if constexpr (GROUPS) {
+    per_group = p.E / p.groups;
+    while (2 * P * p.groups <= 32) P *= 2;
+#pragma unroll
+    for (int j = 0; j < EPL; ++j) place[j] = (uint8_t)(expert_of<VEC>(j) / per_group * P);
+  }
   for (long long t = blockIdx.x * RW + warp; t < p.T; t += gridDim.x * RW) {
     const T* row = logits + t * p.ld;
-    float x[EPL];
-    load_row<T, EPL, VEC>(row, p, x);
+    float k[EPL];                            // keys, first of all the logits
+    load_row<T, EPL, VEC>(row, p, k);
     float m = 0.f, sum = 1.f;
-    if (!p.sigmoid && (scored || !p.renormalise)) softmax_parts<EPL>(x, m, sum);
-    // keys: what experts are ordered by (o), what groups are worth by (k)
-    float k[EPL];
-    uint32_t o[EPL];
-    bool nan = false;
+    if (!p.sigmoid && (scored || !p.renormalise)) softmax_parts<EPL>(k, m, sum);
+    bool odd = bad_bias;                     // NaN or +inf: by the definition's arithmetic
 #pragma unroll
-    for (int j = 0; j < EPL; ++j) {
-      k[j] = x[j];
-      nan |= x[j] != x[j] || x[j] == INFINITY;
-    }
-    if (scored) {
-      const float inv = 1.f / sum;
+    for (int j = 0; j < EPL; ++j) odd |= !(k[j] < INFINITY);
+    bool again = __any_sync(kFull, odd);
+
+    uint32_t v[EPL];                         // keys as integers
+    uint32_t close;                          // distances up to this may be in the wrong order
+    if (fixed) {
 #pragma unroll
       for (int j = 0; j < EPL; ++j) {
-        float v = p.sigmoid ? __fdividef(1.f, 1.f + __expf(-x[j])) : __expf(x[j] - m) * inv;
-        if (p.bias && j < p.per && e0 + j < p.E) v += __ldg(p.bias + e0 + j);
-        k[j] = x[j] == -INFINITY ? -INFINITY : v;
-        nan |= k[j] != k[j];
+        const uint32_t d = __float_as_uint(fmaf(fast_sigmoid(k[j]), -f_scale, bias[j]));
+        v[j] = k[j] == -INFINITY ? kNone : d << bits | (uint32_t)expert_of<VEC>(j);
       }
-    }
-    const float near = !scored ? -1.f : (p.sigmoid ? kNearSigmoid : kNearSoftmax / sum);
-    bool again = __any_sync(kFull, nan);       // NaN and +inf: by the definition's arithmetic
-#pragma unroll
-    for (int j = 0; j < EPL; ++j) o[j] = ordered(p.bias ? k[j] : x[j]);
-
-    if (p.groups > 1 && !again) {
-      const int per_group = p.E / p.groups;
-      int P = 1;                                // lanes a group
-      while (2 * P * p.groups <= 32) P *= 2;
-      float* ks = group_keys_s + warp * (p.E + 32);
-      // a group's keys start P words apart from a multiple of its length: no bank conflicts
-      {
-        int g = e0 / per_group, left = per_group - (e0 - g * per_group);
+      // (two steps more: the offsets are rounded to whole steps)
+      const float most = fmaxf(fabsf(1.f + b_hi), fabsf(b_lo));
+      close = (uint32_t)fminf((kNearSigmoid + kRound * most) * f_scale + 6.f, steps) << bits;
+    } else {
+      float near = 0.f;                      // error bound of a difference of two keys
+      if (scored) {
+        const float inv = 1.f / sum;
+        near = p.sigmoid ? kNearSigmoid : kNearSoftmax * inv;
 #pragma unroll
         for (int j = 0; j < EPL; ++j) {
-          if (j < p.per && e0 + j < p.E) ks[e0 + j + g * P] = k[j];
-          if (--left == 0) {
-            ++g;
-            left = per_group;
+          const float s = p.sigmoid ? fast_sigmoid(k[j]) : __expf(k[j] - m) * inv;
+          k[j] = k[j] == -INFINITY ? k[j] : s + bias[j];
+        }
+      }
+      if constexpr (GROUPS) {
+        float* ks = group_keys_s + warp * (p.E + 32);
+        // a group's keys start P words apart from a multiple of its length: no bank conflicts
+#pragma unroll
+        for (int j = 0; j < EPL; ++j)
+          if (expert_of<VEC>(j) < p.E) ks[expert_of<VEC>(j) + place[j]] = k[j];
+        __syncwarp();
+        const int g = lane / P;
+        float a = -INFINITY, b = -INFINITY;
+        if (g < p.groups)
+          for (int i = lane % P; i < per_group; i += P) {
+            const float key = ks[g * (per_group + P) + i];
+            b = fmaxf(b, fminf(a, key));
+            a = fmaxf(a, key);
           }
+        for (int off = P / 2; off > 0; off >>= 1) {
+          const float oa = __shfl_xor_sync(kFull, a, off), ob = __shfl_xor_sync(kFull, b, off);
+          b = fmaxf(fminf(a, oa), fmaxf(b, ob));
+          a = fmaxf(a, oa);
+        }
+        __syncwarp();
+        const float worth = p.group_keys == 2 ? a + b : a;
+        int before = 0;
+        for (int j = 0; j < p.groups; ++j) {
+          const float other = __shfl_sync(kFull, worth, j * P);
+          before += other > worth || (other == worth && j < g);
+        }
+        const bool first = lane % P == 0 && g < p.groups;
+        // bits P g of the groups that take part
+        const uint32_t kept = __ballot_sync(kFull, first && before < p.top_groups);
+        if (scored && p.top_groups < p.groups && !again) {
+          const int in = __ffs(__ballot_sync(kFull, first && before == p.top_groups - 1)) - 1;
+          const int out = __ffs(__ballot_sync(kFull, first && before == p.top_groups)) - 1;
+          const float hi = __shfl_sync(kFull, worth, in), lo = __shfl_sync(kFull, worth, out);
+          again = lo > -INFINITY &&
+                  hi - lo <= 2.f * near + 2.f * kRound * fmaxf(fabsf(hi), fabsf(lo));
+        }
+#pragma unroll
+        for (int j = 0; j < EPL; ++j) {
+          const int e = expert_of<VEC>(j);
+          if (!biased && scored && e < p.E) k[j] = to_f32(row[e]);   // experts go by logit
+          if (!((kept >> place[j]) & 1u)) k[j] = -INFINITY;
         }
       }
-      __syncwarp();
-      const int g = lane / P;
-      float a = -INFINITY, b = -INFINITY;
-      if (g < p.groups)
-        for (int i = lane % P; i < per_group; i += P) {
-          const float v = ks[g * (per_group + P) + i];
-          b = fmaxf(b, fminf(a, v));
-          a = fmaxf(a, v);
-        }
-      for (int off = P / 2; off > 0; off >>= 1) {
-        const float oa = __shfl_xor_sync(kFull, a, off), ob = __shfl_xor_sync(kFull, b, off);
-        b = fmaxf(fminf(a, oa), fmaxf(b, ob));
-        a = fmaxf(a, oa);
-      }
-      __syncwarp();
-      const float worth = p.group_keys == 2 ? a + b : a;
-      int before = 0;
-      for (int j = 0; j < p.groups; ++j) {
-        const float other = __shfl_sync(kFull, worth, j * P);
-        before += other > worth || (other == worth && j < g);
-      }
-      const bool first = lane % P == 0 && g < p.groups;
-      const uint32_t kept = __ballot_sync(kFull, first && before < p.top_groups);
-      if (scored && p.top_groups < p.groups) {
-        const int in = __ffs(__ballot_sync(kFull, first && before == p.top_groups - 1)) - 1;
-        const int out = __ffs(__ballot_sync(kFull, first && before == p.top_groups)) - 1;
-        const float hi = __shfl_sync(kFull, worth, in), lo = __shfl_sync(kFull, worth, out);
-        again = lo > -INFINITY && hi - lo <= 2.f * near + 2.f * kRound * fmaxf(fabsf(hi), fabsf(lo));
-      }
-      int ge = e0 / per_group, left = per_group - (e0 - ge * per_group);
+      // distance below the largest in steps of the range, then the expert
+      float hi = -INFINITY, lo = INFINITY;
 #pragma unroll
       for (int j = 0; j < EPL; ++j) {
-        if (j < p.per && ge < p.groups && !((kept >> (ge * P)) & 1u)) o[j] = 0;
-        if (--left == 0) {
-          ++ge;
-          left = per_group;
-        }
+        hi = fmaxf(hi, k[j]);
+        lo = fminf(lo, k[j] == -INFINITY ? INFINITY : k[j]);
       }
+      hi = unordered(__reduce_max_sync(kFull, ordered(hi)));
+      lo = unordered(__reduce_min_sync(kFull, ordered(lo)));
+      const float range = hi - lo;
+      const float scale = range > 1e-30f ? steps / range : 0.f;
+#pragma unroll
+      for (int j = 0; j < EPL; ++j) {
+        // the sum's low 23 bits are the rounded distance; the shift leaves nothing else
+        const uint32_t d = __float_as_uint(fmaf(hi - k[j], scale, kMagic));
+        v[j] = k[j] == -INFINITY ? kNone : d << bits | (uint32_t)expert_of<VEC>(j);
+      }
+      const float bound =
+          (biased ? near + kRound * fmaxf(fabsf(hi), fabsf(lo)) : 0.f) * scale + 4.f;
+      close = (uint32_t)fminf(bound, steps) << bits;
     }
 
     int mine = -1;
     if (!again) {
-      uint32_t last = 0;
-      int last_e = 0;
-      for (int r = 0; r <= p.R; ++r) {          // one more: the first that is left out
-        uint32_t best = 0;
-#pragma unroll
-        for (int j = 0; j < EPL; ++j) best = max(best, o[j]);
-        const uint32_t all = warp_max(best);
-        if (all == 0) break;
-        const int src = __ffs(__ballot_sync(kFull, best == all)) - 1;
-        int at = 0;
-#pragma unroll
-        for (int j = EPL - 1; j >= 0; --j)
-          if (o[j] == all) at = j;
-        const int e = __shfl_sync(kFull, e0 + at, src);
-        if (p.bias && r > 0) {
-          const float hi = unordered(last), lo = unordered(all);
-          if (hi - lo <= near + kRound * fmaxf(fabsf(hi), fabsf(lo)) &&
-              (to_f32(row[e]) != to_f32(row[last_e]) || p.bias[e] != p.bias[last_e])) {
-            again = true;
-            break;
+      uint32_t s[3];
+      smallest_three<EPL>(v, 0, s);
+      auto take = [&](uint32_t best) {        // the lane that holds it goes on to its next
+        const bool popped = s[0] == best;
+        if (popped) {
+          s[0] = s[1]; s[1] = s[2]; s[2] = kNone;
+        }
+        if (EPL > 3 && __any_sync(kFull, popped && s[0] == kNone)) {
+          uint32_t more[3];
+          smallest_three<EPL>(v, best, more);
+          if (popped) {
+            s[0] = more[0]; s[1] = more[1]; s[2] = more[2];
           }
         }
-        if (lane == src) {
-#pragma unroll
-          for (int j = 0; j < EPL; ++j)
-            if (j == at) o[j] = 0;
-        }
-        if (lane == r && r < p.R) mine = e;
-        last = all;
-        last_e = e;
+      };
+      auto differ = [&](uint32_t a, uint32_t b) {   // not the same logit under the same bias
+        const int x = a & ((1u << bits) - 1), y = b & ((1u << bits) - 1);
+        return to_f32(row[x]) != to_f32(row[y]) || (biased && p.bias[x] != p.bias[y]);
+      };
+      uint32_t last = 0;
+      int taken = 0;                          // experts in order; lane r holds the r-th
+      bool unsure = false;                    // two that follow each other may be swapped
+      for (; taken < p.R; ++taken) {
+        const uint32_t best = __reduce_min_sync(kFull, s[0]);
+        if (best == kNone) break;
+        if (best - last <= close) unsure |= differ(best, last);
+        if (lane == taken) mine = best & ((1u << bits) - 1);
+        take(best);
+        last = best;
       }
+      while (true) {                          // those left out that may belong before the last
+        const uint32_t best = __reduce_min_sync(kFull, s[0]);
+        if (best == kNone || taken < p.R || best - last > close || !differ(best, last)) break;
+        unsure = true;
+        if (taken == 32) {
+          again = true;
+          break;
+        }
+        if (lane == taken) mine = best & ((1u << bits) - 1);
+        take(best);
+        last = best;
+        ++taken;
+      }
+      if (unsure && !again) mine = order_exact<T>(row, p, mine);
     }
-    if (again) mine = choose_exact<T, EPL>(row, p);
+    if (again) mine = choose_exact<T>(row, p);
     const bool here = lane < p.R && mine >= 0;
     const float xm = here ? to_f32(row[mine]) : 0.f;
-    const float v = weight_of(p, xm, here, m, sum);
+    const float weight = weight_of(p, xm, here, m, sum, half);
     if (lane < p.R) {
       idx[t * p.R + lane] = mine;
-      w[t * p.R + lane] = v;
+      w[t * p.R + lane] = weight;
     }
   }
 }
@@ -386,7 +531,6 @@ route_scores_bwd_kernel(const T* __restrict__ logits, const RouteParams p,
                         const int32_t* __restrict__ idx, const float* __restrict__ dw,
                         T* __restrict__ dlogits, long long ld_out) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int e0 = lane * p.per;
   for (long long t = blockIdx.x * RW + warp; t < p.T; t += gridDim.x * RW) {
     const T* row = logits + t * p.ld;
     T* out = dlogits + t * ld_out;
@@ -411,7 +555,7 @@ route_scores_bwd_kernel(const T* __restrict__ logits, const RouteParams p,
     } else if (p.renormalise) {
       RouteParams one = p;
       one.scale = 1.f;
-      const float u = weight_of(one, x, here, m, sum);
+      const float u = weight_of(one, x, here, m, sum, 16);
       dot = warp_sum(here ? g * u : 0.f);
       d = u * (g - dot);
       if (p.sigmoid) d /= 1.f + expf(x);
@@ -434,11 +578,12 @@ route_scores_bwd_kernel(const T* __restrict__ logits, const RouteParams p,
       if constexpr (VEC) {
 #pragma unroll
         for (int j = 0; j < EPL; j += 4)
-          Vec<T, 4>::store(out + e0 + j, Vec<T, 4>::pack(v + j));
+          if (expert_of<VEC>(j) < p.E)
+            Vec<T, 4>::store(out + expert_of<VEC>(j), Vec<T, 4>::pack(v + j));
       } else {
 #pragma unroll
         for (int j = 0; j < EPL; ++j)
-          if (j < p.per && e0 + j < p.E) out[e0 + j] = from_f32<T>(v[j]);
+          if (expert_of<VEC>(j) < p.E) out[expert_of<VEC>(j)] = from_f32<T>(v[j]);
       }
       if (first) all -= expf(x - m) / sum * dot;
     } else {
@@ -451,28 +596,33 @@ route_scores_bwd_kernel(const T* __restrict__ logits, const RouteParams p,
 
 RouteParams params_of(const ScoresArgs& a) {
   const moe_router_t& r = a.router;
-  return {a.ld, a.T, a.E, a.R, ceil_div(a.E, 32), r.score == MOE_SCORE_SIGMOID, r.groups,
+  return {a.ld, a.T, a.E, a.R, r.score == MOE_SCORE_SIGMOID, r.groups,
           r.top_groups, r.group_keys, r.renormalise != 0, r.scale, a.bias};
 }
 
 int blocks_of(int T) { return (int)std::min<long long>(((long long)T + RW - 1) / RW, 152 * 16); }
 
-// A row's experts in vectors of four: E = 32 EPL, rows and base aligned to four elements.
+// A row's experts in vectors of four: their number, the rows and the base allow it.
 template <typename T>
 bool vectors(const void* p, long long ld, int E) {
-  return E % 128 == 0 && reinterpret_cast<uintptr_t>(p) % (4 * sizeof(T)) == 0 && ld % 4 == 0;
+  return E % 4 == 0 && reinterpret_cast<uintptr_t>(p) % (4 * sizeof(T)) == 0 && ld % 4 == 0;
 }
 
-// Calls f(std::integral_constant EPL, vec) for the smallest EPL that holds E experts.
-#define MOE_EPL(E, CALL)                      \
+// CALL(EPL, VEC) for the smallest EPL that holds E experts.
+#define MOE_EPL(E, vec, CALL)                 \
   do {                                        \
     const int per_ = ceil_div(E, 32);         \
-    if (per_ <= 2) { CALL(2); }               \
-    else if (per_ <= 4) { CALL(4); }          \
-    else if (per_ <= 8) { CALL(8); }          \
-    else if (per_ <= 12) { CALL(12); }        \
-    else if (per_ <= 16) { CALL(16); }        \
-    else { CALL(32); }                        \
+    if (vec) {                                \
+      if (per_ <= 4) CALL(4, true);           \
+      else if (per_ <= 8) CALL(8, true);      \
+      else if (per_ <= 12) CALL(12, true);    \
+      else if (per_ <= 16) CALL(16, true);    \
+      else CALL(32, true);                    \
+    } else {                                  \
+      if (per_ <= 2) CALL(2, false);          \
+      else if (per_ <= 8) CALL(8, false);     \
+      else CALL(32, false);                   \
+    }                                         \
   } while (0)
 
 template <typename T>
@@ -481,12 +631,14 @@ cudaError_t route_typed(const ScoresArgs& a, int32_t* idx, float* w, cudaStream_
   const T* l = static_cast<const T*>(a.logits);
   const size_t smem = p.groups > 1 ? (size_t)RW * (a.E + 32) * sizeof(float) : 0;
   const bool vec = vectors<T>(a.logits, a.ld, a.E);
-#define MOE_ROUTE(N)                                                                       \
-  if (vec && p.per == N && N % 4 == 0)                                                     \
-    route_scores_kernel<T, N, N % 4 == 0><<<blocks_of(a.T), RT, smem, s>>>(l, p, idx, w);  \
-  else                                                                                     \
-    route_scores_kernel<T, N, false><<<blocks_of(a.T), RT, smem, s>>>(l, p, idx, w)
-  MOE_EPL(a.E, MOE_ROUTE);
+#define MOE_ROUTE(N, V)                                                                      \
+  do {                                                                                       \
+    if (p.groups > 1)                                                                        \
+      route_scores_kernel<T, N, V, true><<<blocks_of(a.T), RT, smem, s>>>(l, p, idx, w);     \
+    else                                                                                     \
+      route_scores_kernel<T, N, V, false><<<blocks_of(a.T), RT, 0, s>>>(l, p, idx, w);       \
+  } while (0)
+  MOE_EPL(a.E, vec, MOE_ROUTE);
 #undef MOE_ROUTE
   count_launches(1);
   return cudaGetLastError();
@@ -503,14 +655,9 @@ cudaError_t bwd_typed(const ScoresArgs& a, const int32_t* idx, const float* dw, 
         <<<blocks_of(a.T), RT, 0, s>>>(l, p, idx, dw, o, ld_out);
   } else {
     const bool vec = vectors<T>(a.logits, a.ld, a.E) && vectors<T>(out, ld_out, a.E);
-#define MOE_ROUTE(N)                                                                      \
-  if (vec && p.per == N && N % 4 == 0)                                                    \
-    route_scores_bwd_kernel<T, N, N % 4 == 0, true>                                       \
-        <<<blocks_of(a.T), RT, 0, s>>>(l, p, idx, dw, o, ld_out);                         \
-  else                                                                                    \
-    route_scores_bwd_kernel<T, N, false, true>                                            \
-        <<<blocks_of(a.T), RT, 0, s>>>(l, p, idx, dw, o, ld_out)
-    MOE_EPL(a.E, MOE_ROUTE);
+#define MOE_ROUTE(N, V) \
+  route_scores_bwd_kernel<T, N, V, true><<<blocks_of(a.T), RT, 0, s>>>(l, p, idx, dw, o, ld_out)
+    MOE_EPL(a.E, vec, MOE_ROUTE);
 #undef MOE_ROUTE
   }
   count_launches(1);
