@@ -123,12 +123,13 @@ struct Args {
   int sa_ld;                  // scales of a row of A (PRODUCT_DW: of a block)
   int sb_ld;                  // scales of a row of tiles of w, or of a block of x
   int sb_plane;               // scales of an expert's w
+  // The output's planes: one; PRODUCT_DW one an expert; as many again a split, whose parts
+  // (fp32, dense) take the output's place.
   void* out;
-  long long ld_out;
-  int out_dtype, out_align;   // out_align: 32, 16 or the element's bytes
+  long long ld_out, plane;
+  int out_align;              // 32, 16 or the element's bytes
   bool accumulate;
-  bool boxed;                 // outputs leave as boxes (splits == 1, rows of 16 bytes)
-  float* parts;               // splits > 1: fp32 [splits, N (PRODUCT_DW: E rows), cols]
+  bool boxed;                 // outputs leave as boxes
   int* err;
 };
 
@@ -632,6 +633,7 @@ product_fp8_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constan
       }
       if (!ok) break;
       if (!p.any) continue;
+      const int z = MODE == PRODUCT_DW ? it.split * g.E + it.e : it.split;   // the output's plane
       if (g.boxed && (MODE == PRODUCT_DW || p.row - lane + 32 <= p.row_end)) {
         // whole groups of 32 rows: boxes of 128 bytes a row through shared memory, sent by
         // bulk tensor stores (which clip at the matrix's edges)
@@ -657,7 +659,6 @@ product_fp8_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constan
           fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) {
-            const int z = MODE == PRODUCT_DW ? it.e : 0;
             if (MODE == PRODUCT_DW && g.accumulate)
               tma_add_3d(&tmO, box0 + slot * OUT_BOX, p.c0 + c, p.row, z);
             else
@@ -668,18 +669,11 @@ product_fp8_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constan
         continue;
       }
       if (p.row >= p.row_end) continue;
-      const size_t out_row = MODE == PRODUCT_DW ? (size_t)it.e * g.rows + p.row : (size_t)p.row;
+      T* out = static_cast<T*>(g.out) + z * g.plane + p.row * g.ld_out + p.c0;
 #pragma unroll
       for (int c = 0; c < CW; c += 16) {
         if (p.c0 + c >= g.cols) break;
-        if (g.splits.d > 1) {
-          const size_t all = MODE == PRODUCT_DW ? (size_t)g.E * g.rows : (size_t)g.N;
-          store16(g.parts + ((size_t)it.split * all + out_row) * g.cols + p.c0 + c, acc + c, 16,
-                  false);
-        } else {
-          store16(static_cast<T*>(g.out) + out_row * g.ld_out + p.c0 + c, acc + c, g.out_align,
-                  MODE == PRODUCT_DW && g.accumulate);
-        }
+        store16(out + c, acc + c, g.out_align, MODE == PRODUCT_DW && g.accumulate);
       }
     }
     if (lane == 0) bulk_wait_all();          // the boxes have left before shared memory goes
@@ -694,17 +688,16 @@ product_fp8_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constan
   }
 }
 
-// out = the splits' parts added in order (and to what is there), for the rows that the
-// product computed: [offsets[0], offsets[E]) of the N, or all (PRODUCT_DW).  A thread takes
-// four columns.
+// out = the splits' parts (g.out, see Args) added in order (and to what is there), for the
+// rows that the product computed: [offsets[0], offsets[E]) of the N, or all (PRODUCT_DW).  A
+// thread takes four columns.
 template <typename T, bool DW>
 __global__ void __launch_bounds__(256)
-join_parts_kernel(const float* __restrict__ parts, long long rows, const Args g,
-                  T* __restrict__ out) {
+join_parts_kernel(const Args g, long long rows, T* __restrict__ out, long long ld_out,
+                  bool accumulate) {
   wait_for_previous();
+  const float* parts = static_cast<const float*>(g.out);
   const int splits = g.splits.d, cols = g.cols;
-  const long long ld_out = g.ld_out;
-  const bool accumulate = DW && g.accumulate;
   long long r0 = 0, r1 = rows;
   if (g.offsets) {   // offsets that are not valid: nothing was computed, nothing is written
     bool bad = false;
@@ -731,7 +724,8 @@ join_parts_kernel(const float* __restrict__ parts, long long rows, const Args g,
     T* o = out + r * ld_out + c;
     const float x[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-    for (int j = 0; j < 4; ++j) o[j] = from_f32<T>(accumulate ? x[j] + to_f32(o[j]) : x[j]);
+    for (int j = 0; j < 4; ++j)
+      o[j] = from_f32<T>(DW && accumulate ? x[j] + to_f32(o[j]) : x[j]);
   }
 }
 
@@ -766,9 +760,9 @@ cudaError_t launch(const CUtensorMap& ma, const CUtensorMap& mb, const CUtensorM
 }
 
 template <int MODE>
-cudaError_t launch_typed(const CUtensorMap& ma, const CUtensorMap& mb, const CUtensorMap& mo,
-                         const Args& g, long long items, cudaStream_t s) {
-  switch (g.out_dtype) {
+cudaError_t launch_typed(int dtype, const CUtensorMap& ma, const CUtensorMap& mb,
+                         const CUtensorMap& mo, const Args& g, long long items, cudaStream_t s) {
+  switch (dtype) {
     case MOE_BF16: return launch<MODE, __nv_bfloat16>(ma, mb, mo, g, items, s);
     case MOE_F16: return launch<MODE, __half>(ma, mb, mo, g, items, s);
     default: return launch<MODE, float>(ma, mb, mo, g, items, s);
@@ -776,33 +770,45 @@ cudaError_t launch_typed(const CUtensorMap& ma, const CUtensorMap& mb, const CUt
 }
 
 template <typename T>
-cudaError_t join(const Args& g, bool dw, long long rows, cudaStream_t s) {
+cudaError_t join(const ProductArgs& a, const Args& g, long long rows, cudaStream_t s) {
   const long long quads = rows * (g.cols / 4);
   const int blocks = (int)std::max<long long>(1, std::min<long long>((quads + 255) / 256, kSms * 8));
-  T* out = static_cast<T*>(g.out);
-  const cudaError_t e =
-      dw ? launch_after(join_parts_kernel<T, true>, blocks, 256, s, g.parts, rows, g, out)
-         : launch_after(join_parts_kernel<T, false>, blocks, 256, s, g.parts, rows, g, out);
+  T* out = static_cast<T*>(a.out);
+  const cudaError_t e = a.mode == PRODUCT_DW
+      ? launch_after(join_parts_kernel<T, true>, blocks, 256, s, g, rows, out, a.ld_out, a.accumulate)
+      : launch_after(join_parts_kernel<T, false>, blocks, 256, s, g, rows, out, a.ld_out, false);
   count_launches(1);
   return e;
 }
 
 // Over how many CTAs a tile's contraction is split, and the items' number at most.  Known
-// from the sizes alone.
+// from the sizes alone: the split with the least estimated time, counting half a microsecond a
+// block of 128 in a CTA, 3 us for the second kernel and 4 TB/s for writing and reading the
+// parts.  Measured without and with a split: 1 row, n = K = 4096: 21 and 11 us (9 CTAs a
+// tile); 1001 rows, n 2064, K 1040: 12 and 18 us (3 CTAs a tile; not taken).
 struct Cut {
   int splits;
   long long items;
 };
 
 Cut cut_of(int mode, int N, int n, int K, int E) {
-  const int nt = ceil_div(mode == PRODUCT ? n : K, BN);
+  const int cols = mode == PRODUCT ? n : K, nt = ceil_div(cols, BN);
   long long tiles = (long long)E * ceil_div(n, BM) * nt;
   if (mode != PRODUCT_DW)
     tiles = std::min<long long>(N, ((long long)N + (long long)std::min(E, N) * (BM - 1)) / BM) * nt;
   const int kblocks = ceil_div(mode == PRODUCT_DW ? N : (mode == PRODUCT ? K : n), BK);
   Cut c{1, tiles};
-  if (tiles > 0 && 2 * tiles <= kSms && kblocks >= 2)
-    c.splits = (int)std::min<long long>(kSms / tiles, kblocks);
+  if (tiles > 0 && 2 * tiles <= kSms) {
+    const double part_us = (double)(mode == PRODUCT_DW ? (long long)E * n : N) * cols * 8 / 4e6;
+    double best = 0.5 * kblocks;
+    for (int s = 2; s <= kblocks && s * tiles <= kSms; ++s) {
+      const double t = 0.5 * ceil_div(kblocks, s) + 3.0 + s * part_us;
+      if (t < best) {
+        best = t;
+        c.splits = s;
+      }
+    }
+  }
   c.items *= c.splits;
   return c;
 }
@@ -842,19 +848,21 @@ cudaError_t launch_product_fp8(const ProductArgs& a, float* parts, int* err, cud
   g.sa_vec = g.sa_ld % 4 == 0 && reinterpret_cast<uintptr_t>(a.sa) % 16 == 0 &&
              cut.splits == 1;
   g.sb_plane = ceil_div(a.n, BK) * ceil_div(a.K, BK);
-  g.out = a.out;
-  g.ld_out = a.ld_out;
-  g.out_dtype = a.out_dtype;
-  const int es = dtype_bytes(a.out_dtype);
+  const int planes = dw ? a.E : 1;
+  const long long all = dw ? (long long)a.E * a.n : (long long)a.N;   // rows of the output
+  const bool split = cut.splits > 1;
+  const int dtype = split ? MOE_F32 : a.out_dtype, es = dtype_bytes(dtype);
+  g.out = split ? parts : a.out;
+  g.ld_out = split ? cols : a.ld_out;
+  g.plane = (dw ? a.n : a.N) * g.ld_out;
   const unsigned long long low =
-      reinterpret_cast<uintptr_t>(a.out) | (unsigned long long)(a.ld_out * es);
+      reinterpret_cast<uintptr_t>(g.out) | (unsigned long long)(g.ld_out * es);
   g.out_align = low % 32 == 0 ? 32 : (low % 16 == 0 ? 16 : es);
-  g.accumulate = a.accumulate;
-  g.parts = parts;
+  g.accumulate = a.accumulate && !split;
   g.err = err;
   // boxes out: rows of 16-byte aligned pieces; sums added to 16-bit outputs are rounded once,
   // by the thread that reads them
-  g.boxed = cut.splits == 1 && g.out_align >= 16 && !(a.accumulate && es == 2);
+  g.boxed = g.out_align >= 16 && !(g.accumulate && es == 2);
   CUtensorMap ma, mb, mo;
   // a: [N, inner]; b: w [E, n, K], or x [N, K].  A matrix without rows is not read.
   const void* pa = a.N > 0 ? a.a : a.out;
@@ -865,20 +873,20 @@ cudaError_t launch_product_fp8(const ProductArgs& a, float* parts, int* err, cud
     return cudaErrorInvalidValue;
   mo = ma;
   if (g.boxed &&
-      !encode_map_out(&mo, a.out_dtype, a.out, dw ? a.E : 1, dw ? a.n : rows, cols, a.ld_out))
+      !encode_map_out(&mo, dtype, g.out, (long long)planes * cut.splits, dw ? a.n : rows, cols,
+                      g.ld_out))
     return cudaErrorInvalidValue;
   cudaError_t e;
   switch (a.mode) {
-    case PRODUCT: e = launch_typed<PRODUCT>(ma, mb, mo, g, cut.items, s); break;
-    case PRODUCT_DX: e = launch_typed<PRODUCT_DX>(ma, mb, mo, g, cut.items, s); break;
-    default: e = launch_typed<PRODUCT_DW>(ma, mb, mo, g, cut.items, s); break;
+    case PRODUCT: e = launch_typed<PRODUCT>(dtype, ma, mb, mo, g, cut.items, s); break;
+    case PRODUCT_DX: e = launch_typed<PRODUCT_DX>(dtype, ma, mb, mo, g, cut.items, s); break;
+    default: e = launch_typed<PRODUCT_DW>(dtype, ma, mb, mo, g, cut.items, s); break;
   }
-  if (e != cudaSuccess || cut.splits == 1) return e;
-  const long long all = dw ? (long long)a.E * a.n : (long long)a.N;
+  if (e != cudaSuccess || !split) return e;
   switch (a.out_dtype) {
-    case MOE_BF16: return join<__nv_bfloat16>(g, dw, all, s);
-    case MOE_F16: return join<__half>(g, dw, all, s);
-    default: return join<float>(g, dw, all, s);
+    case MOE_BF16: return join<__nv_bfloat16>(a, g, all, s);
+    case MOE_F16: return join<__half>(a, g, all, s);
+    default: return join<float>(a, g, all, s);
   }
 }
 

@@ -96,7 +96,7 @@ template <typename T> struct Words {
 
 // VEC: 16 elements of x are aligned vectors of 16 bytes.
 template <typename T, int FORM, bool VEC>
-__global__ void __launch_bounds__(QT, sizeof(T) == 2 && FORM != (ROWS | COLS) ? 4 : 2)
+__global__ void __launch_bounds__(QT, sizeof(T) == 2 ? 4 : (FORM == ROWS ? 3 : 2))
 quantize_fp8_kernel(const T* __restrict__ x, long long ldx, long long n, int K, long long plane,
                     int row_tiles, int col_tiles, uint8_t* __restrict__ row_codes,
                     float* __restrict__ row_scales, uint8_t* __restrict__ col_codes,
@@ -199,6 +199,11 @@ quantize_fp8_kernel(const T* __restrict__ x, long long ldx, long long n, int K, 
   }
 
   if (FORM & COLS) {
+    // the words anew: the floats of the rows' codes are not kept (146 registers instead of 77)
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int j = 0; j < W::n; ++j) asm volatile("" : "+r"(raw[i][j]));
     uint32_t top[W::n];
 #pragma unroll
     for (int j = 0; j < W::n; ++j) {
