@@ -62,14 +62,19 @@ constexpr int STAGES = 3;                      // of one box of A and two of B
 constexpr int STAGE_BYTES = 3 * BOX;
 // Blocks' scales in shared memory: for each of the CTA's 128 rows the product of both
 // operands' scales, once for either half of the columns; PRODUCT_DW: the rows' scales and the
-// 256 columns'.  A slot is written when the accumulator two blocks before it is full: every
+// 256 columns', in the order in which threads take them (column_slot).  A slot is written when the accumulator two blocks before it is full: every
 // epilogue warp has then given back the one four blocks before, so it has read the scales of
 // the one five blocks before.
 template <int MODE> struct Ring {
   static constexpr int slots = 5;
-  static constexpr int floats = 128 + (MODE == PRODUCT_DW ? BN : 128);
+  static constexpr int floats = 128 + (MODE == PRODUCT_DW ? 2 * 4 * 36 : 128);
   static constexpr int bytes = slots * floats * 4;
 };
+// PRODUCT_DW: a thread owns columns 2 q, 2 q + 1 of every eight (q = lane % 4) of its warp's
+// 128, so theirs lie together, those of another q 36 floats on (no bank conflicts).
+__device__ __forceinline__ int column_slot(int c) {   // c: even column of the 256
+  return 128 + ((c >> 7) * 4 + (c >> 1 & 3)) * 36 + (c >> 3 & 15) * 2;
+}
 // Finished sums on their way out: two boxes of 32 rows of 128 bytes an epilogue warp.
 constexpr int OUT_BOX = 32 * 128;
 constexpr int OUT_BYTES = EPI_WARPS * 2 * OUT_BOX;
@@ -127,7 +132,7 @@ struct Args {
   // (fp32, dense) take the output's place.
   void* out;
   long long ld_out, plane;
-  int out_align;              // 32, 16 or the element's bytes
+  int out_align;              // 16 or the element's bytes
   bool accumulate;
   bool boxed;                 // outputs leave as boxes
   int* err;
@@ -153,6 +158,21 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, float (&v)[32]) {
         "=f"(v[20]), "=f"(v[21]), "=f"(v[22]), "=f"(v[23]), "=f"(v[24]), "=f"(v[25]),
         "=f"(v[26]), "=f"(v[27]), "=f"(v[28]), "=f"(v[29]), "=f"(v[30]), "=f"(v[31])
       : "r"(taddr));
+}
+// 32 columns of the warp's 32 lanes in fragments of 8 columns: element 16 h + 4 i + k is row
+// 16 h + lane / 4 + 8 (k / 2), column 8 i + 2 (lane % 4) + k % 2.
+__device__ __forceinline__ void tmem_ld_fragments(uint32_t taddr, float (&v)[32]) {
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    float* o = v + 16 * h;
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x256b.x4.b32 "
+        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : "=f"(o[0]), "=f"(o[1]), "=f"(o[2]), "=f"(o[3]), "=f"(o[4]), "=f"(o[5]), "=f"(o[6]),
+          "=f"(o[7]), "=f"(o[8]), "=f"(o[9]), "=f"(o[10]), "=f"(o[11]), "=f"(o[12]),
+          "=f"(o[13]), "=f"(o[14]), "=f"(o[15])
+        : "r"(taddr + ((uint32_t)(16 * h) << 16)));
+  }
 }
 // The loads of tmem_ld32 so far have landed.  Their values are used by asm volatile only
 // (add_scaled), which stays behind this; naming the 32 registers here as operands costs a
@@ -274,53 +294,21 @@ __device__ __forceinline__ int schedule(const Args& g, Ctl* ctl) {
   return bad ? -1 : total;
 }
 
-// 16 finished sums of one row to `p` (a multiple of 16 columns), in the widest stores
-// that the alignment allows.
+// 16 finished sums of one row to `p`, in the widest stores that the alignment allows.
 template <typename T>
-__device__ __forceinline__ void store16(T* p, const float* v, int align, bool accumulate) {
+__device__ __forceinline__ void store16(T* p, const float* v, int align) {
+  T o[16];
+#pragma unroll
+  for (int i = 0; i < 16; ++i) o[i] = from_f32<T>(v[i]);
   if (align >= 16) {
-    if (sizeof(T) == 4) {
-      float* f = reinterpret_cast<float*>(p);
-      float o[16];
+    uint4 r[sizeof(o) / 16];
+    memcpy(r, o, sizeof(o));
 #pragma unroll
-      for (int i = 0; i < 16; i += 4) {
-        float4 old = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (accumulate) old = *reinterpret_cast<const float4*>(f + i);
-        o[i] = v[i] + old.x; o[i + 1] = v[i + 1] + old.y;
-        o[i + 2] = v[i + 2] + old.z; o[i + 3] = v[i + 3] + old.w;
-      }
-      if (align >= 32) {
-        st_global_v8(f, o);
-        st_global_v8(f + 8, o + 8);
-      } else {
+    for (int i = 0; i < (int)(sizeof(o) / 16); ++i) reinterpret_cast<uint4*>(p)[i] = r[i];
+  } else {
 #pragma unroll
-        for (int i = 0; i < 16; i += 4)
-          *reinterpret_cast<float4*>(f + i) = make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
-      }
-      return;
-    }
-    union {
-      T h[16];
-      Raw32 r;
-    } u;
-    if (accumulate) {
-      u.r.a = *reinterpret_cast<const uint4*>(p);
-      u.r.b = *reinterpret_cast<const uint4*>(p + 8);
-#pragma unroll
-      for (int i = 0; i < 16; ++i) u.h[i] = from_f32<T>(v[i] + to_f32(u.h[i]));
-    } else {
-#pragma unroll
-      for (int i = 0; i < 16; ++i) u.h[i] = from_f32<T>(v[i]);
-    }
-    if (align >= 32) {
-      store32(p, u.r);
-    } else {
-      *reinterpret_cast<uint4*>(p) = u.r.a;
-      *reinterpret_cast<uint4*>(p + 8) = u.r.b;
-    }
-    return;
+    for (int i = 0; i < 16; ++i) p[i] = o[i];
   }
-  for (int i = 0; i < 16; ++i) p[i] = from_f32<T>(accumulate ? v[i] + to_f32(p[i]) : v[i]);
 }
 
 template <int MODE, typename T>
@@ -531,7 +519,8 @@ product_fp8_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constan
         if (MODE == PRODUCT_DW) {
           slot[tid] = a[0][0];
           slot[tid + PT] = a[1][0];
-          *reinterpret_cast<float4*>(slot + 128 + 4 * tid) = cols;
+          *reinterpret_cast<float2*>(slot + column_slot(4 * tid)) = make_float2(cols.x, cols.y);
+          *reinterpret_cast<float2*>(slot + column_slot(4 * tid + 2)) = make_float2(cols.z, cols.w);
         } else {
 #pragma unroll
           for (int i = 0; i < 2; ++i)
@@ -586,21 +575,20 @@ product_fp8_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constan
         tc_fence_before();
         if (lane == 0) mbar_arrive(bars + kTempty + 8 * (count & 1u));
       };
-      auto add = [&](float* to, const float (&v)[32], int c, float f, const float* w) {
+      auto load = [&](uint32_t t, float (&v)[32]) {
+        if (MODE == PRODUCT_DW) tmem_ld_fragments(t, v);
+        else tmem_ld32(t, v);
+      };
+      // f: the row's scale (PRODUCT_DW: its four rows'), w: this thread's columns' of the chunk
+      auto add = [&](float* to, const float (&v)[32], const float (&f)[4], const float4 (&w)[2]) {
+        if (MODE == PRODUCT_DW) {
+          const float ws[8] = {w[0].x, w[0].y, w[0].z, w[0].w, w[1].x, w[1].y, w[1].z, w[1].w};
 #pragma unroll
-        for (int i = 0; i < 32; i += 4) {
-          if (MODE == PRODUCT_DW) {
-            const float4 x = *reinterpret_cast<const float4*>(w + c + i);
-            add_scaled(to[i], v[i], x.x * f);
-            add_scaled(to[i + 1], v[i + 1], x.y * f);
-            add_scaled(to[i + 2], v[i + 2], x.z * f);
-            add_scaled(to[i + 3], v[i + 3], x.w * f);
-          } else {
-            add_scaled(to[i], v[i], f);
-            add_scaled(to[i + 1], v[i + 1], f);
-            add_scaled(to[i + 2], v[i + 2], f);
-            add_scaled(to[i + 3], v[i + 3], f);
-          }
+          for (int j = 0; j < 32; ++j)
+            add_scaled(to[j], v[j], ws[(j >> 2 & 3) * 2 + (j & 1)] * f[(j >> 4) * 2 + (j >> 1 & 1)]);
+        } else {
+#pragma unroll
+          for (int j = 0; j < 32; ++j) add_scaled(to[j], v[j], f[0]);
         }
       };
 #pragma unroll 1
@@ -610,26 +598,35 @@ product_fp8_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constan
         ok = __all_sync(kFull, ok);
         if (!ok) break;
         tc_fence_after();
-        if (p.any) tmem_ld32(t, v0);
+        if (p.any) load(t, v0);
         const float* slot = ring + (count % Rg::slots) * Rg::floats;
-        const float f =
-            slot[MODE == PRODUCT_DW ? q * 32 + lane : part * CW / 128 * 128 + q * 32 + lane];
-        const float* w = slot + 128 + part * CW;
+        float f[4];
+        float4 w[4][2];                       // by 32 columns
+        if (MODE == PRODUCT_DW) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) f[i] = slot[q * 32 + lane / 4 + 8 * i];
+          const float4* ws =
+              reinterpret_cast<const float4*>(slot + column_slot(part * 128 + 2 * (lane & 3)));
+#pragma unroll
+          for (int i = 0; i < 8; ++i) w[i / 2][i % 2] = ws[i];
+        } else {
+          f[0] = slot[part * 128 + q * 32 + lane];
+        }
         if (p.any) {
           tmem_ld_wait();
-          tmem_ld32(t + 32, v1);
-          add(acc, v0, 0, f, w);
+          load(t + 32, v1);
+          add(acc, v0, f, w[0]);
           tmem_ld_wait();
-          tmem_ld32(t + 64, v0);
-          add(acc + 32, v1, 32, f, w);
+          load(t + 64, v0);
+          add(acc + 32, v1, f, w[1]);
           tmem_ld_wait();
-          tmem_ld32(t + 96, v1);
-          add(acc + 64, v0, 64, f, w);
+          load(t + 96, v1);
+          add(acc + 64, v0, f, w[2]);
           tmem_ld_wait();
         }
         release();
         ++count;
-        if (p.any) add(acc + 96, v1, 96, f, w);
+        if (p.any) add(acc + 96, v1, f, w[3]);
       }
       if (!ok) break;
       if (!p.any) continue;
@@ -639,22 +636,39 @@ product_fp8_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constan
         // bulk tensor stores (which clip at the matrix's edges)
         constexpr int BC = 128 / sizeof(T);   // columns a box
         const uint32_t box0 = smem_u32(boxes) + (warp - EPI_WARP0) * (2 * OUT_BOX);
-        uint8_t* row0 = boxes + (warp - EPI_WARP0) * (2 * OUT_BOX) + lane * 128;
+        uint8_t* box_p = boxes + (warp - EPI_WARP0) * (2 * OUT_BOX);
 #pragma unroll
         for (int c = 0; c < CW; c += BC) {
           if (p.c0 + c >= g.cols) break;
           const int slot = c / BC & 1;
-          if (lane == 0) {                    // the box before in this slot has been read
-            if (c < 2 * BC) bulk_wait_read_0();
-            else bulk_wait_read_1();
+          if (c != BC) {                      // the boxes before in both slots, or in this one,
+            if (lane == 0) {                  // have been read
+              if (c == 0) bulk_wait_read_0();
+              else bulk_wait_read_1();
+            }
+            __syncwarp();
           }
-          __syncwarp();
+          if (MODE == PRODUCT_DW) {
 #pragma unroll
-          for (int j = 0; j < 8; ++j) {       // 16 bytes each, 128-byte swizzle
-            constexpr int W = 16 / sizeof(T);
-            const typename Vec<T, W>::Raw r = Vec<T, W>::pack(acc + c + j * W);
-            *reinterpret_cast<typename Vec<T, W>::Raw*>(row0 + slot * OUT_BOX +
-                                                        ((j ^ (lane & 7)) * 16)) = r;
+            for (int j = 0; j < BC; j += 2) { // pairs of a fragment, 128-byte swizzle
+              const int ch = j / 32, h = j >> 4 & 1, i = j >> 2 & 3, up = j >> 1 & 1;
+              const int r = 16 * h + lane / 4 + 8 * up;
+              const int byte = (32 * ch + 8 * i + 2 * (lane & 3)) * (int)sizeof(T);
+              T two[2] = {from_f32<T>(acc[c + j]), from_f32<T>(acc[c + j + 1])};
+              using Pair = typename RawOf<2 * sizeof(T)>::type;
+              Pair raw;
+              memcpy(&raw, two, sizeof(raw));
+              *reinterpret_cast<Pair*>(box_p + slot * OUT_BOX + r * 128 +
+                                       (((byte >> 4) ^ (r & 7)) << 4) + (byte & 15)) = raw;
+            }
+          } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {     // 16 bytes each, 128-byte swizzle
+              constexpr int W = 16 / sizeof(T);
+              const typename Vec<T, W>::Raw r = Vec<T, W>::pack(acc + c + j * W);
+              *reinterpret_cast<typename Vec<T, W>::Raw*>(box_p + slot * OUT_BOX + lane * 128 +
+                                                          ((j ^ (lane & 7)) * 16)) = r;
+            }
           }
           fence_proxy_async_smem();
           __syncwarp();
@@ -668,12 +682,23 @@ product_fp8_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constan
         }
         continue;
       }
+      T* out = static_cast<T*>(g.out) + z * g.plane;
+      if (MODE == PRODUCT_DW) {               // added to 16-bit gradients: one rounding
+#pragma unroll
+        for (int j = 0; j < CW; ++j) {
+          const int row = p.row - lane + 16 * (j >> 4 & 1) + lane / 4 + 8 * (j >> 1 & 1);
+          const int col = p.c0 + 32 * (j >> 5) + 8 * (j >> 2 & 3) + 2 * (lane & 3) + (j & 1);
+          if (row >= p.row_end || col >= g.cols) continue;
+          T* o = out + row * g.ld_out + col;
+          *o = from_f32<T>(acc[j] + to_f32(*o));
+        }
+        continue;
+      }
       if (p.row >= p.row_end) continue;
-      T* out = static_cast<T*>(g.out) + z * g.plane + p.row * g.ld_out + p.c0;
 #pragma unroll
       for (int c = 0; c < CW; c += 16) {
         if (p.c0 + c >= g.cols) break;
-        store16(out + c, acc + c, g.out_align, MODE == PRODUCT_DW && g.accumulate);
+        store16(out + p.row * g.ld_out + p.c0 + c, acc + c, g.out_align);
       }
     }
     if (lane == 0) bulk_wait_all();          // the boxes have left before shared memory goes
@@ -857,12 +882,12 @@ cudaError_t launch_product_fp8(const ProductArgs& a, float* parts, int* err, cud
   g.plane = (dw ? a.n : a.N) * g.ld_out;
   const unsigned long long low =
       reinterpret_cast<uintptr_t>(g.out) | (unsigned long long)(g.ld_out * es);
-  g.out_align = low % 32 == 0 ? 32 : (low % 16 == 0 ? 16 : es);
+  g.out_align = low % 16 == 0 ? 16 : es;
   g.accumulate = a.accumulate && !split;
   g.err = err;
   // boxes out: rows of 16-byte aligned pieces; sums added to 16-bit outputs are rounded once,
   // by the thread that reads them
-  g.boxed = g.out_align >= 16 && !(g.accumulate && es == 2);
+  g.boxed = g.out_align == 16 && !(g.accumulate && es == 2);
   CUtensorMap ma, mb, mo;
   // a: [N, inner]; b: w [E, n, K], or x [N, K].  A matrix without rows is not read.
   const void* pa = a.N > 0 ? a.a : a.out;
