@@ -885,9 +885,9 @@ cudaError_t launch_product_fp8(const ProductArgs& a, float* parts, int* err, cud
   g.out_align = low % 16 == 0 ? 16 : es;
   g.accumulate = a.accumulate && !split;
   g.err = err;
-  // boxes out: rows of 16-byte aligned pieces; sums added to 16-bit outputs are rounded once,
-  // by the thread that reads them
-  g.boxed = g.out_align == 16 && !(g.accumulate && es == 2);
+  // boxes out: rows of 16-byte aligned pieces (apart by less than a tensor map's limit); sums
+  // added to 16-bit outputs are rounded once, by the thread that reads them
+  g.boxed = g.out_align == 16 && !(g.accumulate && es == 2) && g.ld_out < (1LL << 37);
   CUtensorMap ma, mb, mo;
   // a: [N, inner]; b: w [E, n, K], or x [N, K].  A matrix without rows is not read.
   const void* pa = a.N > 0 ? a.a : a.out;

@@ -272,9 +272,10 @@ __device__ __forceinline__ void load_row(const T* row, const RouteParams& p, flo
   }
 }
 
-// Largest logit of the token and the sum of exp(l - m), as needed for softmax scores.
-template <int EPL>
-__device__ __forceinline__ void softmax_parts(const float (&x)[EPL], float& m, float& sum) {
+// Largest logit of the token and the sum of exp(l - m), as needed for softmax scores; KEEP:
+// x becomes exp(l - m).
+template <int EPL, bool KEEP>
+__device__ __forceinline__ void softmax_parts(float (&x)[EPL], float& m, float& sum) {
   m = -INFINITY;
   bool nan = false;
 #pragma unroll
@@ -287,7 +288,11 @@ __device__ __forceinline__ void softmax_parts(const float (&x)[EPL], float& m, f
   if (__any_sync(kFull, nan)) m = NAN;
   sum = 0.f;
 #pragma unroll
-  for (int j = 0; j < EPL; ++j) sum += x[j] == -INFINITY ? 0.f : expf(x[j] - m);
+  for (int j = 0; j < EPL; ++j) {
+    const float z = x[j] == -INFINITY ? 0.f : expf(x[j] - m);
+    sum += z;
+    if (KEEP) x[j] = z;
+  }
   sum = warp_sum(sum);
 }
 
@@ -350,8 +355,9 @@ route_scores_kernel(const T* __restrict__ logits, const RouteParams p, int32_t* 
   b_lo = unordered(__reduce_min_sync(kFull, ordered(b_lo)));
   // Sigmoid scores and a bias: every key is in [b_lo, 1 + b_hi], the same for all tokens, and
   // a key's integer is one fma of its score.
-  const bool fixed = !GROUPS && p.sigmoid && biased && !bad_bias;
-  const float f_scale = steps / (1.f + b_hi - b_lo);
+  const float f_range = 1.f + b_hi - b_lo;
+  const bool fixed = !GROUPS && p.sigmoid && biased && !bad_bias && f_range < 1e30f;
+  const float f_scale = steps / f_range;
   if (fixed) {
 #pragma unroll
     for (int j = 0; j < EPL; ++j) bias[j] = fmaf(1.f + b_hi - bias[j], f_scale, kMagic);
@@ -369,7 +375,7 @@ route_scores_kernel(const T* __restrict__ logits, const RouteParams p, int32_t* 
     float k[EPL];                            // keys, first of all the logits
     load_row<T, EPL, VEC>(row, p, k);
     float m = 0.f, sum = 1.f;
-    if (!p.sigmoid && (scored || !p.renormalise)) softmax_parts<EPL>(k, m, sum);
+    if (!p.sigmoid && (scored || !p.renormalise)) softmax_parts<EPL, false>(k, m, sum);
     bool odd = bad_bias;                     // NaN or +inf: by the definition's arithmetic
 #pragma unroll
     for (int j = 0; j < EPL; ++j) odd |= !(k[j] < INFINITY);
@@ -451,6 +457,7 @@ route_scores_kernel(const T* __restrict__ logits, const RouteParams p, int32_t* 
       hi = unordered(__reduce_max_sync(kFull, ordered(hi)));
       lo = unordered(__reduce_min_sync(kFull, ordered(lo)));
       const float range = hi - lo;
+      again |= range == INFINITY;
       const float scale = range > 1e-30f ? steps / range : 0.f;
 #pragma unroll
       for (int j = 0; j < EPL; ++j) {
@@ -534,6 +541,8 @@ route_scores_bwd_kernel(const T* __restrict__ logits, const RouteParams p,
   for (long long t = blockIdx.x * RW + warp; t < p.T; t += gridDim.x * RW) {
     const T* row = logits + t * p.ld;
     T* out = dlogits + t * ld_out;
+    float v[EPL];
+    if (DENSE) load_row<T, EPL, VEC>(row, p, v);
     int e = lane < p.R ? idx[t * p.R + lane] : -1;
     if ((unsigned)e >= (unsigned)p.E) e = -1;
     float x = e >= 0 ? to_f32(row[e]) : -INFINITY;
@@ -541,17 +550,15 @@ route_scores_bwd_kernel(const T* __restrict__ logits, const RouteParams p,
     if (!here) x = 0.f;
     const float g = here ? dw[t * p.R + lane] * p.scale : 0.f;
     float d, m = 0.f, sum = 1.f;
-    float v[EPL];
     float dot = 0.f;
     if (DENSE) {
-      load_row<T, EPL, VEC>(row, p, v);
-      softmax_parts<EPL>(v, m, sum);
+      softmax_parts<EPL, true>(v, m, sum);
       const float s = here ? expf(x - m) / sum : 0.f;
       dot = warp_sum(here ? g * s : 0.f);
       d = s * g;
-      const float inv = 1.f / sum;
+      const float inv = sum == 0.f ? 0.f : 1.f / sum;   // 0: every expert is closed
 #pragma unroll
-      for (int j = 0; j < EPL; ++j) v[j] = v[j] == -INFINITY ? 0.f : -expf(v[j] - m) * inv * dot;
+      for (int j = 0; j < EPL; ++j) v[j] = -(v[j] * inv) * dot;
     } else if (p.renormalise) {
       RouteParams one = p;
       one.scale = 1.f;
@@ -563,15 +570,18 @@ route_scores_bwd_kernel(const T* __restrict__ logits, const RouteParams p,
       const float z = expf(-fabsf(x));
       d = g * z / ((1.f + z) * (1.f + z));
     }
-    // an expert named twice gets both
-    float all = 0.f;
+    float all = d;
     bool first = here;      // the lowest slot that names this expert
-    for (int r = 0; r < p.R; ++r) {
-      const int er = __shfl_sync(kFull, e, r);
-      const float dr = __shfl_sync(kFull, d, r);
-      if (er == e && here) {
-        all += dr;
-        if (r < lane) first = false;
+    const uint32_t same = __match_any_sync(kFull, here ? e : -1 - lane);
+    if (__any_sync(kFull, __popc(same) > 1)) {   // an expert named twice gets both
+      all = 0.f;
+      for (int r = 0; r < p.R; ++r) {
+        const int er = __shfl_sync(kFull, e, r);
+        const float dr = __shfl_sync(kFull, d, r);
+        if (er == e && here) {
+          all += dr;
+          if (r < lane) first = false;
+        }
       }
     }
     if (DENSE) {

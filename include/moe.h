@@ -743,12 +743,12 @@ moe_status_t moe_quantize_fp8_tiles(const void* w, int dtype, int E, int n, int 
  * are summed in fp32, those sums times both scales in fp32, one rounding at the end.
  * xq, xs: rows [N,K] in the row form; wq, wscale: [E,n,K] in tiles; out: [N,n] of bf16, fp16
  * or fp32, rows ld_out elements apart.  offsets: int32 [E+1] on the device, not falling, in
- * [0, N]; NULL with E == 1: all N rows (a plain matrix product).  Rows outside every segment
- * are not read and left as they are.  Offsets that are not valid are reported
+ * [0, N]; NULL with E == 1: all N rows (a plain matrix product).  Rows of xq outside every
+ * segment have no effect, those of out are left as they are.  Offsets that are not valid are reported
  * (MOE_ERR_BAD_ROUTING with MOE_CHECK) and nothing is computed.
  * n and K are multiples of 16, N <= 2^30, E <= 1024; codes 16-byte aligned.  The workspace
- * (error word; sums of few tiles split over several CTAs) is the same for the three
- * products of one N, n, K, E.
+ * (error word; sums of few tiles split over several CTAs) has one size for the three products
+ * of one N, n, K, E; calls that may overlap need one each.  Bitwise reproducible.
  */
 moe_status_t moe_product_fp8(const uint8_t* xq, const float* xs, const int32_t* offsets, int N,
                              int n, int K, int E, const uint8_t* wq, const float* wscale,
@@ -771,7 +771,8 @@ moe_status_t moe_product_fp8_dx(const uint8_t* dyq, const float* dys, const int3
  * dyq, dys: dL/dout [N,n], xq, xs: [N,K], both in the column form.  Blocks of 128 rows
  * belong to one expert: offsets are multiples of 128 (moe_sort with align 128), a segment
  * that ends at N may end anywhere.  dw: [E,n,K] of bf16, fp16 or fp32, dense, 16-byte
- * aligned; with MOE_ACCUMULATE the sum is added to it.  xs and dys 16-byte aligned.
+ * aligned; with MOE_ACCUMULATE the sum is added to it (fp32: a value below the normal range
+ * counts as zero).  xs and dys 16-byte aligned.
  */
 moe_status_t moe_product_fp8_dw(const uint8_t* dyq, const float* dys, const uint8_t* xq,
                                 const float* xs, const int32_t* offsets, int N, int n, int K,

@@ -343,3 +343,54 @@ def test_replayed_graph_follows_its_inputs(lib):
     step()
     torch.cuda.synchronize()
     assert torch.equal(got[0], idx) and torch.equal(got[1], w) and torch.equal(got[2], dl)
+
+
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+@pytest.mark.parametrize("renormalise", [True, False])
+def test_gradient_of_closed_tokens_is_zero(lib, score, renormalise):
+    """Every expert closed (a padded token), or the chosen ones alone."""
+    x = torch.randn(6, 64, device="cuda", generator=torch.Generator(device="cuda").manual_seed(1))
+    x[:2] = -float("inf")
+    x[2, :4] = -float("inf")
+    idx = torch.arange(4, device="cuda").int().repeat(6, 1)
+    idx[0] = -1
+    dw = torch.ones(6, 4, device="cuda")
+    out = torch.full((6, 64), float("nan"), device="cuda")
+    lib.moe_route_scores_bwd(x, lib.Router(score=score, renormalise=renormalise), idx, dw, out)
+    assert torch.isfinite(out).all()
+    assert (out[:3] == 0).all()
+    if renormalise:     # equal dw: the weights' sum is fixed, so the gradient is 0 but for rounding
+        assert (out[3:].abs() <= 64 * 2.0 ** -24).all()
+    else:
+        assert (out[3:] != 0).any(1).all()
+
+
+def test_logits_and_biases_of_any_range(lib):
+    """Keys whose range leaves the steps of a key's integer, or fp32 altogether."""
+    g = torch.Generator(device="cuda").manual_seed(6)
+    x = torch.randn(40, 96, device="cuda", generator=g)
+    x[::4] *= 1e-6
+    x[1::4] *= 1e30
+    x[2::4, ::2] = 3e38
+    x[2::4, 1::2] = -3e38
+    for score in ("sigmoid", "softmax"):
+        idx, _ = forward(lib, x, None, 8, score=score)
+        assert np.array_equal(idx.cpu().numpy(), choice(x.double().cpu().numpy(), None, 8, score))
+    x = torch.randn(40, 96, device="cuda", generator=g)
+    for size in (1e-8, 1e3, 1e20, 1e35):
+        bias = torch.randn(96, device="cuda", generator=g) * size
+        idx, _ = forward(lib, x, bias, 8, score="sigmoid")
+        ref = choice(x.double().cpu().numpy(), bias.double().cpu().numpy(), 8, "sigmoid")
+        assert np.array_equal(idx.cpu().numpy(), ref), size
+
+
+def test_a_long_run_of_near_ties(lib):
+    """More keys within the error bound of each other than a warp has lanes: all of the token's
+    choice in 64 bits.  Logits of 20 to 30 have sigmoids within 2e-9 of each other."""
+    g = torch.Generator(device="cuda").manual_seed(9)
+    x = torch.rand(20, 256, device="cuda", generator=g) * 10 + 20
+    x[::2, 100:] -= 30
+    bias = torch.zeros(256, device="cuda")
+    for groups in (1, 8):
+        check(lib, x, bias, 8, groups=groups, top_groups=max(1, groups // 2),
+              group_keys=2 if groups > 1 else 1)
