@@ -146,18 +146,19 @@ struct Item {
 };
 
 // 32 consecutive fp32 columns of this thread's TMEM lane; the values are there after
-// tmem_ld_wait.
+// tmem_ld_wait.  (Two loads of 16: 32 registers in a row across a loop's end cost spills.)
 __device__ __forceinline__ void tmem_ld32(uint32_t taddr, float (&v)[32]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
-      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
-      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
-      : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]),
-        "=f"(v[7]), "=f"(v[8]), "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]),
-        "=f"(v[14]), "=f"(v[15]), "=f"(v[16]), "=f"(v[17]), "=f"(v[18]), "=f"(v[19]),
-        "=f"(v[20]), "=f"(v[21]), "=f"(v[22]), "=f"(v[23]), "=f"(v[24]), "=f"(v[25]),
-        "=f"(v[26]), "=f"(v[27]), "=f"(v[28]), "=f"(v[29]), "=f"(v[30]), "=f"(v[31])
-      : "r"(taddr));
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    float* o = v + 16 * h;
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : "=f"(o[0]), "=f"(o[1]), "=f"(o[2]), "=f"(o[3]), "=f"(o[4]), "=f"(o[5]), "=f"(o[6]),
+          "=f"(o[7]), "=f"(o[8]), "=f"(o[9]), "=f"(o[10]), "=f"(o[11]), "=f"(o[12]),
+          "=f"(o[13]), "=f"(o[14]), "=f"(o[15])
+        : "r"(taddr + 16 * h));
+  }
 }
 // 32 columns of the warp's 32 lanes in fragments of 8 columns: element 16 h + 4 i + k is row
 // 16 h + lane / 4 + 8 (k / 2), column 8 i + 2 (lane % 4) + k % 2.
@@ -580,8 +581,9 @@ product_fp8_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constan
         else tmem_ld32(t, v);
       };
       // f: the row's scale (PRODUCT_DW: its four rows'), w: this thread's columns' of the chunk
-      auto add = [&](float* to, const float (&v)[32], const float (&f)[4], const float4 (&w)[2]) {
-        if (MODE == PRODUCT_DW) {
+      constexpr int NF = MODE == PRODUCT_DW ? 4 : 1, NW = MODE == PRODUCT_DW ? 2 : 1;
+      auto add = [&](float* to, const float (&v)[32], const float (&f)[NF], const float4 (&w)[NW]) {
+        if constexpr (MODE == PRODUCT_DW) {
           const float ws[8] = {w[0].x, w[0].y, w[0].z, w[0].w, w[1].x, w[1].y, w[1].z, w[1].w};
 #pragma unroll
           for (int j = 0; j < 32; ++j)
@@ -591,6 +593,15 @@ product_fp8_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constan
           for (int j = 0; j < 32; ++j) add_scaled(to[j], v[j], f[0]);
         }
       };
+      // The last 32 columns of a block are added beside the first load of the next one.
+      float f_last[NF];
+      float4 w_last[NW];                      // (PRODUCT_DW)
+#pragma unroll
+      for (int i = 0; i < NF; ++i) f_last[i] = 0.f;
+#pragma unroll
+      for (int i = 0; i < NW; ++i) w_last[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int i = 0; i < 32; ++i) v1[i] = 0.f;
 #pragma unroll 1
       for (int kb = it.kb0; kb < it.kb1 && ok; ++kb) {
         const uint32_t buf = count & 1u, t = lanes + buf * BN;
@@ -598,21 +609,22 @@ product_fp8_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constan
         ok = __all_sync(kFull, ok);
         if (!ok) break;
         tc_fence_after();
-        if (p.any) load(t, v0);
-        const float* slot = ring + (count % Rg::slots) * Rg::floats;
-        float f[4];
-        float4 w[4][2];                       // by 32 columns
-        if (MODE == PRODUCT_DW) {
-#pragma unroll
-          for (int i = 0; i < 4; ++i) f[i] = slot[q * 32 + lane / 4 + 8 * i];
-          const float4* ws =
-              reinterpret_cast<const float4*>(slot + column_slot(part * 128 + 2 * (lane & 3)));
-#pragma unroll
-          for (int i = 0; i < 8; ++i) w[i / 2][i % 2] = ws[i];
-        } else {
-          f[0] = slot[part * 128 + q * 32 + lane];
-        }
         if (p.any) {
+          load(t, v0);
+          const float* slot = ring + (count % Rg::slots) * Rg::floats;
+          float f[NF];
+          float4 w[4][NW];                    // by 32 columns
+          if constexpr (MODE == PRODUCT_DW) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) f[i] = slot[q * 32 + lane / 4 + 8 * i];
+            const float4* ws =
+                reinterpret_cast<const float4*>(slot + column_slot(part * 128 + 2 * (lane & 3)));
+#pragma unroll
+            for (int i = 0; i < 8; ++i) w[i / 2][i % 2] = ws[i];
+          } else {
+            f[0] = slot[part * 128 + q * 32 + lane];
+          }
+          add(acc + 96, v1, f_last, w_last);
           tmem_ld_wait();
           load(t + 32, v1);
           add(acc, v0, f, w[0]);
@@ -623,11 +635,17 @@ product_fp8_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constan
           load(t + 96, v1);
           add(acc + 64, v0, f, w[2]);
           tmem_ld_wait();
+#pragma unroll
+          for (int i = 0; i < NF; ++i) f_last[i] = f[i];
+          if constexpr (MODE == PRODUCT_DW) {
+            w_last[0] = w[3][0];
+            w_last[1] = w[3][1];
+          }
         }
         release();
         ++count;
-        if (p.any) add(acc + 96, v1, f, w[3]);
       }
+      if (p.any) add(acc + 96, v1, f_last, w_last);
       if (!ok) break;
       if (!p.any) continue;
       const int z = MODE == PRODUCT_DW ? it.split * g.E + it.e : it.split;   // the output's plane
