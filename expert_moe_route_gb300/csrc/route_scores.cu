@@ -14,7 +14,7 @@
 // Equal logits under equal biases are equal in any precision and need no second look.
 //
 // A warp takes a token, a lane up to EPL of its experts.  A key becomes one 32-bit integer:
-// its distance below the token's largest key in 2^23 (E > 512: 2^22) steps of the keys' range,
+// its distance below the largest in 2^23 steps of the keys' range (2^22 where a lane holds 32),
 // then the expert, so that the warp's smallest integer (redux.sync) is the next expert and ties
 // go to the lower one by themselves.  A lane keeps its three smallest in order and finds the
 // next three when they are taken (8% of the tokens of 8 in 384).  A token whose keys are not
@@ -323,17 +323,22 @@ __device__ __forceinline__ void smallest_three(const uint32_t (&v)[EPL], uint32_
   }
 }
 
-// GROUPS: groups > 1.  Blocks an SM: choose_exact, rare, would else set the registers of all.
-template <typename T, int EPL, bool VEC, bool GROUPS>
-__global__ void __launch_bounds__(RT, EPL <= 8 ? 4 : (EPL <= 16 ? 3 : 2))
+// What a call's keys are: logits or scores of one group; of several groups; sigmoid scores
+// with a bias and one group, whose integer is one fma of the score, since every token's keys
+// are in [lowest bias, 1 + highest bias].
+enum Keys : int { ANY = 0, GROUPED = 1, BIASED = 2 };
+
+// Blocks an SM: choose_exact, rare, would else set the registers of all.
+template <typename T, int EPL, bool VEC, int KEYS>
+__global__ void __launch_bounds__(RT, EPL <= 8 || (EPL <= 12 && KEYS == BIASED) ? 4 : (EPL <= 16 ? 3 : 2))
 route_scores_kernel(const T* __restrict__ logits, const RouteParams p, int32_t* __restrict__ idx,
                     float* __restrict__ w) {
-  extern __shared__ float group_keys_s[];    // GROUPS: a token's keys, E + 32 a warp
+  extern __shared__ float group_keys_s[];    // GROUPED: a token's keys, E + 32 a warp
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const bool biased = p.bias != nullptr;
+  const bool biased = KEYS == BIASED || p.bias != nullptr;
   const bool scored = biased || p.group_keys == 2;   // keys are scores, not logits
-  const int bits = p.E > 512 ? 10 : 9;
-  const float steps = (p.E > 512 ? 4194304.f : 8388608.f) - 72.f;
+  constexpr int bits = EPL <= 16 ? 9 : 10;   // of an expert's number
+  constexpr float steps = (float)(1 << (32 - bits)) - 72.f;
   constexpr float kMagic = 8388608.f + 64.f; // distances start at 64: the first is near none
   int half = 1;
   while (2 * half < p.R) half *= 2;
@@ -351,20 +356,23 @@ route_scores_kernel(const T* __restrict__ logits, const RouteParams p, int32_t* 
     }
   }
   bad_bias = __any_sync(kFull, bad_bias);
-  b_hi = unordered(__reduce_max_sync(kFull, ordered(b_hi)));
-  b_lo = unordered(__reduce_min_sync(kFull, ordered(b_lo)));
-  // Sigmoid scores and a bias: every key is in [b_lo, 1 + b_hi], the same for all tokens, and
-  // a key's integer is one fma of its score.
-  const float f_range = 1.f + b_hi - b_lo;
-  const bool fixed = !GROUPS && p.sigmoid && biased && !bad_bias && f_range < 1e30f;
-  const float f_scale = steps / f_range;
-  if (fixed) {
+  float f_scale = 0.f;
+  uint32_t close = 0;                        // distances up to this may be in the wrong order
+  if constexpr (KEYS == BIASED) {
+    b_hi = unordered(__reduce_max_sync(kFull, ordered(b_hi)));
+    b_lo = unordered(__reduce_min_sync(kFull, ordered(b_lo)));
+    const float range = 1.f + b_hi - b_lo;
+    bad_bias |= !(range < 1e30f);
+    f_scale = steps / range;
 #pragma unroll
     for (int j = 0; j < EPL; ++j) bias[j] = fmaf(1.f + b_hi - bias[j], f_scale, kMagic);
+    // (two steps more: the offsets are rounded to whole steps)
+    const float most = fmaxf(fabsf(1.f + b_hi), fabsf(b_lo));
+    close = (uint32_t)fminf((kNearSigmoid + kRound * most) * f_scale + 6.f, steps) << bits;
   }
   int P = 1, per_group = p.E;                // groups: lanes each, and experts
-  uint8_t place[GROUPS ? EPL : 1];           // P times the expert's group
-  if constexpr (GROUPS) {
+  uint8_t place[KEYS == GROUPED ? EPL : 1];  // P times the expert's group
+  if constexpr (KEYS == GROUPED) {
     per_group = p.E / p.groups;
     while (2 * P * p.groups <= 32) P *= 2;
 #pragma unroll
@@ -375,23 +383,20 @@ route_scores_kernel(const T* __restrict__ logits, const RouteParams p, int32_t* 
     float k[EPL];                            // keys, first of all the logits
     load_row<T, EPL, VEC>(row, p, k);
     float m = 0.f, sum = 1.f;
-    if (!p.sigmoid && (scored || !p.renormalise)) softmax_parts<EPL, false>(k, m, sum);
+    if (KEYS != BIASED && !p.sigmoid && (scored || !p.renormalise))
+      softmax_parts<EPL, false>(k, m, sum);
     bool odd = bad_bias;                     // NaN or +inf: by the definition's arithmetic
 #pragma unroll
     for (int j = 0; j < EPL; ++j) odd |= !(k[j] < INFINITY);
     bool again = __any_sync(kFull, odd);
 
     uint32_t v[EPL];                         // keys as integers
-    uint32_t close;                          // distances up to this may be in the wrong order
-    if (fixed) {
+    if constexpr (KEYS == BIASED) {
 #pragma unroll
       for (int j = 0; j < EPL; ++j) {
         const uint32_t d = __float_as_uint(fmaf(fast_sigmoid(k[j]), -f_scale, bias[j]));
         v[j] = k[j] == -INFINITY ? kNone : d << bits | (uint32_t)expert_of<VEC>(j);
       }
-      // (two steps more: the offsets are rounded to whole steps)
-      const float most = fmaxf(fabsf(1.f + b_hi), fabsf(b_lo));
-      close = (uint32_t)fminf((kNearSigmoid + kRound * most) * f_scale + 6.f, steps) << bits;
     } else {
       float near = 0.f;                      // error bound of a difference of two keys
       if (scored) {
@@ -403,7 +408,7 @@ route_scores_kernel(const T* __restrict__ logits, const RouteParams p, int32_t* 
           k[j] = k[j] == -INFINITY ? k[j] : s + bias[j];
         }
       }
-      if constexpr (GROUPS) {
+      if constexpr (KEYS == GROUPED) {
         float* ks = group_keys_s + warp * (p.E + 32);
         // a group's keys start P words apart from a multiple of its length: no bank conflicts
 #pragma unroll
@@ -474,12 +479,14 @@ route_scores_kernel(const T* __restrict__ logits, const RouteParams p, int32_t* 
     if (!again) {
       uint32_t s[3];
       smallest_three<EPL>(v, 0, s);
+      // no lane has given its third while those taken are below every lane's third
+      uint32_t thirds = __reduce_min_sync(kFull, s[2]);
       auto take = [&](uint32_t best) {        // the lane that holds it goes on to its next
         const bool popped = s[0] == best;
         if (popped) {
           s[0] = s[1]; s[1] = s[2]; s[2] = kNone;
         }
-        if (EPL > 3 && __any_sync(kFull, popped && s[0] == kNone)) {
+        if (EPL > 3 && best >= thirds && __any_sync(kFull, popped && s[0] == kNone)) {
           uint32_t more[3];
           smallest_three<EPL>(v, best, more);
           if (popped) {
@@ -644,9 +651,11 @@ cudaError_t route_typed(const ScoresArgs& a, int32_t* idx, float* w, cudaStream_
 #define MOE_ROUTE(N, V)                                                                      \
   do {                                                                                       \
     if (p.groups > 1)                                                                        \
-      route_scores_kernel<T, N, V, true><<<blocks_of(a.T), RT, smem, s>>>(l, p, idx, w);     \
+      route_scores_kernel<T, N, V, GROUPED><<<blocks_of(a.T), RT, smem, s>>>(l, p, idx, w);  \
+    else if (p.sigmoid && p.bias)                                                            \
+      route_scores_kernel<T, N, V, BIASED><<<blocks_of(a.T), RT, 0, s>>>(l, p, idx, w);      \
     else                                                                                     \
-      route_scores_kernel<T, N, V, false><<<blocks_of(a.T), RT, 0, s>>>(l, p, idx, w);       \
+      route_scores_kernel<T, N, V, ANY><<<blocks_of(a.T), RT, 0, s>>>(l, p, idx, w);         \
   } while (0)
   MOE_EPL(a.E, vec, MOE_ROUTE);
 #undef MOE_ROUTE
