@@ -509,18 +509,29 @@ route_scores_kernel(const T* __restrict__ logits, const RouteParams p, int32_t* 
         take(best);
         last = best;
       }
-      while (true) {                          // those left out that may belong before the last
-        const uint32_t best = __reduce_min_sync(kFull, s[0]);
-        if (best == kNone || taken < p.R || best - last > close || !differ(best, last)) break;
-        unsure = true;
-        if (taken == 32) {
-          again = true;
-          break;
+      // Those left out that may belong before one that was taken are within `close` of the last.
+      // Where they all equal it, and no two of those taken may be swapped, they come after it.
+      uint32_t best = taken == p.R ? __reduce_min_sync(kFull, s[0]) : kNone;
+      if (best != kNone && best - last <= close && !unsure) {
+        unsure = differ(best, last);
+        if (!unsure) {
+          bool other = false;
+#pragma unroll
+          for (int j = 0; j < EPL; ++j)
+            if (v[j] != kNone && v[j] > last && v[j] - last <= close) other |= differ(v[j], last);
+          unsure = __any_sync(kFull, other);
         }
-        if (lane == taken) mine = best & ((1u << bits) - 1);
-        take(best);
-        last = best;
-        ++taken;
+      }
+      if (unsure) {
+        for (; best != kNone && best - last <= close; best = __reduce_min_sync(kFull, s[0])) {
+          if (taken == 32) {
+            again = true;
+            break;
+          }
+          if (lane == taken) mine = best & ((1u << bits) - 1);
+          take(best);
+          ++taken;
+        }
       }
       if (unsure && !again) mine = order_exact<T>(row, p, mine);
     }

@@ -394,3 +394,19 @@ def test_a_long_run_of_near_ties(lib):
     for groups in (1, 8):
         check(lib, x, bias, 8, groups=groups, top_groups=max(1, groups // 2),
               group_keys=2 if groups > 1 else 1)
+
+
+@pytest.mark.parametrize("E,R", [(96, 8), (384, 8), (64, 1), (1024, 32), (256, 20)])
+def test_equal_keys_beside_closer_ones(lib, E, R):
+    """Few values and their neighbours in fp32, many times over, beside one far below: equal keys
+    lie between others that the token's range does not tell apart."""
+    g = np.random.default_rng(E + R)
+    values = np.array([2.5, 2.25, 1.75, 0.5], np.float32)
+    x = values[g.integers(0, g.integers(1, 5, (512, 1)), (512, E))]
+    step = g.integers(-2, 3, (512, E)) * (g.random((512, 1)) < 0.7)
+    x = (x.view(np.int32) + step.astype(np.int32)).view(np.float32)
+    x[:, 0] = -9.0
+    x = torch.from_numpy(x).cuda()
+    for score in ("sigmoid", "softmax"):
+        for bias in (None, torch.full((E,), 0.25, device="cuda")):
+            check(lib, x, bias, R, score=score)
