@@ -8,7 +8,7 @@
 // and w = 0.
 //
 // The choice is that of c in 64 bits: two scores can lie closer to each other than 32 bits
-// tell, about one token in five hundred at 384 experts.  The scores are computed in 32 bits;
+// tell, about one token in five hundred of 384 normal logits.  The scores are computed in 32 bits;
 // where two that follow each other lie within the error bound (kNear below), experts are taken
 // on until a gap, and those taken are put in order by their keys in 64 bits, a lane each.
 // Equal logits under equal biases are equal in any precision and need no second look.
@@ -17,9 +17,13 @@
 // its distance below the largest in 2^23 steps of the keys' range (2^22 where a lane holds 32),
 // then the expert, so that the warp's smallest integer (redux.sync) is the next expert and ties
 // go to the lower one by themselves.  A lane keeps its three smallest in order and finds the
-// next three when they are taken (8% of the tokens of 8 in 384).  A token whose keys are not
-// finite, whose groups lie within the error bound or with more than 32 experts in a row that
-// do, goes to choose_exact, all of it in 64 bits (15 us at 256 experts; a lane's one key 3 us).
+// next three when they are taken (4% of the tokens, 8 of 384 experts).  Groups whose worths lie
+// within the error bound are put in order in 64 bits (groups_exact, a lane an expert at a time).
+// A token whose keys are not finite or with more than 32 experts in a row within the bound goes to
+// choose_exact, all of it in 64 bits, and takes 37 us there: kernels that send it one late end
+// late (65536 x 256 in 8 groups: 88 us, 95 to 119 before groups_exact).
+// Bound by the issue of instructions: 65536 tokens x 384 experts, sigmoid and bias, 56 us (15.6
+// at the copy rate).
 #include <math.h>
 
 #include <algorithm>
@@ -189,6 +193,63 @@ __device__ __noinline__ int choose_exact(const T* row, const RouteParams& p) {
   return mine;
 }
 
+// Largest logit of a token and the sum of exp(l - top), in 64 bits.
+template <typename T>
+__device__ __forceinline__ void softmax_parts64(const T* row, int E, double& top, double& sum) {
+  const int lane = threadIdx.x & 31;
+  top = -INFINITY;
+  sum = 0.0;
+#pragma unroll 1
+  for (int e = lane; e < E; e += 32) top = fmax(top, (double)to_f32(row[e]));
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) top = fmax(top, __shfl_xor_sync(kFull, top, off));
+#pragma unroll 1
+  for (int e = lane; e < E; e += 32) sum += exp((double)to_f32(row[e]) - top);
+  sum = warp_sum(sum);
+}
+
+// The groups that take part, bits P g of group g, where worths in 32 bits (lane P g: of group g)
+// do not tell: those in [from, to] are put in order in 64 bits, the ones above are in.
+template <typename T>
+__device__ __noinline__ uint32_t groups_exact(const T* row, const RouteParams& p, int P, float worth,
+                                              float from, float to) {
+  const int lane = threadIdx.x & 31, per_group = p.E / p.groups;
+  const bool first = lane % P == 0 && lane / P < p.groups;
+  const uint32_t in = __ballot_sync(kFull, first && worth > to);
+  const bool open = first && worth >= from && worth <= to;
+  const uint32_t all = __ballot_sync(kFull, open);
+  double top = 0.0, sum = 1.0;
+  if (!p.sigmoid) softmax_parts64(row, p.E, top, sum);
+  unsigned long long mine = 0;
+  for (uint32_t left = all; left; left &= left - 1) {
+    const int at = __ffs(left) - 1, e0 = at / P * per_group;
+    double a = -INFINITY, b = -INFINITY;
+#pragma unroll 1
+    for (int e = e0 + lane; e < e0 + per_group; e += 32) {
+      const double l = (double)to_f32(row[e]);
+      double key = p.sigmoid ? 1.0 / (1.0 + exp(-l)) : exp(l - top) / sum;
+      if (p.bias) key += (double)p.bias[e];
+      if (l == -INFINITY) key = -INFINITY;
+      b = fmax(b, fmin(a, key));
+      a = fmax(a, key);
+    }
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) {
+      const double oa = __shfl_xor_sync(kFull, a, off), ob = __shfl_xor_sync(kFull, b, off);
+      b = fmax(fmin(a, oa), fmax(b, ob));
+      a = fmax(a, oa);
+    }
+    if (lane == at) mine = ordered(p.group_keys == 2 ? a + b : a);
+  }
+  int before = __popc(in);
+  for (uint32_t left = all; left; left &= left - 1) {
+    const int at = __ffs(left) - 1;
+    const unsigned long long o = __shfl_sync(kFull, mine, at);
+    before += o > mine || (o == mine && at < lane);
+  }
+  return in | __ballot_sync(kFull, open && before < p.top_groups);
+}
+
 // Experts of the lanes (or -1) in the order of their keys in 64 bits: lane r receives the r-th.
 template <typename T>
 __device__ __noinline__ int order_exact(const T* row, const RouteParams& p, int e) {
@@ -199,12 +260,9 @@ __device__ __noinline__ int order_exact(const T* row, const RouteParams& p, int 
     if (p.sigmoid) {
       key = 1.0 / (1.0 + exp(-l));
     } else {
-      double top = -INFINITY, sum = 0.0;
-      for (int j = lane; j < p.E; j += 32) top = fmax(top, (double)to_f32(row[j]));
-#pragma unroll
-      for (int off = 16; off > 0; off >>= 1) top = fmax(top, __shfl_xor_sync(kFull, top, off));
-      for (int j = lane; j < p.E; j += 32) sum += exp((double)to_f32(row[j]) - top);
-      key = exp(l - top) / warp_sum(sum);
+      double top, sum;
+      softmax_parts64(row, p.E, top, sum);
+      key = exp(l - top) / sum;
     }
     key += e >= 0 ? (double)p.bias[e] : 0.0;
   }
@@ -437,13 +495,14 @@ route_scores_kernel(const T* __restrict__ logits, const RouteParams p, int32_t* 
         }
         const bool first = lane % P == 0 && g < p.groups;
         // bits P g of the groups that take part
-        const uint32_t kept = __ballot_sync(kFull, first && before < p.top_groups);
+        uint32_t kept = __ballot_sync(kFull, first && before < p.top_groups);
         if (scored && p.top_groups < p.groups && !again) {
           const int in = __ffs(__ballot_sync(kFull, first && before == p.top_groups - 1)) - 1;
           const int out = __ffs(__ballot_sync(kFull, first && before == p.top_groups)) - 1;
           const float hi = __shfl_sync(kFull, worth, in), lo = __shfl_sync(kFull, worth, out);
-          again = lo > -INFINITY &&
-                  hi - lo <= 2.f * near + 2.f * kRound * fmaxf(fabsf(hi), fabsf(lo));
+          const float bound = 2.f * near + 2.f * kRound * fmaxf(fabsf(hi), fabsf(lo));
+          if (lo > -INFINITY && hi - lo <= bound)
+            kept = groups_exact<T>(row, p, P, worth, hi - bound, lo + bound);
         }
 #pragma unroll
         for (int j = 0; j < EPL; ++j) {

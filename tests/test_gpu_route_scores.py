@@ -410,3 +410,29 @@ def test_equal_keys_beside_closer_ones(lib, E, R):
     for score in ("sigmoid", "softmax"):
         for bias in (None, torch.full((E,), 0.25, device="cuda")):
             check(lib, x, bias, R, score=score)
+
+
+@pytest.mark.parametrize("E,groups,top_groups", [(256, 8, 4), (1024, 4, 1), (62, 31, 20), (96, 6, 5),
+                                                 (64, 32, 9)])
+def test_groups_closer_than_32_bits(lib, E, groups, top_groups):
+    """Groups that are others' copies, some a unit of 2^-24 off or exact: their worths differ by
+    less than 32 bits tell, or tie; in some tokens fewer groups are open than may take part."""
+    g = np.random.default_rng(E)
+    T, per = 512, E // groups
+    x = g.normal(size=(T, groups, per)).astype(np.float32)
+    for t in range(T):
+        of = g.integers(0, groups, groups) if t % 3 else np.zeros(groups, int)
+        x[t] = x[t, of]
+        step = g.integers(-1, 2, (groups, 1))
+        x[t] = np.where(step == 0, x[t], np.nextafter(x[t], np.float32(9) * step.astype(np.float32)))
+        if t % 5 == 0:
+            x[t, g.permutation(groups)[:groups // 2]] = -np.inf
+        if t % 7 == 0:
+            x[t, :, g.integers(0, per)] = -np.inf
+    x = torch.from_numpy(np.ascontiguousarray(x.reshape(T, E))).cuda()
+    R = min(8, per * top_groups)
+    for score in ("sigmoid", "softmax"):
+        for bias in (None, torch.full((E,), 0.25, device="cuda")):
+            for keys in (1, 2):
+                check(lib, x, bias, R, score=score, groups=groups, top_groups=top_groups,
+                      group_keys=keys)
