@@ -381,6 +381,11 @@ __device__ __forceinline__ void smallest_three(const uint32_t (&v)[EPL], uint32_
   }
 }
 
+// A bound of keys' distances in steps, as a difference of their integers.
+__device__ __forceinline__ uint32_t within(float bound, float steps, int bits) {
+  return bound < steps ? (uint32_t)bound << bits : 0xffffffffu;
+}
+
 // What a call's keys are: logits or scores of one group; of several groups; sigmoid scores
 // with a bias and one group, whose integer is one fma of the score, since every token's keys
 // are in [lowest bias, 1 + highest bias].
@@ -407,7 +412,7 @@ route_scores_kernel(const T* __restrict__ logits, const RouteParams p, int32_t* 
   for (int j = 0; j < EPL; ++j) {
     const int e = expert_of<VEC>(j);
     bias[j] = biased && e < p.E ? p.bias[e] : 0.f;
-    bad_bias |= !(bias[j] < INFINITY) || bias[j] == -INFINITY;
+    bad_bias |= !(fabsf(bias[j]) < 1e30f);   // (sums of two are finite)
     if (e < p.E) {
       b_hi = fmaxf(b_hi, bias[j]);
       b_lo = fminf(b_lo, bias[j]);
@@ -419,14 +424,13 @@ route_scores_kernel(const T* __restrict__ logits, const RouteParams p, int32_t* 
   if constexpr (KEYS == BIASED) {
     b_hi = unordered(__reduce_max_sync(kFull, ordered(b_hi)));
     b_lo = unordered(__reduce_min_sync(kFull, ordered(b_lo)));
-    const float range = 1.f + b_hi - b_lo;
-    bad_bias |= !(range < 1e30f);
-    f_scale = steps / range;
+    f_scale = steps / (1.f + (b_hi - b_lo));
 #pragma unroll
-    for (int j = 0; j < EPL; ++j) bias[j] = fmaf(1.f + b_hi - bias[j], f_scale, kMagic);
-    // (two steps more: the offsets are rounded to whole steps)
-    const float most = fmaxf(fabsf(1.f + b_hi), fabsf(b_lo));
-    close = (uint32_t)fminf((kNearSigmoid + kRound * most) * f_scale + 6.f, steps) << bits;
+    for (int j = 0; j < EPL; ++j) bias[j] = fmaf(1.f + (b_hi - bias[j]), f_scale, kMagic);
+    // two keys' distances: the offsets' two roundings, theirs to whole steps and the sum's, each
+    // half a step, are 4 steps; a key in 64 bits is rounded to 2^-53 of itself
+    const float most = fmaxf(fabsf(b_hi), fabsf(b_lo)) + 1.f;
+    close = within((kNearSigmoid + 1e-15f * most) * f_scale + 6.f, steps, bits);
   }
   int P = 1, per_group = p.E;                // groups: lanes each, and experts
   uint8_t place[KEYS == GROUPED ? EPL : 1];  // P times the expert's group
@@ -531,7 +535,7 @@ route_scores_kernel(const T* __restrict__ logits, const RouteParams p, int32_t* 
       }
       const float bound =
           (biased ? near + kRound * fmaxf(fabsf(hi), fabsf(lo)) : 0.f) * scale + 4.f;
-      close = (uint32_t)fminf(bound, steps) << bits;
+      close = within(bound, steps, bits);
     }
 
     int mine = -1;

@@ -436,3 +436,17 @@ def test_groups_closer_than_32_bits(lib, E, groups, top_groups):
             for keys in (1, 2):
                 check(lib, x, bias, R, score=score, groups=groups, top_groups=top_groups,
                       group_keys=keys)
+
+
+@pytest.mark.parametrize("size", [-3e7, 1e4, 3e7, 1e9, 1e29, 3e38])
+def test_large_biases_that_hardly_differ(lib, size):
+    """A bias that is far above the scores, for all experts or all but a step of fp32: what is
+    left of the scores in 64 bits decides."""
+    g = torch.Generator(device="cuda").manual_seed(11)
+    x = torch.randn(200, 128, device="cuda", generator=g)
+    bias = torch.full((128,), size, device="cuda")
+    for groups in (1, 4):
+        kw = dict(groups=groups, top_groups=max(1, groups // 2), group_keys=2 if groups > 1 else 1)
+        check(lib, x, bias, 8, **kw)
+        some = bias.view(torch.int32) - torch.arange(128, device="cuda", dtype=torch.int32) % 3
+        check(lib, x, some.view(torch.float32), 8, **kw)
