@@ -17,11 +17,14 @@
 // transposed in memory.  Every wait is bounded.
 //
 // What bounds it (GB300, 131072 rows, 128 experts, K 4096, n 1536, 410 us at twice the measured
-// bf16 rate): loads and MMAs alone 535 us, with the handshakes of the two accumulators 605, with
-// the sums 652: a block's MMAs take 540 cycles, reading its accumulator and adding it about as
-// long, and each begins some 400 cycles after the other ended.  PRODUCT_DW has a scale a column
-// too, two operations a sum: 1306 us.  Measured against it: 16 epilogue warps +26 to +50%;
-// paired fma (f32x2) +12%; pairs of CTAs (cta_group::2, 256 x 256 tiles) -5% to +4%, and -6%
+// bf16 rate, no more than a few launches in a row): 671 us, 2.46 PFLOP/s; PRODUCT_DX 727.  Loads
+// and MMAs alone take 535, without the stores 616.  A block's MMAs are 540 cycles of the tensor
+// pipe, but its 48 KB come into shared memory and go out again, 768 cycles at 128 bytes a cycle;
+// adding its accumulator takes about 520, and each side waits for the other's barrier: 920 cycles
+// a block.  PRODUCT_DW has a scale a column too, two operations a sum, and four bytes a result:
+// 1240 us, 945 without its stores, 1013 without its sums, 634 without both.  Long runs are held
+// by the power limit, 784 and 1316.  Measured against it: 16 epilogue warps +26 to +50%; paired
+// fma (f32x2) +12%; pairs of CTAs (cta_group::2, 256 x 256 tiles) -5% to +4%, and slower by 6%
 // where experts' rows do not fill their tiles; scales copied by the epilogue warps +40%.
 #include <cudaTypedefs.h>
 
@@ -62,9 +65,9 @@ constexpr int STAGES = 3;                      // of one box of A and two of B
 constexpr int STAGE_BYTES = 3 * BOX;
 // Blocks' scales in shared memory: for each of the CTA's 128 rows the product of both
 // operands' scales, once for either half of the columns; PRODUCT_DW: the rows' scales and the
-// 256 columns', in the order in which threads take them (column_slot).  A slot is written when the accumulator two blocks before it is full: every
-// epilogue warp has then given back the one four blocks before, so it has read the scales of
-// the one five blocks before.
+// 256 columns', in the order in which threads take them (column_slot).  A slot is written when
+// the accumulator two blocks before it is full: every epilogue warp has then given back the one
+// four blocks before, so it has read the scales of the one five blocks before.
 template <int MODE> struct Ring {
   static constexpr int slots = 5;
   static constexpr int floats = 128 + (MODE == PRODUCT_DW ? 2 * 4 * 36 : 128);
@@ -146,7 +149,9 @@ struct Item {
 };
 
 // 32 consecutive fp32 columns of this thread's TMEM lane; the values are there after
-// tmem_ld_wait.  (Two loads of 16: 32 registers in a row across a loop's end cost spills.)
+// tmem_ld_wait, and only asm volatile (add_scaled), which stays behind it, may use them: naming
+// them as operands of the wait costs a move each.  (Two loads of 16: 32 registers in a row
+// across a loop's end cost spills.)
 __device__ __forceinline__ void tmem_ld32(uint32_t taddr, float (&v)[32]) {
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
@@ -175,9 +180,6 @@ __device__ __forceinline__ void tmem_ld_fragments(uint32_t taddr, float (&v)[32]
         : "r"(taddr + ((uint32_t)(16 * h) << 16)));
   }
 }
-// The loads of tmem_ld32 so far have landed.  Their values are used by asm volatile only
-// (add_scaled), which stays behind this; naming the 32 registers here as operands costs a
-// move each.
 // a += b c, in the order of the loads around it.
 __device__ __forceinline__ void add_scaled(float& a, float b, float c) {
   asm volatile("fma.rn.f32 %0, %1, %2, %0;" : "+f"(a) : "f"(b), "f"(c));
@@ -827,8 +829,9 @@ cudaError_t join(const ProductArgs& a, const Args& g, long long rows, cudaStream
 // Over how many CTAs a tile's contraction is split, and the items' number at most.  Known
 // from the sizes alone: the split with the least estimated time, counting half a microsecond a
 // block of 128 in a CTA, 3 us for the second kernel and 4 TB/s for writing and reading the
-// parts.  Measured without and with a split: 1 row, n = K = 4096: 21 and 11 us (9 CTAs a
-// tile); 1001 rows, n 2064, K 1040: 12 and 18 us (3 CTAs a tile; not taken).
+// parts.  Measured without and with a split: 1 row, n = K = 4096: 16.9 and 10.0 us (9 CTAs a
+// tile; 9.2 to 11.5 with 4 to 18); 1 row, n 2048, K 7168: 26.3 and 11.3; 1001 rows, n 2064, K
+// 1040: 10.3 and 17.9 (3 CTAs a tile; not taken).
 struct Cut {
   int splits;
   long long items;

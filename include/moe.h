@@ -744,8 +744,8 @@ moe_status_t moe_quantize_fp8_tiles(const void* w, int dtype, int E, int n, int 
  * xq, xs: rows [N,K] in the row form; wq, wscale: [E,n,K] in tiles; out: [N,n] of bf16, fp16
  * or fp32, rows ld_out elements apart.  offsets: int32 [E+1] on the device, not falling, in
  * [0, N]; NULL with E == 1: all N rows (a plain matrix product).  Rows of xq outside every
- * segment have no effect, those of out are left as they are.  Offsets that are not valid are reported
- * (MOE_ERR_BAD_ROUTING with MOE_CHECK) and nothing is computed.
+ * segment have no effect, those of out are left as they are.  Offsets that are not valid are
+ * reported (MOE_ERR_BAD_ROUTING with MOE_CHECK) and nothing is computed.
  * n and K are multiples of 16, N <= 2^30, E <= 1024; codes 16-byte aligned.  The workspace
  * (error word; sums of few tiles split over several CTAs) has one size for the three products
  * of one N, n, K, E; calls that may overlap need one each.  Bitwise reproducible.
