@@ -24,6 +24,7 @@
 // late (65536 x 256 in 8 groups: 88 us, 95 to 119 before groups_exact).
 // Bound by the issue of instructions: 65536 tokens x 384 experts, sigmoid and bias, 56 us (15.6
 // at the copy rate).
+#include <float.h>
 #include <math.h>
 
 #include <algorithm>
@@ -39,9 +40,12 @@ constexpr int RT = 256;                 // threads per block: eight tokens
 constexpr int RW = RT / 32;
 
 // Integers in the order of the floats; NaN first of all, -inf (closed) 0.
+__device__ __forceinline__ uint32_t sortable(float v) {   // of numbers; -0 below 0
+  const uint32_t b = __float_as_uint(v);
+  return b ^ ((uint32_t)((int)b >> 31) | 0x80000000u);
+}
 __device__ __forceinline__ uint32_t ordered(float v) {
-  const uint32_t b = __float_as_uint(v + 0.f);   // -0 and 0 are equal
-  const uint32_t o = b ^ ((uint32_t)((int)b >> 31) | 0x80000000u);
+  const uint32_t o = sortable(v + 0.f);   // -0 and 0 are equal
   return v != v ? 0xffffffffu : (v == -INFINITY ? 0u : o);
 }
 __device__ __forceinline__ float unordered(uint32_t o) {
@@ -75,9 +79,11 @@ __device__ __forceinline__ double warp_sum(double v) {
 // 2.5e-7 + 6e-8 of itself, a softmax within 9e-7 of the token's largest score; the bias's
 // addition rounds by 2^-24 of the key.  Two keys whose distance is above
 //   kNear * (largest score) + kRound * (larger key)
-// are in the right order.
+// are in the right order.  A group's worth is within kNear * (largest score) + kRound * (the
+// magnitudes of its one or two keys) of itself: of its keys, which may cancel in the sum.
 constexpr float kNearSigmoid = 1.0e-6f, kNearSoftmax = 2.5e-6f, kRound = 2.5e-7f;
 constexpr uint32_t kNone = 0xffffffffu;   // no expert
+constexpr uint32_t kMinusInf = 0x007fffffu;   // sortable(-inf)
 
 struct RouteParams {
   long long ld;
@@ -208,15 +214,13 @@ __device__ __forceinline__ void softmax_parts64(const T* row, int E, double& top
   sum = warp_sum(sum);
 }
 
-// The groups that take part, bits P g of group g, where worths in 32 bits (lane P g: of group g)
-// do not tell: those in [from, to] are put in order in 64 bits, the ones above are in.
+// The groups that take part, bits P g of group g, where worths in 32 bits do not tell (lane P g:
+// of group g): those that are `sure` do, the rest are the best of the `open`, in order in 64 bits.
 template <typename T>
-__device__ __noinline__ uint32_t groups_exact(const T* row, const RouteParams& p, int P, float worth,
-                                              float from, float to) {
+__device__ __noinline__ uint32_t groups_exact(const T* row, const RouteParams& p, int P, bool sure,
+                                              bool open) {
   const int lane = threadIdx.x & 31, per_group = p.E / p.groups;
-  const bool first = lane % P == 0 && lane / P < p.groups;
-  const uint32_t in = __ballot_sync(kFull, first && worth > to);
-  const bool open = first && worth >= from && worth <= to;
+  const uint32_t in = __ballot_sync(kFull, sure);
   const uint32_t all = __ballot_sync(kFull, open);
   double top = 0.0, sum = 1.0;
   if (!p.sigmoid) softmax_parts64(row, p.E, top, sum);
@@ -501,12 +505,17 @@ route_scores_kernel(const T* __restrict__ logits, const RouteParams p, int32_t* 
         // bits P g of the groups that take part
         uint32_t kept = __ballot_sync(kFull, first && before < p.top_groups);
         if (scored && p.top_groups < p.groups && !again) {
-          const int in = __ffs(__ballot_sync(kFull, first && before == p.top_groups - 1)) - 1;
-          const int out = __ffs(__ballot_sync(kFull, first && before == p.top_groups)) - 1;
-          const float hi = __shfl_sync(kFull, worth, in), lo = __shfl_sync(kFull, worth, out);
-          const float bound = 2.f * near + 2.f * kRound * fmaxf(fabsf(hi), fabsf(lo));
-          if (lo > -INFINITY && hi - lo <= bound)
-            kept = groups_exact<T>(row, p, P, worth, hi - bound, lo + bound);
+          // Each worth lies between `least` and `most` (-inf: the group is closed).  A group is
+          // in for sure above all that are out, and out below all that are in.
+          const float size = fabsf(a) + (p.group_keys == 2 ? fabsf(b) : 0.f);
+          const float err = fminf(near + kRound * size, FLT_MAX);
+          const uint32_t least = sortable(worth - err), most = sortable(worth + err);
+          const bool in = first && (kept >> lane) & 1u;
+          const uint32_t lo = __reduce_min_sync(kFull, in ? least : kNone);
+          const uint32_t hi = __reduce_max_sync(kFull, first && !in ? most : 0u);
+          if (hi > kMinusInf && lo <= hi)
+            kept = groups_exact<T>(row, p, P, first && least > hi,
+                                   first && least <= hi && most >= lo);
         }
 #pragma unroll
         for (int j = 0; j < EPL; ++j) {
