@@ -451,10 +451,11 @@ route_scores_kernel(const T* __restrict__ logits, const RouteParams p, int32_t* 
     float m = 0.f, sum = 1.f;
     if (KEYS != BIASED && !p.sigmoid && (scored || !p.renormalise))
       softmax_parts<EPL, false>(k, m, sum);
-    bool odd = bad_bias;                     // NaN or +inf: by the definition's arithmetic
+    bool odd = false;                        // NaN or +inf: by the definition's arithmetic
 #pragma unroll
     for (int j = 0; j < EPL; ++j) odd |= !(k[j] < INFINITY);
-    bool again = __any_sync(kFull, odd);
+    odd = __any_sync(kFull, odd);
+    bool again = odd || bad_bias;
 
     uint32_t v[EPL];                         // keys as integers
     if constexpr (KEYS == BIASED) {
@@ -610,7 +611,9 @@ route_scores_kernel(const T* __restrict__ logits, const RouteParams p, int32_t* 
     if (again) mine = choose_exact<T>(row, p);
     const bool here = lane < p.R && mine >= 0;
     const float xm = here ? to_f32(row[mine]) : 0.f;
-    const float weight = weight_of(p, xm, here, m, sum, half);
+    float weight = weight_of(p, xm, here, m, sum, half);
+    // a softmax that is NaN: weight_of takes renormalised weights from the chosen logits alone
+    if (KEYS != BIASED && !p.sigmoid && odd && here) weight = NAN;
     if (lane < p.R) {
       idx[t * p.R + lane] = mine;
       w[t * p.R + lane] = weight;

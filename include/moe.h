@@ -688,11 +688,13 @@ typedef struct {
  *   w[t,r] = scale * s[idx]                      renormalise == 0
  *   w[t,r] = scale * s[idx] / sum_j s[idx[t,j]]  renormalise != 0
  * The choice is that of keys computed in 64 bits from the logits and biases as they are
- * stored (without a bias experts are ordered by their logits, which is the same order).
+ * stored; without a bias experts (and groups, with group_keys 1) are ordered by their logits,
+ * which for numbers is the same order.
  * A logit of -inf closes its expert for the token: it has score 0 and is never chosen; nor
  * is one whose bias is -inf.  Slots that no expert is left for get idx -1, w 0 (as moe_sort
- * takes them).  A key of NaN comes before all others and its weight is NaN; a logit of +inf
- * makes a softmax NaN.  bias takes no part in the weights.
+ * takes them).  NaN comes before all other keys and logits.  A sigmoid of NaN is NaN; a softmax
+ * over a logit of NaN or +inf is NaN for all its experts: where the choice goes by keys the lowest
+ * come first, and every filled slot has weight NaN.  bias takes no part in the weights.
  * logits: [T,E] of bf16, fp16 or fp32, rows ld_logits elements apart; bias fp32 [E];
  * topk_idx int32 [T,R]; topk_w fp32 [T,R].  R <= 32, E <= 1024, R at most the experts of
  * top_groups groups; group_keys 2 needs groups of two.  No workspace.
@@ -706,7 +708,8 @@ moe_status_t moe_route_scores(const void* logits, long long ld_logits, int dtype
  * experts that the forward chose (constants).  Every logit is written: those of experts
  * that the weights do not depend on get 0.  Slots with idx outside [0, E) and closed
  * experts contribute nothing (their dw is not read for an empty slot); an expert named
- * twice gets the sum.  dlogits: [T,E] of the logits' type, rows ld_dlogits apart.
+ * twice gets the sum.  For renormalised weights only the chosen experts' logits are read: one
+ * of NaN elsewhere shows in the weights, not here.  dlogits: [T,E] of the logits' type, rows ld_dlogits apart.
  */
 moe_status_t moe_route_scores_bwd(const void* logits, long long ld_logits, int dtype,
                                   const int32_t* topk_idx, const float* dw, int T, int E, int R,
