@@ -6,11 +6,12 @@
 // among eight lanes (16-bit types: two rows a shuffle, two elements a maximum) and columns' go
 // through 4 KB of shared memory.
 //
-// The quotient is computed as q = x r, q + (x - q s) r with r = 1/s rounded to nearest
+// The quotient is computed as q = x r, q - (q s - x) r with r = 1/s rounded to nearest
 // (Markstein's correction of a quotient, 1990: the remainder is exact under fma): the
 // rounded quotient, three operations where the compiler's division takes about ten, which
-// would be more than the memory allows.  Scales whose remainders could leave the normal
-// range are divided.
+// would be more than the memory allows.  The remainder has the sign with which a zero keeps its
+// own: q s - x is +0, so that -0 is added to q.  Scales whose remainders could leave the normal
+// range are divided.  Under a scale of 0 codes are zeros with the elements' signs, or NaN.
 #include <type_traits>
 
 #include "kernels.h"
@@ -25,17 +26,22 @@ constexpr int BLK = 128;
 constexpr float kMax = 448.f;
 enum Form : int { ROWS = 1, COLS = 2, TILES = 4 };
 
-// 1 / s for the quotients of a block, 0 for a scale of zero (all codes are 0 then, or NaN).
-__device__ __forceinline__ float inverse(float s) { return s == 0.f ? 0.f : __frcp_rn(s); }
+// 1 / s for the quotients of a block, 0 for a scale of zero.  PAIRS: negative, see quotients.
+template <bool PAIRS> __device__ __forceinline__ float inverse(float s) {
+  const float r = s == 0.f ? 0.f : __frcp_rn(s);
+  return PAIRS ? -r : r;
+}
 __device__ __forceinline__ bool plain_range(float s) {
   return s == 0.f || (s >= 0x1p-69f && s <= 0x1p69f);
 }
 __device__ __forceinline__ float quotient(float x, float s, float r) {
   const float q = x * r;
-  return fmaf(fmaf(-q, s, x), r, q);
+  return fmaf(-fmaf(q, s, -x), r, q);
 }
 
-// Two of them: a pair of products or sums is one instruction.
+// Two of them, negated: a pair of products or sums is one instruction, whose operands cannot
+// change sign on their way in.  With r the negated inverses q is the negated quotient, x + q s is
+// +0 for a zero, and times r -0.
 __device__ __forceinline__ void quotients(const float* x, float s0, float s1, float r0, float r1,
                                           float* q) {
   asm("{\n\t.reg .b64 x, s, r, q;\n\t"
@@ -45,7 +51,7 @@ __device__ __forceinline__ void quotients(const float* x, float s0, float s1, fl
       "fma.rn.f32x2 q, x, r, q;\n\t"
       "mov.b64 {%0, %1}, q;\n\t}"
       : "=f"(q[0]), "=f"(q[1])
-      : "f"(x[0]), "f"(x[1]), "f"(-s0), "f"(-s1), "f"(r0), "f"(r1));
+      : "f"(x[0]), "f"(x[1]), "f"(s0), "f"(s1), "f"(r0), "f"(r1));
 }
 
 __device__ __forceinline__ uint32_t codes4(float a, float b, float c, float d) {
@@ -54,12 +60,14 @@ __device__ __forceinline__ uint32_t codes4(float a, float b, float c, float d) {
   return lo | (hi << 16);
 }
 
-// x / s, 0 under a scale of zero (rare: kept out of the way of the kernel's registers).
+// x / s, a zero under a scale of zero (rare: kept out of the way of the kernel's registers).
 __device__ __noinline__ float divided(float x, float s) { return s == 0.f ? x * 0.f : x / s; }
 
 // Four codes of v with a scale each.  PAIRS: quotients two at a time, where both forms are made
 // and instructions are what is short: bf16 131072 x 4096 403 us against 422.  With one form, bound by
 // memory, the pairs' registers cost more than that: by row 264 against 241, by column 281 against 269.
+// The pairs' negated quotients have their signs put right in the codes, four at a time; negated
+// one by one before they are converted the two forms take 421 us.
 template <bool PAIRS>
 __device__ __forceinline__ uint32_t codes4_of(const float* v, const float4& s, const float4& r,
                                               bool plain) {
@@ -67,7 +75,7 @@ __device__ __forceinline__ uint32_t codes4_of(const float* v, const float4& s, c
     float q[4];
     quotients(v, s.x, s.y, r.x, r.y, q);
     quotients(v + 2, s.z, s.w, r.z, r.w, q + 2);
-    return codes4(q[0], q[1], q[2], q[3]);
+    return codes4(q[0], q[1], q[2], q[3]) ^ 0x80808080u;
   }
   if (plain)
     return codes4(quotient(v[0], s.x, r.x), quotient(v[1], s.y, r.y), quotient(v[2], s.z, r.z),
@@ -216,14 +224,14 @@ quantize_fp8_kernel(const T* __restrict__ x, long long ldx, long long n, int K, 
 #pragma unroll
       for (int i = 0; i < 4; ++i) m[i] = all;
     }
-    float s = m[0] / kMax, inv = inverse(s);
+    float s = m[0] / kMax, inv = inverse<kBoth>(s);
     if ((FORM & TILES) && t == 0) row_scales[id] = s;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const long long r = r0 + 32 * i;
       if (i > 0 && !(FORM & TILES)) {
         s = m[i] / kMax;
-        inv = inverse(s);
+        inv = inverse<kBoth>(s);
       }
       float v[16];
       W::unpack(raw[i], v);
@@ -266,7 +274,7 @@ quantize_fp8_kernel(const T* __restrict__ x, long long ldx, long long n, int K, 
       for (int w = 0; w < QT / 32; ++w) m = fmaxf(m, part[w][t]);
       const float s = m / kMax;
       reinterpret_cast<float*>(scales)[t] = s;
-      reinterpret_cast<float*>(inverses)[t] = inverse(s);
+      reinterpret_cast<float*>(inverses)[t] = inverse<kBoth>(s);
       plain = plain_range(s);
       if (ct * BLK + t < K) col_scales[(size_t)rt * K + ct * BLK + t] = s;
     }

@@ -719,12 +719,13 @@ moe_status_t moe_route_scores_bwd(const void* logits, long long ld_logits, int d
 /*
  * moe_quantize_fp8 -- E4M3 codes and fp32 scales of a matrix x [N,K]:
  *   scale = largest |x| of a block / 448,  code = E4M3(x / scale)  (the fp32 quotient to
- *   nearest even, saturating; 0 under a scale of 0)
+ *   nearest even, saturating, a zero with x's sign; under a scale of 0 such a zero)
  *   row_codes uint8 [N,K],  row_scales fp32 [N, ceil(K/128)]: 128 elements of a row
  *   col_codes uint8 [N,K],  col_scales fp32 [ceil(N/128), K]: 128 elements of a column
  * Either pair may be NULL; both are written in one pass over x.  The last block of a row
- * or column may be shorter.  The row form is that of moe_dispatch_fp8.  A NaN gets the code
- * NaN and does not enter its block's scale; an infinity makes the scale infinite.
+ * or column may be shorter.  For finite x the row form is that of moe_dispatch_fp8 (which makes
+ * +0 of the zeros of a block of zeros).  A NaN gets a code of NaN, of either sign, and does not
+ * enter its block's scale; an infinity makes the scale infinite.
  * x: bf16, fp16 or fp32, rows ldx elements apart; K a multiple of 16; codes 16-byte
  * aligned.  No workspace.
  */
