@@ -3,6 +3,7 @@ import numpy as np
 import pytest
 import torch
 
+from tests import test_gpu_product_fp8 as products
 from tests import test_gpu_route_scores as routes
 
 pytestmark = pytest.mark.gpu
@@ -110,3 +111,108 @@ def test_zeros_of_rows_are_those_of_the_fp8_dispatch(lib):
     empty = (scales == 0).repeat_interleave(128, 1)
     assert empty.any() and (codes[empty] & 0x7f == 0).all() and (xq[empty] == 0).all()
     assert torch.equal(codes[~empty], xq[~empty]) and torch.equal(scales, xs)
+
+
+@pytest.mark.parametrize("back", [False, True])
+@pytest.mark.parametrize("pad", [0, 2])
+def test_products_of_several_tiles_a_block(lib, back, pad):
+    """Uneven segments of 116 row tiles and five column tiles (nine for the gradient): every
+    resident block takes three tiles or more, of several experts."""
+    g = np.random.default_rng(8)
+    counts = [int(c) for c in g.integers(0, 640, 37)]
+    counts[5] = counts[6] = counts[36] = 0
+    counts[0] = 1
+    for dtype in (torch.bfloat16, torch.float32, torch.float16):
+        products.run_rows(lib, counts, 1040, 2064 if back else 656, dtype, back, tail=7, lead=2,
+                          seed=3, pad=pad)
+
+
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+def test_router_of_more_tokens_than_a_pass_takes(lib, score):
+    """Warps take a second and third token."""
+    g = torch.Generator(device="cuda").manual_seed(12)
+    x = torch.randn(45001, 64, device="cuda", generator=g)
+    bias = torch.randn(64, device="cuda", generator=g) * 0.05
+    for b in (None, bias):
+        for kw in ({}, dict(groups=8, top_groups=3, group_keys=2)):
+            routes.check(lib, x, b, 6, score=score, **kw)
+    for renormalise in (True, False):
+        routes.test_gradient(lib, 45001, 60, 3, score, renormalise, torch.float32)
+
+
+def small_codes(shape, g):
+    """Codes of every magnitude below 2, made without a copy in floats."""
+    c = torch.randint(0, 256, shape, dtype=torch.uint8, device="cuda", generator=g)
+    return c.bitwise_and_(0xbf).view(torch.float8_e4m3fn)
+
+
+@pytest.mark.parametrize("back", [False, True])
+def test_product_rows_past_32_bit_offsets(lib, back):
+    """More than 2^31 elements in the matrix of codes, or in the result."""
+    g = torch.Generator(device="cuda").manual_seed(9)
+    N, n, K = (1 << 20) + 300, 16, 2064
+    assert N * K > 1 << 31
+    ends = [0, 1000, N - 700, N]
+    inner, outer = (n, K) if back else (K, n)
+    a, w = small_codes((N, inner), g), small_codes((3, n, K), g)
+    sa = torch.rand(N, products.blocks(inner), device="cuda", generator=g) + 0.25
+    sw = torch.rand(3, 1, products.blocks(K), device="cuda", generator=g) + 0.25
+    out = torch.empty(N, outer, dtype=torch.bfloat16, device="cuda")
+    f = lib.moe_product_fp8_dx if back else lib.moe_product_fp8
+    f(a, sa, w, sw, out, lib.workspace(lib.product_fp8_ws_bytes(N, n, K, 3)),
+      offsets=torch.tensor(ends, dtype=torch.int32, device="cuda"), flags=lib.MOE_CHECK)
+    for e, at, end in ((0, 0, 1000), (1, 1000, 1500), (1, N // 2, N // 2 + 500),
+                       (1, N - 1200, N - 700), (2, N - 700, N)):
+        av = products.value(a[at:end], sa[at:end], "row")
+        wv = products.value(w[e], sw[e], "tile")
+        wv = wv if back else wv.t()
+        products.within(out[at:end], av @ wv, av.abs() @ wv.abs(), inner, torch.bfloat16,
+                        f"rows {at} to {end}")
+
+
+@pytest.mark.parametrize("accumulate", [False, True])
+def test_weights_gradients_past_32_bit_offsets(lib, accumulate):
+    g = torch.Generator(device="cuda").manual_seed(10)
+    E, n, K, N = 260, 2064, 4112, 256
+    assert E * n * K > 1 << 31
+    dy, x = small_codes((N, n), g), small_codes((N, K), g)
+    sy, sx = (torch.rand(2, k, device="cuda", generator=g) + 0.25 for k in (n, K))
+    ends = [0] + [128] * (E - 1) + [256]             # the first and the last expert have rows
+    before = 0.5 if accumulate else float("nan")
+    dw = torch.full((E, n, K), before, dtype=torch.bfloat16, device="cuda")
+    lib.moe_product_fp8_dw(dy, sy, x, sx, dw, lib.workspace(lib.product_fp8_ws_bytes(N, n, K, E)),
+                           offsets=torch.tensor(ends, dtype=torch.int32, device="cuda"),
+                           accumulate=accumulate, flags=lib.MOE_CHECK)
+    assert (dw[1:-1] == (0.5 if accumulate else 0.0)).all()
+    for e, b in ((0, 0), (E - 1, 1)):
+        r = slice(128 * b, 128 * b + 128)
+        yv = products.value(dy[r], sy[b:b + 1], "col").t()
+        xv = products.value(x[r], sx[b:b + 1], "col")
+        products.within(dw[e], yv @ xv, yv.abs() @ xv.abs(), 128, torch.bfloat16, f"expert {e}",
+                        torch.full_like(yv @ xv, 0.5) if accumulate else None)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_gradient_between_other_columns(lib, dtype):
+    """Logits and gradient as parts of wider matrices: what is beside them stays."""
+    g = torch.Generator(device="cuda").manual_seed(13)
+    for cut, E in ((slice(0, 64), 64), (slice(4, 68), 64), (slice(1, 61), 60)):
+        wide = torch.randn(70, 80, device="cuda", generator=g).to(dtype)
+        x = wide[:, cut]
+        idx, _ = routes.forward(lib, x, None, 4, score="softmax")
+        i64 = idx.cpu().numpy()
+        dw = torch.randn(70, 4, device="cuda", generator=g)
+        for score in ("sigmoid", "softmax"):
+            for renormalise in (True, False):
+                r = lib.Router(score=score, renormalise=renormalise)
+                store = torch.full((70, 96), 3.0, device="cuda", dtype=dtype)
+                lib.moe_route_scores_bwd(x, r, idx, dw, store[:, cut])
+                a = [t.double().cpu().numpy() for t in (x, dw)]
+                ref = routes.gradient(a[0], i64, a[1], score, renormalise, 1.0)
+                size = routes.gradient_size(a[0], i64, a[1], score, renormalise, 1.0)
+                # as test_gradient: expf, the sums over E and R, and the store
+                slack = routes.UNIT * (np.ptp(a[0]) + E + 32) * size + 2.0 ** -50 * size.max()
+                bound = slack + routes.HALF[dtype] * (np.abs(ref) + slack) + routes.TINY[dtype]
+                assert (np.abs(store[:, cut].double().cpu().numpy() - ref) <= bound).all()
+                store[:, cut] = 3.0
+                assert (store == 3.0).all()
