@@ -703,7 +703,10 @@ product_fp8_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constan
         continue;
       }
       T* out = static_cast<T*>(g.out) + z * g.plane;
-      if (MODE == PRODUCT_DW) {               // added to 16-bit gradients: one rounding
+      // Added to 16-bit gradients: one rounding.  A load waits for the store before it, which
+      // may be to the same address for all that is known here: 131072 rows, 128 x 1536 x 4096,
+      // bf16 5340 us against 975 overwritten (fp32, as boxes, 1443 against 1243).
+      if (MODE == PRODUCT_DW) {
 #pragma unroll
         for (int j = 0; j < CW; ++j) {
           const int row = p.row - lane + 16 * (j >> 4 & 1) + lane / 4 + 8 * (j >> 1 & 1);

@@ -64,8 +64,8 @@ __device__ __forceinline__ uint32_t codes4(float a, float b, float c, float d) {
 __device__ __noinline__ float divided(float x, float s) { return s == 0.f ? x * 0.f : x / s; }
 
 // Four codes of v with a scale each.  PAIRS: quotients two at a time, where both forms are made
-// and instructions are what is short: bf16 131072 x 4096 403 us against 422.  With one form, bound by
-// memory, the pairs' registers cost more than that: by row 264 against 241, by column 281 against 269.
+// and instructions are what is short: bf16 131072 x 4096 403 us against 421.  With one form, bound by
+// memory, the pairs' registers cost more than that: by row 263 against 240, by column 276 against 269.
 // The pairs' negated quotients have their signs put right in the codes, four at a time; negated
 // one by one before they are converted the two forms take 421 us.
 template <bool PAIRS>
@@ -133,8 +133,8 @@ __device__ __forceinline__ void ldg_nc_32(const void* p, uint32_t* v) {
 }
 
 // VEC: 16 elements of x are aligned vectors of so many bytes, 32 or 16; 0: they are read one by
-// one.  Vectors of 32 bytes read whole sectors: bf16 131072 x 4096 in both forms 421 us against 428,
-// fp32 65536 x 4096 298 against 329.
+// one.  Vectors of 32 bytes read whole sectors: bf16 131072 x 4096 in both forms 403 us against 416,
+// fp32 65536 x 4096 294 against 321.
 template <typename T, int FORM, int VEC>
 __global__ void __launch_bounds__(QT, sizeof(T) == 2 ? 4 : (FORM == ROWS ? 3 : 2))
 quantize_fp8_kernel(const T* __restrict__ x, long long ldx, long long n, int K, long long plane,

@@ -695,6 +695,9 @@ typedef struct {
  * takes them).  NaN comes before all other keys and logits.  A sigmoid of NaN is NaN; a softmax
  * over a logit of NaN or +inf is NaN for all its experts: where the choice goes by keys the lowest
  * come first, and every filled slot has weight NaN.  bias takes no part in the weights.
+ * A logit of -inf costs nothing.  A bias that is not finite, or finite keys (large negative
+ * logits as a mask, without a bias; a large negative bias) far below all others, have every
+ * token's choice made in 64 bits, in about thirty times the time: close experts by their logits.
  * logits: [T,E] of bf16, fp16 or fp32, rows ld_logits elements apart; bias fp32 [E];
  * topk_idx int32 [T,R]; topk_w fp32 [T,R].  R <= 32, E <= 1024, R at most the experts of
  * top_groups groups; group_keys 2 needs groups of two.  No workspace.
@@ -744,12 +747,16 @@ moe_status_t moe_quantize_fp8_tiles(const void* w, int dtype, int E, int n, int 
  * moe_product_fp8 -- each expert's product on its rows, on the fp8 tensor cores:
  *   out[i] = x_i w[e]^T   for the rows i in [offsets[e], offsets[e+1])
  * with x and w the values of their codes and scales; the codes' products of a block of 128
- * are summed in fp32, those sums times both scales in fp32, one rounding at the end.
+ * are summed in fp32, those sums times the product of both scales, in fp32, one rounding at the
+ * end.  (A product of two scales above the fp32 range is infinite and makes infinities and NaN;
+ * one below the normal range keeps fewer bits.)
  * xq, xs: rows [N,K] in the row form; wq, wscale: [E,n,K] in tiles; out: [N,n] of bf16, fp16
  * or fp32, rows ld_out elements apart.  offsets: int32 [E+1] on the device, not falling, in
  * [0, N]; NULL with E == 1: all N rows (a plain matrix product).  Rows of xq outside every
  * segment have no effect, those of out are left as they are.  Offsets that are not valid are
- * reported (MOE_ERR_BAD_ROUTING with MOE_CHECK) and nothing is computed.
+ * reported (MOE_ERR_BAD_ROUTING with MOE_CHECK) and nothing is computed; with N = 0 they are not
+ * read.  Without MOE_CHECK a wait inside the kernel that gives up (MOE_ERR_TIMEOUT) is not
+ * reported either, and the output is then incomplete.
  * n and K are multiples of 16, N <= 2^30, E <= 1024; codes 16-byte aligned.  The workspace
  * (error word; sums of few tiles split over several CTAs) has one size for the three products
  * of one N, n, K, E; calls that may overlap need one each.  Bitwise reproducible.
@@ -776,7 +783,8 @@ moe_status_t moe_product_fp8_dx(const uint8_t* dyq, const float* dys, const int3
  * belong to one expert: offsets are multiples of 128 (moe_sort with align 128), a segment
  * that ends at N may end anywhere.  dw: [E,n,K] of bf16, fp16 or fp32, dense, 16-byte
  * aligned; with MOE_ACCUMULATE the sum is added to it (fp32: a value below the normal range
- * counts as zero).  xs and dys 16-byte aligned.
+ * counts as zero; 16-bit types: rounded once, in several times the time of overwriting it).
+ * Offsets are checked with N = 0 too.  xs and dys 16-byte aligned.
  */
 moe_status_t moe_product_fp8_dw(const uint8_t* dyq, const float* dys, const uint8_t* xq,
                                 const float* xs, const int32_t* offsets, int N, int n, int K,
