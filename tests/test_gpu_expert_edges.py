@@ -216,3 +216,56 @@ def test_gradient_between_other_columns(lib, dtype):
                 assert (np.abs(store[:, cut].double().cpu().numpy() - ref) <= bound).all()
                 store[:, cut] = 3.0
                 assert (store == 3.0).all()
+
+
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+def test_a_bias_of_nan_or_infinity_comes_first(lib, score):
+    """The bias orders experts and takes no part in the weights."""
+    x = torch.randn(40, 64, device="cuda", generator=torch.Generator(device="cuda").manual_seed(2))
+    want = torch.softmax(x.double(), 1) if score == "softmax" else torch.sigmoid(x.double())
+    for bad in (float("nan"), float("inf")):
+        bias = torch.zeros(64, device="cuda")
+        bias[37] = bad
+        for kw in ({}, dict(groups=4, top_groups=2), dict(groups=4, top_groups=1, group_keys=2)):
+            idx, w = routes.forward(lib, x, bias, 6, score=score, renormalise=False, **kw)
+            assert (idx[:, 0] == 37).all(), (bad, kw)
+            got = want.gather(1, idx.long())
+            # logits within 8 of each other, expf and a sum of 64: see test_gpu_route_scores
+            assert ((w.double() - got).abs() <= routes.UNIT * (8 + 64 + 16) * got).all(), (bad, kw)
+
+
+def test_split_products_follow_each_other_in_a_graph(lib):
+    """Few tiles and a long contraction: parts of sums in the workspace and a second kernel.  One
+    workspace for calls one after another, captured and replayed with other values."""
+    g = torch.Generator(device="cuda").manual_seed(14)
+    N, n, K = 3, 256, 4096
+    x, sx = products.made((N, K), "row", g)
+    w, sw = products.made((n, K), "tile", g)
+    w2, sw2 = products.made((K, n), "tile", g)
+    ws = lib.workspace(max(lib.product_fp8_ws_bytes(N, n, K), lib.product_fp8_ws_bytes(N, K, n)))
+    assert ws.numel() > 256                       # split over several blocks
+    a, b, c = (torch.empty(N, n, device="cuda") for _ in range(3))
+
+    def step():
+        lib.moe_product_fp8(x, sx, w, sw, a, ws)
+        lib.moe_product_fp8_dx(x, sx, w2, sw2, b, ws)
+        lib.moe_product_fp8(x, sx, w, sw, c, ws)
+
+    step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    for seed in (1, 2):
+        g.manual_seed(seed)
+        x.copy_(products.made((N, K), "row", g)[0])
+        sx.copy_(torch.rand(sx.shape, device="cuda", generator=g) + 0.25)
+        for t in (a, b, c):
+            t.fill_(float("nan"))
+        graph.replay()
+        torch.cuda.synchronize()
+        xv, wv, w2v = (products.value(*p) for p in ((x, sx, "row"), (w, sw, "tile"),
+                                                    (w2, sw2, "tile")))
+        products.within(a, xv @ wv.t(), xv.abs() @ wv.abs().t(), K, torch.float32, "a")
+        products.within(b, xv @ w2v, xv.abs() @ w2v.abs(), K, torch.float32, "b")
+        assert torch.equal(a, c)
